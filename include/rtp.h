@@ -188,6 +188,95 @@ RTP_API rtp_status rtp_kv_append(const rtp_tensor* k_new, const rtp_tensor* v_ne
                                  const rtp_tensor* k_idx, const rtp_tensor* k_ring, const rtp_tensor* v_ring,
                                  int32_t* lens_out, int32_t* ring_lens, rtp_stream_t stream);
 
+/* ---- taking accepted drafts into the caches ----------------------------------
+ * rtp_kv_append of some of the T rows of k_new / v_new (the drafted tokens of a
+ * speculative step): step i < count[b] of sequence b appends row path[b][i] at
+ * position pos[b] + i, with the projected key, the ring slot and the lengths as
+ * rtp_kv_append would write them for those rows (so T in its text is count[b]).
+ *   path    int32[B, A] device: accepted rows in order, each in [0, T); a step
+ *           whose row is outside [0, T) writes nothing (its position keeps what
+ *           it held)
+ *   A       columns of path, >= 0
+ *   count   int32[B] device, clamped to [0, A]; 0 leaves the caches as they are
+ *           and still writes the lengths
+ * Errors as rtp_kv_append, plus INVALID_ARG for a NULL path or count, A < 0, or
+ * a length output that is path or count.  One launch.
+ */
+RTP_API rtp_status rtp_kv_accept(const rtp_tensor* k_new, const rtp_tensor* v_new, const int32_t* pos,
+                                 const int32_t* path, int32_t A, const int32_t* count, int32_t R,
+                                 const rtp_tensor* P, const rtp_tensor* k_cache, const rtp_tensor* v_cache,
+                                 const rtp_tensor* k_idx, const rtp_tensor* k_ring, const rtp_tensor* v_ring,
+                                 int32_t* lens_out, int32_t* ring_lens, rtp_stream_t stream);
+
+/* ---- per-head norm of queries and keys with the position rotation -------------
+ * Makes the post-rotary rows that the other calls take, from raw projections:
+ *   y = x * w / sqrt(mean(x^2) + eps)     per row (head of a token); no norm for
+ *                                         a tensor whose weight is NULL
+ *   pair i of y turned by angle position * inv_freq[i], i = 0 .. 63:
+ *     (y_a cos - y_b sin, y_b cos + y_a sin)
+ *   q, k        [B, Hq, T, 128], [B, Hk, T, 128] f32 or bf16 (one type); k and
+ *               k_out may both be NULL (queries only).  Any strides: heads side
+ *               by side in one projection's output are a view
+ *   q_weight, k_weight  [1, 128] or [H, 128] f32 or bf16, or NULL
+ *   eps         >= 0, finite
+ *   pos         int32[B] device; token t of sequence b sits at pos[b] + t, or at
+ *   offs        int32[B, T] device or NULL: pos[b] + offs[b][t] (depths in a tree)
+ *   inv_freq    double[64] device: radians per position (0 leaves a pair as it is)
+ *   pairing     RTP_ROPE_HALF: pair i is (i, i + 64); RTP_ROPE_ADJACENT: (2i, 2i + 1)
+ *   q_out, k_out  same shapes, f32 or bf16 (one type); may be q and k themselves
+ *               (same type and strides), must not overlap them otherwise
+ * fp32 arithmetic (angles as fp64 fractions of a turn), one rounding at the end.
+ * At most 65535 heads in all.  The pages take post-rotary rows as given; this
+ * call is library-level.
+ */
+#define RTP_ROPE_HALF      0
+#define RTP_ROPE_ADJACENT  1
+RTP_API rtp_status rtp_qk_norm_rope(const rtp_tensor* q, const rtp_tensor* k, const rtp_tensor* q_weight,
+                                    const rtp_tensor* k_weight, float eps, const int32_t* pos,
+                                    const int32_t* offs, const double* inv_freq, int32_t pairing,
+                                    const rtp_tensor* q_out, const rtp_tensor* k_out, rtp_stream_t stream);
+
+/* ---- attention of a tree of drafted tokens over a cache -----------------------
+ * Verification of a speculative step: T drafted tokens per sequence, not yet in
+ * the cache, attend the committed keys and their own ancestors in one pass.
+ *   q      [B, Hq, T, 128] bf16; k, v [B, Hk, N, 128] bf16 committed rows
+ *   lens   int32[B] device or NULL (N): committed tokens of each sequence
+ *          (negative counts as 0); without `ring` clamped to N
+ *   k_new, v_new  [B, Hk, T, 128] bf16 rows of the drafted tokens
+ *   tree   mask uint32[B, T, mask_words]: bit j % 32 of word j / 32 of row t is
+ *          set iff token t attends drafted token j (its ancestors and itself;
+ *          bits at or past T are ignored); mask_words >= ceil(T / 32).
+ *          depth int32[B, T]: token t sits at position lens[b] + depth[b][t]
+ *          (negative counts as 0); read only when W > 0, else may be NULL
+ *   W      0: every committed key.  >= 1: a window, keys at positions at or below
+ *          lens[b] + depth - W are not attended (drafted keys too)
+ *   ring   0: row j of k, v holds position j.  1: a ring, row j holds the last
+ *          position p < lens[b] with p mod N == j (what rtp_kv_append keeps);
+ *          needs 1 <= W <= N
+ *   sel    NULL, or a selection over committed keys with one row per (b, h, t),
+ *          r = (b * Hq + h) * T + t: only keys whose mask bit is set are
+ *          attended (mask_words >= ceil(N / 32); drafted keys are not selected
+ *          from).  Not with `ring`
+ *   scale  softmax scale;  o [B, Hq, T, 128] f32 or bf16
+ * o = sum softmax(scale * q.k) v over the attended keys, 0 when there are none.
+ * Scores, softmax statistics and sums are fp32 (P goes to the tensor cores as a
+ * bf16 hi + lo pair).  Rows that a query does not attend do not reach its result,
+ * even when they hold infinities or NaN.  Hq / Hk <= 8.  A selection for the T
+ * queries is rtp_topp_select over the committed keys with the [B, Hq, T, 16]
+ * queries viewed as [B, Hq * T, 1, 16].  Workspace: rtp_tree_attn_workspace_size().
+ */
+typedef struct rtp_tree {
+  const uint32_t* mask;
+  int64_t         mask_words;
+  const int32_t*  depth;
+} rtp_tree;
+RTP_API rtp_status rtp_tree_attn(const rtp_tensor* q, const rtp_tensor* k, const rtp_tensor* v,
+                                 const int32_t* lens, const rtp_tensor* k_new, const rtp_tensor* v_new,
+                                 const rtp_tree* tree, int32_t W, int32_t ring, const rtp_selection* sel,
+                                 float scale, const rtp_tensor* o, void* workspace, size_t workspace_bytes,
+                                 rtp_stream_t stream);
+RTP_API size_t rtp_tree_attn_workspace_size(int64_t B, int64_t Hq, int64_t T, int64_t Hk, int64_t N);
+
 /* ---- a4 (decode): exact attention over each query's selected keys -------
  *   q      [B, Hq, 1, 128]  bf16 or f32 (retrieval query heads)
  *   k, v   [B, Hk, N, 128]  same dtype (full KV cache of the retrieval heads)

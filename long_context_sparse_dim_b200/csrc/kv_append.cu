@@ -17,6 +17,10 @@
 // attention of the newest token is the ordinary window attention over the
 // min(n, W) stored ring rows; the kernel writes that length per sequence, and
 // the sequence length after the append (the next append's position).
+//
+// rtp_kv_accept is the same pass over some of the T rows: step i of sequence b
+// takes row path[b][i] (the accepted tokens of a drafted tree, root first), for
+// the first count[b] steps.
 #include "common.cuh"
 #include "launch.h"
 #include "project.cuh"
@@ -55,9 +59,11 @@ struct Row4 {
 
 constexpr int kAppSmemHeads = 8;  // P of up to this many retrieval heads is staged in shared memory
 
-template <typename T>
+// kPath: step t of sequence b takes row path[b][t] of the new rows, for t < count[b]; else row t, t < T.
+template <typename T, bool kPath>
 __global__ void __launch_bounds__(kAppThreads, 3)
 kv_append_kernel(KvAppendArgs A) {
+  const int steps = kPath ? A.A : A.T;
   // P [R, 16, 128] f32 in shared memory (32 KB per 4 heads), read there by every projection
   extern __shared__ float4 p_smem[];
   const bool p_in_smem = A.R <= kAppSmemHeads;
@@ -69,7 +75,7 @@ kv_append_kernel(KvAppendArgs A) {
   const int lane = threadIdx.x & 31;
   const int64_t warp0 = ((int64_t)blockIdx.x * kAppThreads + threadIdx.x) >> 5;
   const int64_t nwarps = ((int64_t)gridDim.x * kAppThreads) >> 5;
-  const int64_t rows = (int64_t)A.B * A.H * A.T;
+  const int64_t rows = (int64_t)A.B * A.H * steps;
   for (int64_t r0 = warp0; r0 < rows; r0 += kAppUnroll * nwarps) {
     // up to kAppUnroll rows of this warp: every load first, then the writes
     Row4<T> kx[kAppUnroll], vx[kAppUnroll];
@@ -82,9 +88,16 @@ kv_append_kernel(KvAppendArgs A) {
       const int64_t r = r0 + u * nwarps;
       kdst[u] = nullptr;
       if (r >= rows) continue;
-      const int t = (int)(r % A.T);
-      const int64_t bh = r / A.T;
+      const int t = (int)(r % steps);
+      const int64_t bh = r / steps;
       const int h = (int)(bh % A.H), b = (int)(bh / A.H);
+      int n_new = steps, src = t;  // rows this sequence appends; the row of this step
+      if (kPath) {
+        n_new = min(max(A.count[b], 0), steps);
+        if (t >= n_new) continue;
+        src = A.path[(int64_t)b * steps + t];
+        if (src < 0 || src >= A.T) continue;  // no such row: nothing written
+      }
       const int p = A.pos[b] + t;  // position of this token in its sequence
       hrow[u] = h;
       idst[u] = nullptr;
@@ -95,15 +108,15 @@ kv_append_kernel(KvAppendArgs A) {
         idst[u] = static_cast<T*>(A.k_idx.data) + b * A.k_idx.sb + h * A.k_idx.sh + (int64_t)p * A.k_idx.sn;
       } else {
         // only the last W tokens of the append are kept (two tokens W apart share a slot)
-        if (p < 0 || t < A.T - A.W) continue;
+        if (p < 0 || t < n_new - A.W) continue;
         const int l = h - A.R;
         const int slot = p % A.W;
         kdst[u] = static_cast<T*>(A.k_ring.data) + b * A.k_ring.sb + l * A.k_ring.sh + (int64_t)slot * A.k_ring.sn;
         vdst[u] = static_cast<T*>(A.v_ring.data) + b * A.v_ring.sb + l * A.v_ring.sh + (int64_t)slot * A.v_ring.sn;
       }
-      kx[u].load(static_cast<const T*>(A.k_new.data) + b * A.k_new.sb + h * A.k_new.sh + (int64_t)t * A.k_new.sn,
+      kx[u].load(static_cast<const T*>(A.k_new.data) + b * A.k_new.sb + h * A.k_new.sh + (int64_t)src * A.k_new.sn,
                  lane);
-      vx[u].load(static_cast<const T*>(A.v_new.data) + b * A.v_new.sb + h * A.v_new.sh + (int64_t)t * A.v_new.sn,
+      vx[u].load(static_cast<const T*>(A.v_new.data) + b * A.v_new.sb + h * A.v_new.sh + (int64_t)src * A.v_new.sn,
                  lane);
     }
 #pragma unroll
@@ -122,30 +135,35 @@ kv_append_kernel(KvAppendArgs A) {
   }
   if (blockIdx.x == 0) {
     for (int b = threadIdx.x; b < A.B; b += kAppThreads) {
-      const int end = A.pos[b] + A.T;  // one past the last appended position
+      // one past the last appended position
+      const int end = A.pos[b] + (kPath ? min(max(A.count[b], 0), steps) : steps);
       if (A.lens_out) A.lens_out[b] = A.R > 0 ? max(min(end, A.N), 0) : max(end, 0);
       if (A.ring_lens) A.ring_lens[b] = max(min(end, A.W), 0);
     }
   }
 }
 
+template <typename T, bool kPath>
+cudaError_t launch(const KvAppendArgs& a, unsigned blocks, size_t smem, cudaStream_t stream) {
+  cudaFuncSetAttribute(kv_append_kernel<T, kPath>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  kv_append_kernel<T, kPath><<<blocks, kAppThreads, smem, stream>>>(a);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_kv_append(const KvAppendArgs& a, bool bf16, cudaStream_t stream) {
-  const int64_t rows = (int64_t)a.B * a.H * a.T;
+  const int64_t rows = (int64_t)a.B * a.H * (a.path ? a.A : a.T);
   if (a.B == 0 || (rows == 0 && !a.lens_out && !a.ring_lens)) return cudaSuccess;
   int64_t blocks = (rows + kAppUnroll * (kAppThreads / 32) - 1) / (kAppUnroll * (kAppThreads / 32));
   if (blocks < 1) blocks = 1;  // an empty append still writes the lengths
   if (blocks > 148 * 16) blocks = 148 * 16;
   const size_t smem = a.R <= kAppSmemHeads ? (size_t)a.R * kIdxDim * kHeadDim * sizeof(float) : 0;
-  if (bf16) {
-    cudaFuncSetAttribute(kv_append_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    kv_append_kernel<__nv_bfloat16><<<(unsigned)blocks, kAppThreads, smem, stream>>>(a);
-  } else {
-    cudaFuncSetAttribute(kv_append_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    kv_append_kernel<float><<<(unsigned)blocks, kAppThreads, smem, stream>>>(a);
-  }
-  return cudaGetLastError();
+  if (a.path)
+    return bf16 ? launch<__nv_bfloat16, true>(a, (unsigned)blocks, smem, stream)
+                : launch<float, true>(a, (unsigned)blocks, smem, stream);
+  return bf16 ? launch<__nv_bfloat16, false>(a, (unsigned)blocks, smem, stream)
+              : launch<float, false>(a, (unsigned)blocks, smem, stream);
 }
 
 }  // namespace rtp

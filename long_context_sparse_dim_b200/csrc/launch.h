@@ -177,8 +177,50 @@ struct KvAppendArgs {
   int32_t* lens_out;         // [B] or null: pos + T (clamped to [0, N] when R > 0)
   int32_t* ring_lens;        // [B] or null: min(pos + T, W)
   int B, H, T, R, N, W;
+  const int32_t* path = nullptr;   // rtp_kv_accept: [B, A] rows of the new tensors, in order
+  const int32_t* count = nullptr;  // and [B] how many of them count
+  int A = 0;
 };
 cudaError_t launch_kv_append(const KvAppendArgs& a, bool bf16, cudaStream_t stream);
+
+// Per-head norm and position rotation (rtp_qk_norm_rope).
+struct NormRopeArgs {
+  View4 q, k;                // [B, Hq, T, 128], [B, Hk, T, 128]
+  MutView4 q_out, k_out;
+  const void* qw;            // norm weights, one row of 128 per head (row stride 0: one for all), or null: no norm
+  const void* kw;
+  int64_t qw_stride, kw_stride;
+  bool qw_bf16, kw_bf16;
+  float eps;
+  const int32_t* pos;        // [B]
+  const int32_t* offs;       // [B, T] or null: token t sits at pos[b] + offs[b][t], or pos[b] + t
+  const double* inv_freq;    // [64]
+  int B, Hq, Hk, T;
+  int heads_per_group;       // set by the launcher
+};
+cudaError_t launch_qk_norm_rope(NormRopeArgs a, bool in_bf16, bool out_bf16, bool half, cudaStream_t stream);
+
+// Attention of drafted tokens over the committed cache and their tree (rtp_tree_attn), bf16.
+struct TreeAttnArgs {
+  View4 q;                   // [B, Hq, T, 128]
+  View4 k, v;                // [B, Hk, N, 128] committed rows: by position, or a ring (position p in row p mod N)
+  View4 kn, vn;              // [B, Hk, T, 128] drafted rows
+  const int32_t* lens;       // [B] committed tokens, or null: N
+  const uint32_t* tree;      // [B, T, tree_words] bits: token t attends drafted token j
+  int64_t tree_words;
+  const int32_t* depth;      // [B, T] or null (W == 0)
+  const uint32_t* sel;       // [B * Hq * T, sel_words] bits over committed rows, or null
+  int64_t sel_words;
+  int B, Hq, Hk, G, T, N, W, ring;
+  float scale_log2;          // scale * log2 e
+  MutView4 o;                // [B, Hq, T, 128]
+  int o_bf16;
+  void* ws;
+  int* err;
+  long long budget;
+};
+size_t tree_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t T, int64_t Hk, int64_t N);
+cudaError_t launch_tree_attn(const TreeAttnArgs& a, cudaStream_t stream);
 
 // Records a CUDA error for rtp_last_cuda_error() on this thread.
 void set_last_cuda_error(int32_t e);

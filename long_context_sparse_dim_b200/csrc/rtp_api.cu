@@ -242,10 +242,11 @@ rtp_status rtp_topk_select(const rtp_tensor* q_idx, const rtp_tensor* k_idx, con
 }
 
 // ---- cache maintenance ---------------------------------------------------------------
-rtp_status rtp_kv_append(const rtp_tensor* k_new, const rtp_tensor* v_new, const int32_t* pos, int32_t R,
-                         const rtp_tensor* P, const rtp_tensor* k_cache, const rtp_tensor* v_cache,
-                         const rtp_tensor* k_idx, const rtp_tensor* k_ring, const rtp_tensor* v_ring,
-                         int32_t* lens_out, int32_t* ring_lens, rtp_stream_t stream) {
+// Every check of rtp_kv_append and the launch arguments both calls share.
+static rtp_status check_kv_append(const rtp_tensor* k_new, const rtp_tensor* v_new, const int32_t* pos, int32_t R,
+                                  const rtp_tensor* P, const rtp_tensor* k_cache, const rtp_tensor* v_cache,
+                                  const rtp_tensor* k_idx, const rtp_tensor* k_ring, const rtp_tensor* v_ring,
+                                  int32_t* lens_out, int32_t* ring_lens, rtp::KvAppendArgs* out) {
   rtp_status s;
   if ((s = check_kv(k_new, v_new)) != RTP_OK) return s;
   if (!pos) return RTP_ERR_INVALID_ARG;
@@ -276,7 +277,7 @@ rtp_status rtp_kv_append(const rtp_tensor* k_new, const rtp_tensor* v_new, const
     if (k_ring->shape[2] > INT32_MAX) return RTP_ERR_SHAPE;
     W = k_ring->shape[2];
   }
-  rtp::KvAppendArgs a;
+  rtp::KvAppendArgs& a = *out;
   a.k_new = view(k_new);
   a.v_new = view(v_new);
   a.pos = pos;
@@ -294,7 +295,107 @@ rtp_status rtp_kv_append(const rtp_tensor* k_new, const rtp_tensor* v_new, const
   a.R = R;
   a.N = (int)N;
   a.W = (int)W;
+  return RTP_OK;
+}
+
+rtp_status rtp_kv_append(const rtp_tensor* k_new, const rtp_tensor* v_new, const int32_t* pos, int32_t R,
+                         const rtp_tensor* P, const rtp_tensor* k_cache, const rtp_tensor* v_cache,
+                         const rtp_tensor* k_idx, const rtp_tensor* k_ring, const rtp_tensor* v_ring,
+                         int32_t* lens_out, int32_t* ring_lens, rtp_stream_t stream) {
+  rtp_status s;
+  rtp::KvAppendArgs a;
+  if ((s = check_kv_append(k_new, v_new, pos, R, P, k_cache, v_cache, k_idx, k_ring, v_ring, lens_out, ring_lens,
+                           &a)) != RTP_OK)
+    return s;
   return cuda_status(rtp::launch_kv_append(a, k_new->dtype == RTP_BF16, (cudaStream_t)stream));
+}
+
+rtp_status rtp_kv_accept(const rtp_tensor* k_new, const rtp_tensor* v_new, const int32_t* pos, const int32_t* path,
+                         int32_t A, const int32_t* count, int32_t R, const rtp_tensor* P, const rtp_tensor* k_cache,
+                         const rtp_tensor* v_cache, const rtp_tensor* k_idx, const rtp_tensor* k_ring,
+                         const rtp_tensor* v_ring, int32_t* lens_out, int32_t* ring_lens, rtp_stream_t stream) {
+  rtp_status s;
+  rtp::KvAppendArgs a;
+  if ((s = check_kv_append(k_new, v_new, pos, R, P, k_cache, v_cache, k_idx, k_ring, v_ring, lens_out, ring_lens,
+                           &a)) != RTP_OK)
+    return s;
+  if (!path || !count || A < 0) return RTP_ERR_INVALID_ARG;
+  const void* written[2] = {lens_out, ring_lens};
+  for (const void* w : written)
+    if (w && (w == path || w == count)) return RTP_ERR_INVALID_ARG;
+  a.path = path;
+  a.count = count;
+  a.A = A;
+  return cuda_status(rtp::launch_kv_append(a, k_new->dtype == RTP_BF16, (cudaStream_t)stream));
+}
+
+// ---- per-head norm and rotation --------------------------------------------------------
+// A norm weight: [1 or H, 128] rows, f32 or bf16, or NULL (no norm).
+static rtp_status check_norm_weight(const rtp_tensor* w, int64_t H, const void** data, int64_t* stride, bool* bf16) {
+  *data = nullptr;
+  *stride = 0;
+  *bf16 = false;
+  if (!w) return RTP_OK;
+  if (!w->data) return RTP_ERR_INVALID_ARG;
+  if (!dtype_ok(w->dtype)) return RTP_ERR_DTYPE;
+  if (w->ndim != 2 || w->shape[1] != 128 || (w->shape[0] != 1 && w->shape[0] != H)) return RTP_ERR_SHAPE;
+  if (w->stride[1] != 1 || ((uintptr_t)w->data) % 16) return RTP_ERR_ALIGNMENT;
+  if (w->shape[0] > 1) {
+    if (w->stride[0] < 0 || (w->stride[0] * elt_size(w->dtype)) % 16) return RTP_ERR_ALIGNMENT;
+    *stride = w->stride[0];
+  }
+  *data = w->data;
+  *bf16 = w->dtype == RTP_BF16;
+  return RTP_OK;
+}
+
+rtp_status rtp_qk_norm_rope(const rtp_tensor* q, const rtp_tensor* k, const rtp_tensor* q_weight,
+                            const rtp_tensor* k_weight, float eps, const int32_t* pos, const int32_t* offs,
+                            const double* inv_freq, int32_t pairing, const rtp_tensor* q_out,
+                            const rtp_tensor* k_out, rtp_stream_t stream) {
+  rtp_status s;
+  if ((s = check4(q, 128)) != RTP_OK) return s;
+  if ((s = check4(q_out, 128)) != RTP_OK) return s;
+  if (!same_bhn(q, q_out)) return RTP_ERR_SHAPE;
+  if (!k != !k_out) return RTP_ERR_INVALID_ARG;
+  if (!k && k_weight) return RTP_ERR_INVALID_ARG;
+  if (k) {
+    if ((s = check4(k, 128)) != RTP_OK) return s;
+    if ((s = check4(k_out, 128)) != RTP_OK) return s;
+    if (!same_bhn(k, k_out) || k->shape[0] != q->shape[0] || k->shape[2] != q->shape[2]) return RTP_ERR_SHAPE;
+    if (k->dtype != q->dtype || k_out->dtype != q_out->dtype) return RTP_ERR_DTYPE;
+  }
+  // in place means exactly in place: the same rows and type (a partial overlap cannot be seen here)
+  const rtp_tensor* pair[2][2] = {{q, q_out}, {k, k_out}};
+  for (auto& p : pair) {
+    if (!p[0] || !p[0]->data || p[0]->data != p[1]->data) continue;
+    if (p[0]->dtype != p[1]->dtype) return RTP_ERR_INVALID_ARG;
+    for (int i = 0; i < 3; ++i)
+      if (p[0]->shape[i] > 1 && p[0]->stride[i] != p[1]->stride[i]) return RTP_ERR_INVALID_ARG;
+  }
+  if (!pos || !inv_freq || !(eps >= 0.f) || !isfinite(eps)) return RTP_ERR_INVALID_ARG;
+  if (pairing != RTP_ROPE_HALF && pairing != RTP_ROPE_ADJACENT) return RTP_ERR_INVALID_ARG;
+  if (((uintptr_t)inv_freq) % 8) return RTP_ERR_ALIGNMENT;
+  rtp::NormRopeArgs a;
+  if ((s = check_norm_weight(q_weight, q->shape[1], &a.qw, &a.qw_stride, &a.qw_bf16)) != RTP_OK) return s;
+  if ((s = check_norm_weight(k_weight, k ? k->shape[1] : 0, &a.kw, &a.kw_stride, &a.kw_bf16)) != RTP_OK) return s;
+  const int64_t Hk = k ? k->shape[1] : 0;
+  if (q->shape[1] + Hk > 65535) return RTP_ERR_UNSUPPORTED;
+  a.q = view(q);
+  a.k = k ? view(k) : rtp::View4{nullptr, 0, 0, 0};
+  a.q_out = mview(q_out);
+  a.k_out = k ? mview(k_out) : rtp::MutView4{nullptr, 0, 0, 0};
+  a.eps = eps;
+  a.pos = pos;
+  a.offs = offs;
+  a.inv_freq = inv_freq;
+  a.B = (int)q->shape[0];
+  a.Hq = (int)q->shape[1];
+  a.Hk = (int)Hk;
+  a.T = (int)q->shape[2];
+  a.heads_per_group = 0;
+  return cuda_status(rtp::launch_qk_norm_rope(a, q->dtype == RTP_BF16, q_out->dtype == RTP_BF16,
+                                              pairing == RTP_ROPE_HALF, (cudaStream_t)stream));
 }
 
 // ---- a4 decode -------------------------------------------------------------------
@@ -518,6 +619,63 @@ rtp_status rtp_window_attn(const rtp_tensor* q, const rtp_tensor* k, const rtp_t
   a.o_bf16 = o->dtype == RTP_BF16;
   a.ws = workspace;
   return cuda_status(rtp::launch_attn_decode(a, (cudaStream_t)stream));
+}
+
+// ---- attention of a drafted tree ---------------------------------------------------------
+size_t rtp_tree_attn_workspace_size(int64_t B, int64_t Hq, int64_t T, int64_t Hk, int64_t N) {
+  if (B <= 0 || Hq <= 0 || T <= 0 || Hk <= 0 || N < 0 || Hq % Hk) return 0;
+  return rtp::tree_attn_workspace_bytes(B, Hq, T, Hk, N);
+}
+
+rtp_status rtp_tree_attn(const rtp_tensor* q, const rtp_tensor* k, const rtp_tensor* v, const int32_t* lens,
+                         const rtp_tensor* k_new, const rtp_tensor* v_new, const rtp_tree* tree, int32_t W,
+                         int32_t ring, const rtp_selection* sel, float scale, const rtp_tensor* o, void* workspace,
+                         size_t workspace_bytes, rtp_stream_t stream) {
+  rtp_status s;
+  if ((s = check_decode_common(q, k, v, o, scale)) != RTP_OK) return s;
+  if ((s = check_kv(k_new, v_new)) != RTP_OK) return s;
+  if (q->dtype != RTP_BF16 || k_new->dtype != RTP_BF16) return RTP_ERR_DTYPE;  // tensor-core tiles
+  const int64_t B = q->shape[0], Hq = q->shape[1], T = q->shape[2], Hk = k->shape[1], N = k->shape[2];
+  if (k_new->shape[0] != B || k_new->shape[1] != Hk || k_new->shape[2] != T) return RTP_ERR_SHAPE;
+  if (!tree || !tree->mask) return RTP_ERR_INVALID_ARG;
+  if (tree->mask_words < (T + 31) / 32) return RTP_ERR_SHAPE;
+  if (W < 0 || (W > 0 && !tree->depth)) return RTP_ERR_INVALID_ARG;
+  if (ring != 0 && ring != 1) return RTP_ERR_INVALID_ARG;
+  // a ring holds the last N tokens: the window must lie inside it, and selections name positions, not its rows
+  if (ring && (W < 1 || W > N || sel)) return RTP_ERR_INVALID_ARG;
+  if (sel && !sel->mask) return RTP_ERR_INVALID_ARG;
+  if (sel && sel->mask_words < (N + 31) / 32) return RTP_ERR_SHAPE;
+  if (B * Hk > INT32_MAX / 8 || Hq * T > INT32_MAX / 8) return RTP_ERR_UNSUPPORTED;
+  const size_t need = rtp_tree_attn_workspace_size(B, Hq, T, Hk, N);
+  if ((s = check_workspace(workspace, workspace_bytes, need)) != RTP_OK) return s;
+  rtp::TreeAttnArgs a;
+  a.q = view(q);
+  a.k = view(k);
+  a.v = view(v);
+  a.kn = view(k_new);
+  a.vn = view(v_new);
+  a.lens = lens;
+  a.tree = tree->mask;
+  a.tree_words = tree->mask_words;
+  a.depth = W > 0 ? tree->depth : nullptr;
+  a.sel = sel ? sel->mask : nullptr;
+  a.sel_words = sel ? sel->mask_words : 0;
+  a.B = (int)B;
+  a.Hq = (int)Hq;
+  a.Hk = (int)Hk;
+  a.G = (int)(Hq / Hk);
+  a.T = (int)T;
+  a.N = (int)N;
+  a.W = W;
+  a.ring = ring;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.o = mview(o);
+  a.o_bf16 = o->dtype == RTP_BF16;
+  a.ws = workspace;
+  a.budget = rtp::wait_budget_cycles();
+  cudaError_t e = rtp::device_error_word(&a.err);
+  if (e != cudaSuccess) return cuda_status(e);
+  return cuda_status(rtp::launch_tree_attn(a, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -417,3 +417,96 @@ class CachedDecodeLayer:
                 call()
         self._cur = 1 - self._cur
         return self.o
+
+
+class TreeDecodeLayer(CachedDecodeLayer):
+    """Speculative decoding over the caches of CachedDecodeLayer: up to T drafted
+    tokens per sequence (a tree) are verified in one pass, then the accepted ones
+    are taken into the caches.
+
+        tree_step
+            rtp_qk_norm_rope    raw projections -> post-rotary queries and keys of the
+                                drafts, at positions lens + depth (when inv_freq is given)
+            a1  rtp_index_project   queries of the retrieval heads -> q_idx
+            a3  rtp_topp_select     top-p of every drafted query over the committed keys
+            rtp_tree_attn       retrieval heads: the selected committed keys and the
+                                draft's ancestors; local heads: the window over the ring
+                                and the ancestors
+        accept
+            rtp_kv_accept       accepted drafts -> caches, projected keys, rings, lengths
+
+    The selection ranks committed keys only: a draft always attends its ancestors.
+    The drafts' rows stay in the layer's buffers until ``accept``; nothing is
+    written to the caches before, so a rejected branch leaves no trace (a ring in
+    particular still holds the last W committed tokens).  bf16 caches.
+    """
+
+    def __init__(self, B: int, Hq: int, Hkv: int, N: int, R: int, W: int, p: float, P: torch.Tensor, T: int,
+                 q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                 eps: float = 1e-6, inv_freq: Optional[torch.Tensor] = None, pairing: str = "half",
+                 out_dtype: torch.dtype = torch.float32, scale: Optional[float] = None, device=None):
+        super().__init__(B, Hq, Hkv, N, R, W, p, P, torch.bfloat16, out_dtype, scale, device)
+        if T < 1:
+            raise ValueError("need T >= 1 drafted tokens per sequence")
+        if inv_freq is None and (q_weight is not None or k_weight is not None):
+            raise ValueError("norm weights need inv_freq: without it the drafts arrive normed and rotated")
+        dev, G, L = self.q.device, self.G, Hkv - R
+        self.T = T
+        self.q_weight, self.k_weight, self.eps = q_weight, k_weight, float(eps)
+        self.inv_freq, self.pairing = inv_freq, pairing
+        self.tree_q = torch.zeros(B, Hq, T, self.D, dtype=torch.bfloat16, device=dev)
+        self.tree_k = torch.zeros(B, Hkv, T, self.D, dtype=torch.bfloat16, device=dev)
+        self.tree_v = torch.zeros(B, Hkv, T, self.D, dtype=torch.bfloat16, device=dev)
+        self.tree_o = torch.zeros(B, Hq, T, self.D, dtype=out_dtype, device=dev)
+        self.tree_q_idx = torch.zeros(B, R * G, T, 16, dtype=torch.bfloat16, device=dev)
+        self.tree_sel = rtp.Selection.empty(B * R * G * T, N, dev)
+        self.ws_tree_sel = rtp.workspace(rtp.topp_select_workspace_size(B, R * G * T, 1, R, N), dev)
+        self.ws_tree_ret = rtp.workspace(rtp.tree_attn_workspace_size(B, R * G, T, R, N), dev) if R else None
+        self.ws_tree_loc = rtp.workspace(rtp.tree_attn_workspace_size(B, L * G, T, L, W), dev) if L else None
+
+    def tree_step(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, tree_mask: torch.Tensor,
+                  depth: torch.Tensor, stream=None, side_stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+        """Attention of the drafted tokens, o [B, Hq, T, D].  q [B, Hq, T, D] and k, v
+        [B, Hkv, T, D] are the drafts' rows: raw projections when the layer has
+        inv_freq, else normed and rotated; tree_mask int32 [B, T, words] (bit j of row
+        t: token t attends draft j) and depth int32 [B, T] describe the trees.  With
+        ``side_stream`` the local heads run there."""
+        main = torch.cuda.current_stream() if stream is None else stream
+        R, RG, L = self.R, self.R * self.G, self.Hkv - self.R
+        lens = self.lens
+        with torch.cuda.stream(main):
+            if self.inv_freq is None:
+                self.tree_q.copy_(q)
+                self.tree_k.copy_(k)
+            else:
+                rtp.qk_norm_rope(q, k, self.q_weight, self.k_weight, self.eps, lens, self.inv_freq, self.tree_q,
+                                 self.tree_k, offs=depth, pairing=self.pairing, stream=main)
+            self.tree_v.copy_(v)
+        local = main if side_stream is None else side_stream
+        if L:
+            if side_stream is not None:
+                side_stream.wait_stream(main)
+            rtp.tree_attn(self.tree_q[:, RG:], self.k_ring, self.v_ring, lens, self.tree_k[:, R:], self.tree_v[:, R:],
+                          tree_mask, self.scale, self.tree_o[:, RG:], self.ws_tree_loc, depth=depth, W=self.W,
+                          ring=True, stream=local)
+        if R:
+            rtp.index_project(self.tree_q[:, :RG], self.P, self.tree_q_idx, main)
+            rtp.topp_select(self.tree_q_idx.view(self.B, RG * self.T, 1, 16), self.k_idx, lens, self.p,
+                            self.tree_sel, self.ws_tree_sel, main)
+            rtp.tree_attn(self.tree_q[:, :RG], self.k_cache, self.v_cache, lens, self.tree_k[:, :R],
+                          self.tree_v[:, :R], tree_mask, self.scale, self.tree_o[:, :RG], self.ws_tree_ret,
+                          sel=self.tree_sel, stream=main)
+        if L and side_stream is not None:
+            main.wait_stream(side_stream)
+        return self.tree_o
+
+    def accept(self, path: torch.Tensor, count: torch.Tensor, stream=None) -> None:
+        """Take the accepted drafts of the last tree_step, rows path[b, :count[b]] in
+        order (path int32 [B, A], count int32 [B]), into the caches."""
+        R, L = self.R, self.Hkv - self.R
+        cur = self._cur
+        rtp.kv_accept(self.tree_k, self.tree_v, self._lens[cur], path, count, R, self.P if R else None,
+                      self.k_cache if R else None, self.v_cache if R else None, self.k_idx if R else None,
+                      self.k_ring if L else None, self.v_ring if L else None, self._lens[1 - cur],
+                      self.ring_lens if L else None, stream)
+        self._cur = 1 - cur
