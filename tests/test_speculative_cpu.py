@@ -149,8 +149,8 @@ def test_binding_refuses_host_tensors_and_wrong_arrays():
     with pytest.raises(ValueError, match="current CUDA device"):
         rtp.kv_accept(kv, kv, i1, torch.zeros(1, 2, dtype=torch.int32), i1, 0, k_ring=kv, v_ring=kv)
     with pytest.raises(ValueError, match="contiguous"):
-        rtp._ints(i1.long(), (1,), "pos")
+        rtp._ints(i1.long(), -1, (1,), "pos")
     with pytest.raises(ValueError, match="contiguous"):
-        rtp._ints(torch.zeros(2, 6, dtype=torch.int32)[:, ::2], (2, 3), "depth")
+        rtp._ints(torch.zeros(2, 6, dtype=torch.int32)[:, ::2], -1, (2, 3), "depth")
     with pytest.raises(ValueError, match="shape"):
-        rtp._ints(i1, (2,), "count")
+        rtp._ints(i1, -1, (2,), "count")
