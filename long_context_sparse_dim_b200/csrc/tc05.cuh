@@ -214,4 +214,47 @@ RTP_DEVICE void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
 }
 RTP_DEVICE void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
+// ---- fp32 arithmetic of the softmax ------------------------------------------
+RTP_DEVICE float ex2a(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+
+RTP_DEVICE float max3f(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// (a * s + c, b * s + c) in one packed fp32x2 fused multiply-add.
+RTP_DEVICE void fma2(float a, float b, float sc, float c, float& ra, float& rb) {
+  uint64_t x, y, z, r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(x) : "f"(a), "f"(b));
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(y) : "f"(sc), "f"(sc));
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(z) : "f"(c), "f"(c));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(ra), "=f"(rb) : "l"(r));
+}
+
+// (acc0, acc1) += (a, b) in one packed fp32x2 add.
+RTP_DEVICE void add2(float& acc0, float& acc1, float a, float b) {
+  uint64_t x, y, r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(x) : "f"(acc0), "f"(acc1));
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(y) : "f"(a), "f"(b));
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(x), "l"(y));
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(acc0), "=f"(acc1) : "l"(r));
+}
+
+// (a - c, b - d) in one packed fp32x2 subtract.
+RTP_DEVICE void sub2p(float a, float b, float c, float d, float& ra, float& rb) {
+  uint64_t x, y, r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(x) : "f"(a), "f"(b));
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(y) : "f"(c), "f"(d));
+  asm("sub.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(x), "l"(y));
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(ra), "=f"(rb) : "l"(r));
+}
+
+RTP_DEVICE void named_sync(int id, int n) { asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(n) : "memory"); }
+
 }  // namespace rtp

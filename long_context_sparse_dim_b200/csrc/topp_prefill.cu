@@ -168,12 +168,6 @@ RTP_DEVICE void mul2(float a, float b, float s, float& ra, float& rb) {
   asm("mov.b64 {%0, %1}, %2;\n" : "=f"(ra), "=f"(rb) : "l"(r));
 }
 
-RTP_DEVICE float max3f(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
 // Level-0 bin of u: floor(u) clamped to [0, 31] (31 is the tail; NaN -> 0),
 // by rounding u + 2^23 down, which leaves floor(u) in the low mantissa bits.
 RTP_DEVICE int lin0_bin(float u) {

@@ -9,112 +9,1094 @@
 //     depth_j > depth_t - W),
 // and o = sum_j softmax_j(scale * q.k_j) v_j over them (0 when there are none).
 // The committed rows lie by position, or in a ring: position p in row p mod N.
+//
+// Bound: HBM (each committed row once per KV head) up to about 128 query rows
+// per KV head (G heads x T drafts), the tensor cores above.
+//
+// Design (B200, tcgen05).  The query rows of a KV head go on the N side of both
+// products and the KEYS (then the head dims) on the M side, so that a tile
+// always fills the tensor core's 128 lanes however few drafts there are:
+//   S^T = K Q^T      [128 keys x NR rows], A = K tile, B = Q, both K-major
+//   O^T += V^T P^T   [128 dims x NR rows], A = V tile, B = P, both MN-major
+// With the rows on M, 64 rows would waste half of every instruction.
+//   softmax  a thread holds one key and 32 query rows.  Exponentials are taken
+//            against a reference per row that is not the running maximum but
+//            some earlier maximum: it is raised (to the maximum, by a reduction
+//            over the tile's keys) only when a logit exceeds it by 2^16, which
+//            one vote per tile finds out.  Any reference within that range
+//            gives the same fp32 precision, and a tile needs no reduction over
+//            keys at all.  P goes to shared memory as a bf16 hi + lo pair.
+//   O        is summed in TMEM over an epoch of up to 8 tiles (the tensor core
+//            truncates, so a long sum would drift), then added to a second TMEM
+//            tile by fp32 adds; a raised reference also ends an epoch, and the
+//            second tile is rescaled on that occasion.
+// Warps: softmax (NR / 8), 4 loaders, 1 MMA issuer.  Interior tiles come by TMA
+// (128-byte swizzle), tiles with rows to leave out (past the end, a ring's seam,
+// drafts, selected keys) by 16-byte cp.async into the same layout, with zeros in
+// the rows that hold no token.
+//
+// Work: the tiles of all (sequence, KV head) groups form one line, cut into
+// equal ranges, one CTA each; a CTA's range may begin or end inside a group, and
+// such pieces are joined by a second kernel (one warp or more per query row).
+//
+// With a selection a CTA reads the mask words of its rows, 512 keys at a time,
+// queues the keys that any row selected (a ballot per key transposes the bits:
+// the queue holds a key's row bits), and gathers only those, 128 to a tile.
+//
+// A row whose result is not finite is computed again by a scalar pass over the
+// keys it attends: 0 * inf in a product with P = 0 must not reach it.
 #include <math.h>
 
-#include "common.cuh"
 #include "launch.h"
+#include "tc05.cuh"
 
 namespace rtp {
 
 namespace {
 
-constexpr int kTrThreads = 128;
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kTrKeys = 128;                 // keys per tile
+constexpr int kTrStages = 2;                 // K/V ring
+constexpr int kTrHalf = kTrKeys * 128;       // 128 rows x 64 bf16, 128-byte swizzle
+constexpr int kTrTile = 2 * kTrHalf;         // one K or V tile: 32 KB
+constexpr int kTrLoadWarps = 4;
+constexpr int kTrEpoch = 8;                  // tiles summed in TMEM before an fp32 add
+constexpr float kTrSlack = 16.f;             // log2 units a logit may lie above the reference
+constexpr float kTrNone = -3.0e38f;          // reference of a row that has attended nothing yet
+constexpr uint32_t kTrNoKey = 0x007fffffu;   // score_key(-inf)
+constexpr int kTrRound = 512;                // keys whose selection bits are read at a time
+constexpr int kTrQueue = 1024;               // >= 128 left over + one round
+constexpr int kTrSms = 148;
+constexpr int kBarSoft = 1, kBarLoad = 2;    // named barriers
 
-// Committed tokens of sequence b, and how many cache rows hold one of them.
+// NR query rows per CTA.  64 rows leave room for two P tiles and the queue of selected keys.
+template <int NR>
+struct TrSmem {
+  static constexpr int kPBufs = NR == 64 ? 2 : 1;
+  static constexpr int kSoftWarps = NR / 8;
+  static constexpr int kThreads = (kSoftWarps + kTrLoadWarps + 4) * 32;  // (whole warpgroups: one warp issues the MMAs)
+  // registers per thread of each role; the launch's threads x registers hold them all
+  static constexpr int kSoftRegs = NR == 64 ? 168 : 96, kLoadRegs = NR == 64 ? 88 : 56, kMmaRegs = NR == 64 ? 88 : 40;
+  static constexpr int kLaunchRegs = NR == 64 ? 128 : 80;
+  static_assert(kSoftWarps * kSoftRegs + kTrLoadWarps * kLoadRegs + 4 * kMmaRegs <=
+                    (kSoftWarps + kTrLoadWarps + 4) * kLaunchRegs, "register split");
+  static constexpr int kQueue = NR == 64 ? kTrQueue : 1;
+  alignas(1024) uint8_t q[NR * 256];
+  alignas(1024) uint8_t k[kTrStages][kTrTile];
+  alignas(1024) uint8_t v[kTrStages][kTrTile];
+  alignas(1024) uint8_t p[kPBufs][2][kTrKeys * NR * 2];  // hi, lo
+  alignas(16) float nref[NR];    // minus the reference of each row (log2 units)
+  alignas(16) float alpha[NR];   // 2^(old - new reference) of the last raise; a segment's row sums at its end
+  uint32_t colmax[NR];           // score_key of a tile's row maxima
+  uint64_t k_full[kTrStages], v_full[kTrStages], kv_empty[kTrStages];
+  uint64_t s_full[2], s_free[2], p_full[kPBufs], p_free[kPBufs];
+  uint64_t q_full, q_free, o_free, fin;
+  uint32_t bad[NR / 32];         // rows with a result that is not finite
+  int meta[kTrStages];           // tile number in the group, times two, plus 1 for the segment's last
+  int new_epoch[2];
+  int dead[2];
+  uint32_t tmem_base;
+  unsigned long long total;
+  int64_t start_base;
+  int start_b;
+  int cnt[2][kTrLoadWarps];
+  int qkey[kQueue];              // selected keys waiting for a tile (ring)
+  uint2 qbits[kQueue];           // and which rows selected them
+  uint32_t kmask[NR == 64 ? kTrStages : 1][2][NR == 64 ? kTrKeys : 1];  // row bits of the tile's keys
+};
+
+// ---- small helpers --------------------------------------------------------------
+RTP_DEVICE void cp16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+RTP_DEVICE void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+RTP_DEVICE void cp_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory"); }
+RTP_DEVICE void fence_async() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
+
+template <int N>
+RTP_DEVICE void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
+template <int N>
+RTP_DEVICE void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
+
+// Barrier of n threads that also ORs a predicate.
+RTP_DEVICE bool bar_or(int id, int n, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(r)
+      : "r"((uint32_t)x), "r"(id), "r"(n)
+      : "memory");
+  return r != 0;
+}
+
+// (a * s + c.lo, b * s + c.hi), c a pair of floats in one 64-bit word.
+RTP_DEVICE void fma2c(uint32_t a, uint32_t b, uint64_t s, uint64_t c, float& ra, float& rb) {
+  uint64_t x, r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(x) : "r"(a), "r"(b));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(x), "l"(s), "l"(c));
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(ra), "=f"(rb) : "l"(r));
+}
+
+// Column c of every lane reduced over the 32 lanes, left in lane c (31 shuffles).
+template <int O, typename F>
+RTP_DEVICE float reduce_columns(float (&x)[2 * O], int lane, F op) {
+  const bool up = lane & O;
+  float y[O];
+#pragma unroll
+  for (int i = 0; i < O; ++i) {
+    const float keep = up ? x[i + O] : x[i], send = up ? x[i] : x[i + O];
+    y[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, O));
+  }
+  if constexpr (O == 1)
+    return y[0];
+  else
+    return reduce_columns<O / 2>(y, lane, op);
+}
+
+// ---- what a sequence's rows attend -------------------------------------------------
+// Committed tokens of sequence b.
 RTP_DEVICE int committed(const TreeAttnArgs& A, int b) {
   const int n = A.lens ? max(A.lens[b], 0) : A.N;
   return A.ring ? n : min(n, A.N);
 }
 
-// Tokens between cache row j and the newest committed one (0: the newest).
-RTP_DEVICE int row_age(const TreeAttnArgs& A, int n, int j) {
-  if (!A.ring || n <= A.N) return n - 1 - j;
-  const int newest = (n - 1) % A.N;
-  return newest >= j ? newest - j : newest - j + A.N;
+RTP_DEVICE int row_of(const TreeAttnArgs& A, uint32_t p) { return A.ring ? (int)(p % (uint32_t)A.N) : (int)p; }
+
+// Tokens between a draft and the oldest committed key it attends, less the draft's own depth (W > 0).
+RTP_DEVICE int draft_depth(const TreeAttnArgs& A, int b, int t) {
+  return A.W > 0 ? max(__ldg(A.depth + (int64_t)b * A.T + t), 0) : 0;
+}
+RTP_DEVICE int oldest_age(const TreeAttnArgs& A, int depth) { return A.W - 2 - depth; }
+
+RTP_DEVICE bool tree_bit(const TreeAttnArgs& A, int b, int t, int j) {
+  return (__ldg(A.tree + ((int64_t)b * A.T + t) * A.tree_words + (j >> 5)) >> (j & 31)) & 1u;
 }
 
-RTP_DEVICE float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-  return y;
+// Tiles of one KV head of a sequence: its drafts first, then the committed keys from position lo on (with a
+// selection: rounds of kTrRound keys, aligned).
+struct TrSpan {
+  int n, lo, draft_tiles, tiles;
+};
+template <bool SEL>
+RTP_DEVICE TrSpan span_of(const TreeAttnArgs& A, int b) {
+  constexpr uint32_t kStep = SEL ? kTrRound : kTrKeys;
+  TrSpan s;
+  s.n = committed(A, b);
+  s.lo = A.W > 0 ? max(0, s.n - (A.W - 1)) : 0;
+  if (SEL) s.lo = s.lo / kTrRound * kTrRound;
+  s.draft_tiles = (A.T + kTrKeys - 1) / kTrKeys;
+  s.tiles = s.draft_tiles + (int)(((uint32_t)(s.n - s.lo) + kStep - 1) / kStep);
+  return s;
 }
 
-// One CTA per (sequence, query head, draft); its warps take keys in turn.
-__global__ void __launch_bounds__(kTrThreads) tree_attn_kernel(TreeAttnArgs A) {
-  __shared__ float wm[4], wl[4];
-  __shared__ __align__(16) float wo[4][kHeadDim];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t = blockIdx.x, bh = blockIdx.y;
-  const int b = bh / A.Hq, h = bh % A.Hq, kvh = h / A.G;
-  const int n = committed(A, b), used = min(n, A.N);
-  const int depth = A.W > 0 ? max(A.depth[(int64_t)b * A.T + t], 0) : 0;
+// One segment: the tiles [u0, u1) of a group (b, kvh) that a CTA works on.
+struct TrSeg {
+  int b, kvh;
+  TrSpan span;
+  int u0, u1;
+  int64_t base;  // the line's tile number of the group's tile 0
+};
+
+// Walks the segments of the range [lo, hi) of the line of tiles.
+template <bool SEL>
+struct TrWalk {
+  int64_t pos, hi, base_b;
+  TrSeg s;
+  RTP_DEVICE void start(const TreeAttnArgs& A, int64_t lo, int64_t end, int b, int64_t base) {
+    pos = lo;
+    hi = end;
+    base_b = base;
+    s.b = b;
+    s.span = span_of<SEL>(A, b);
+    s.kvh = (int)((lo - base) / s.span.tiles);
+    fill();
+  }
+  RTP_DEVICE void fill() {
+    s.base = base_b + (int64_t)s.kvh * s.span.tiles;
+    s.u0 = (int)(pos - s.base);
+    s.u1 = (int)min((int64_t)s.span.tiles, hi - s.base);
+  }
+  RTP_DEVICE bool next(const TreeAttnArgs& A) {
+    pos = s.base + s.u1;
+    if (pos >= hi) return false;
+    if (++s.kvh == A.Hk) {
+      base_b += (int64_t)A.Hk * s.span.tiles;
+      s.kvh = 0;
+      s.span = span_of<SEL>(A, ++s.b);
+    }
+    fill();
+    return true;
+  }
+};
+
+// ---- the scalar pass ------------------------------------------------------------------
+// One warp computes one row from the definition.
+__device__ __noinline__ void scalar_row(const TreeAttnArgs& A, int b, int h, int t, float4& out) {
+  const int lane = threadIdx.x & 31, kvh = h / A.G;
   auto row = [&](const View4& x, int head, int64_t r) {
-    return static_cast<const __nv_bfloat16*>(x.data) + b * x.sb + head * x.sh + r * x.sn + 4 * lane;
-  };
-  auto load = [](const __nv_bfloat16* p) {
-    const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(x.data) + b * x.sb +
+                                                         head * x.sh + r * x.sn + 4 * lane));
     return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
   };
-  const float4 q = load(row(A.q, h, t));
+  const float4 q = row(A.q, h, t);
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto take = [&](const __nv_bfloat16* kp, const __nv_bfloat16* vp) {
-    const float4 k = load(kp), v = load(vp);
+  auto take = [&](const float4 k, const float4 v) {
     const float s = warp_sum(q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w) * A.scale_log2;
     const float mn = fmaxf(m, s);
-    const float al = mn == -INFINITY ? 1.f : ex2(m - mn), p = mn == -INFINITY ? 0.f : ex2(s - mn);
+    const float al = mn == -INFINITY ? 1.f : ex2a(m - mn), p = mn == -INFINITY ? 0.f : ex2a(s - mn);
     m = mn;
     l = l * al + p;
     o = make_float4(o.x * al + p * v.x, o.y * al + p * v.y, o.z * al + p * v.z, o.w * al + p * v.w);
   };
-  const uint32_t* sel = A.sel ? A.sel + ((int64_t)bh * A.T + t) * A.sel_words : nullptr;
-  const int oldest = A.W > 0 ? A.W - 2 - depth : n;  // age of the oldest committed key the token attends
-  const int first = A.ring ? 0 : oldest < 0 ? used : max(0, n - 1 - oldest);
-  for (int j = first + warp; j < used; j += 4) {
-    if (row_age(A, n, j) > oldest) continue;
-    if (sel && !((__ldg(sel + (j >> 5)) >> (j & 31)) & 1u)) continue;
-    take(row(A.k, kvh, j), row(A.v, kvh, j));
-  }
-  const uint32_t* tree = A.tree + ((int64_t)b * A.T + t) * A.tree_words;
-  for (int j = warp; j < A.T; j += 4) {
-    if (!((__ldg(tree + (j >> 5)) >> (j & 31)) & 1u)) continue;
-    if (A.W > 0 && max(A.depth[(int64_t)b * A.T + j], 0) <= depth - A.W) continue;
+  const int n = committed(A, b), depth = draft_depth(A, b, t);
+  const int lo = A.W > 0 ? max(0, n - 1 - oldest_age(A, depth)) : 0;  // (past n when the window holds none)
+  const uint32_t* sel = A.sel ? A.sel + ((int64_t)(b * A.Hq + h) * A.T + t) * A.sel_words : nullptr;
+  if (A.W <= 0 || oldest_age(A, depth) >= 0)
+    for (int p = lo; p < n; ++p) {
+      if (sel && !((__ldg(sel + (p >> 5)) >> (p & 31)) & 1u)) continue;
+      const int r = row_of(A, (uint32_t)p);
+      take(row(A.k, kvh, r), row(A.v, kvh, r));
+    }
+  for (int j = 0; j < A.T; ++j) {
+    if (!tree_bit(A, b, t, j)) continue;
+    if (A.W > 0 && draft_depth(A, b, j) <= depth - A.W) continue;
     take(row(A.kn, kvh, j), row(A.vn, kvh, j));
   }
-  if (lane == 0) {
-    wm[warp] = m;
-    wl[warp] = l;
-  }
-  reinterpret_cast<float4*>(wo[warp])[lane] = o;
-  __syncthreads();
-  const int d = threadIdx.x;
-  float M = -INFINITY, L = 0.f, x = 0.f;
-  for (int w = 0; w < 4; ++w) M = fmaxf(M, wm[w]);
-  for (int w = 0; w < 4; ++w) {
-    const float f = wm[w] == -INFINITY ? 0.f : ex2(wm[w] - M);
-    L += f * wl[w];
-    x += f * wo[w][d];
-  }
-  const float y = L != 0.f ? x / L : 0.f;  // (a NaN stays one)
-  const int64_t off = b * A.o.sb + h * A.o.sh + t * A.o.sn + d;
+  const float inv = l != 0.f ? 1.f / l : 0.f;  // (a NaN stays one)
+  out = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+}
+
+RTP_DEVICE void store_row4(const TreeAttnArgs& A, int b, int h, int t, int lane, const float4& y) {
+  const int64_t off = b * A.o.sb + h * A.o.sh + t * A.o.sn + 4 * lane;
   if (A.o_bf16)
-    static_cast<__nv_bfloat16*>(A.o.data)[off] = __float2bfloat16_rn(y);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(A.o.data) + off) =
+        make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
   else
-    static_cast<float*>(A.o.data)[off] = y;
+    *reinterpret_cast<float4*>(static_cast<float*>(A.o.data) + off) = y;
+}
+
+RTP_DEVICE bool finite4(const float4& y) {
+  return isfinite(y.x) && isfinite(y.y) && isfinite(y.z) && isfinite(y.w);
+}
+
+// ---- layout of the workspace -------------------------------------------------------------
+struct TrLayout {
+  int nr, rbs, ranges;  // rows per CTA, row blocks per KV head, ranges of the line of tiles
+  size_t table, o, ml;  // byte sizes
+  size_t bytes() const { return table + o + ml; }
+};
+
+TrLayout tree_layout(int64_t B, int64_t Hq, int64_t T, int64_t Hk, bool sel) {
+  TrLayout L;
+  const int64_t rows = Hq / Hk * T;
+  // 128 rows read the keys once for 65 rows and more; 64 keep two P tiles in flight (and the queue of a selection)
+  L.nr = sel || rows <= 64 ? 64 : 128;
+  L.rbs = (int)((rows + L.nr - 1) / L.nr);
+  L.ranges = L.rbs >= kTrSms ? 1 : kTrSms / L.rbs;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  L.table = up((size_t)(B * Hk) * sizeof(int2));
+  const size_t slots = (size_t)L.rbs * L.ranges * 2 * L.nr;
+  L.o = up(slots * kHeadDim * sizeof(float));
+  L.ml = up(slots * sizeof(float2));
+  return L;
+}
+
+// What the kernels know of it.  A piece of a group lies in slot 2 range + (1 if it begins the group).
+struct TrParts {
+  int2* table;  // [B * Hk] first range and number of pieces
+  float* o;     // [row block][2 * ranges][nr][128]
+  float2* ml;   // [row block][2 * ranges][nr] reference (log2), sum
+  int nr, rbs, ranges;
+};
+
+struct TrMaps {
+  CUtensorMap k, v;
+};
+
+// ---- the kernel --------------------------------------------------------------------------
+template <int NR, bool SEL>
+__global__ void __launch_bounds__(TrSmem<NR>::kThreads, 1)
+tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                 const __grid_constant__ TreeAttnArgs A, const __grid_constant__ TrParts W, int use_tma) {
+  using Smem = TrSmem<NR>;
+  constexpr int kSoft = Smem::kSoftWarps * 32, kLoad = kTrLoadWarps * 32;
+  constexpr int kPBufs = Smem::kPBufs;
+  constexpr uint32_t kTmemOe = 2 * NR, kTmemOt = 3 * NR, kTmemCols = 4 * NR;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  Smem& S = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rb = blockIdx.x % W.rbs, range = blockIdx.x / W.rbs;
+  const int rows = A.G * A.T, row0 = rb * NR, nrows = min(NR, rows - row0);
+
+  if (tid == 0) {
+    for (int i = 0; i < kTrStages; ++i) {
+      mbar_init(&S.k_full[i], 1);
+      mbar_init(&S.v_full[i], 1);
+      mbar_init(&S.kv_empty[i], 1);
+      S.new_epoch[i] = 0;
+      S.dead[i] = 0;
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&S.s_full[i], 1);
+      mbar_init(&S.s_free[i], Smem::kSoftWarps);
+    }
+    for (int i = 0; i < kPBufs; ++i) {
+      mbar_init(&S.p_full[i], Smem::kSoftWarps);
+      mbar_init(&S.p_free[i], 1);
+    }
+    mbar_init(&S.q_full, 1);
+    mbar_init(&S.q_free, 1);
+    mbar_init(&S.o_free, Smem::kSoftWarps);
+    mbar_init(&S.fin, 1);
+    mbar_fence_init();
+    S.total = 0;
+  }
+  if (tid < NR) S.colmax[tid] = kTrNoKey;
+  if (tid < NR / 32) S.bad[tid] = 0u;
+  if (warp == 0) tmem_alloc(&S.tmem_base, kTmemCols);
+  // rows past the last one never get a P: zeros
+  if (nrows < NR) {
+    uint4* p = reinterpret_cast<uint4*>(&S.p[0][0][0]);
+    for (int i = tid; i < (int)(sizeof(S.p) / 16); i += Smem::kThreads) p[i] = make_uint4(0u, 0u, 0u, 0u);
+    fence_async();
+  }
+  pdl_wait();
+  pdl_release();
+  __syncthreads();
+
+  // ---- this CTA's range of the line of tiles ----
+  {
+    unsigned long long mine = 0;
+    for (int b = tid; b < A.B; b += Smem::kThreads) mine += (unsigned long long)span_of<SEL>(A, b).tiles;
+    if (mine) atomicAdd(&S.total, mine);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = S.tmem_base;
+  const int64_t total = (int64_t)S.total * A.Hk;
+  const int64_t per = (total + W.ranges - 1) / W.ranges;
+  const int64_t lo = range * per, hi = min(lo + per, total);
+  if (lo < hi && warp == 0) {
+    int64_t base = 0;
+    for (int b0 = 0; b0 < A.B; b0 += 32) {
+      const int64_t mine = b0 + lane < A.B ? (int64_t)span_of<SEL>(A, b0 + lane).tiles * A.Hk : 0;
+      int64_t incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, base + incl > lo);
+      if (past) {
+        if (lane == __ffs(past) - 1) {
+          S.start_b = b0 + lane;
+          S.start_base = base + incl - mine;
+        }
+        break;
+      }
+      base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+  }
+  __syncthreads();
+
+  bool alive = true;
+  TrWalk<SEL> walk;
+  bool more = lo < hi;
+  if (more) walk.start(A, lo, hi, S.start_b, S.start_base);
+  uint32_t it = 0;  // tiles of this CTA so far
+
+  if (warp >= Smem::kSoftWarps && warp < Smem::kSoftWarps + kTrLoadWarps) {
+    // ---------------- loaders ----------------
+    regs_dec<Smem::kLoadRegs>();
+    const int lt = tid - kSoft, lw = warp - Smem::kSoftWarps;
+    const int chunk = lt & 15, r_first = lt >> 4;  // this thread's 16-byte column; rows r_first + 8 i
+    // (8 rows on, the swizzle is the same)
+    const uint32_t slot0 = (uint32_t)r_first * 128u + (uint32_t)(((chunk & 7) ^ r_first) << 4);
+    const uint32_t slot_kv = slot0 + (uint32_t)(chunk >> 3) * (uint32_t)kTrHalf;
+    uint32_t segs = 0;
+    bool q_due = false;
+    // Waits for a free stage; false (for all loaders alike) once any wait gave up.
+    auto stage_free = [&]() {
+      const bool ok = mbar_wait(&S.kv_empty[it & 1], ((it >> 1) & 1u) ^ 1u, alive, A.err, A.budget);
+      return !bar_or(kBarLoad, kLoad, !ok);
+    };
+    // The tile's rows by cp.async: row_at(r, ok) gives the row of tile row r.
+    auto gather = [&](const View4& kv_k, const View4& kv_v, const TrSeg& s, int meta, auto&& row_at) {
+      const int st = it & 1;
+      const __nv_bfloat16* kb = static_cast<const __nv_bfloat16*>(kv_k.data) + s.b * kv_k.sb + s.kvh * kv_k.sh + chunk * 8;
+      const uint32_t ks = smem_addr(S.k[st]) + slot_kv;
+      const __nv_bfloat16* vb = static_cast<const __nv_bfloat16*>(kv_v.data) + s.b * kv_v.sb + s.kvh * kv_v.sh + chunk * 8;
+      const uint32_t vs = smem_addr(S.v[st]) + slot_kv;
+      int row[16];
+      uint32_t oks = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        bool ok;
+        row[i] = row_at(r_first + 8 * i, ok);
+        oks |= (uint32_t)ok << i;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const bool ok = (oks >> i) & 1u;
+        cp16(ks + 1024u * i, ok ? (const void*)(kb + row[i] * kv_k.sn) : A.q.data, ok);
+      }
+      cp_commit();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const bool ok = (oks >> i) & 1u;
+        cp16(vs + 1024u * i, ok ? (const void*)(vb + row[i] * kv_v.sn) : A.q.data, ok);
+      }
+      cp_commit();
+      if (lt == 0) S.meta[st] = meta;
+      cp_wait<1>();
+      fence_async();
+      named_sync(kBarLoad, kLoad);
+      if (lt == 0) {
+        if (q_due) mbar_arrive(&S.q_full);
+        mbar_arrive(&S.k_full[st]);
+      }
+      q_due = false;
+      cp_wait<0>();
+      fence_async();
+      named_sync(kBarLoad, kLoad);
+      if (lt == 0) mbar_arrive(&S.v_full[st]);
+      ++it;
+    };
+    bool ok = true;
+    for (; more && ok; more = walk.next(A)) {
+      const TrSeg& s = walk.s;
+      // ---- the query rows (the previous segment's products are done with the buffer) ----
+      {
+        const bool free = segs == 0 || mbar_wait(&S.q_free, (segs - 1) & 1u, alive, A.err, A.budget);
+        if (bar_or(kBarLoad, kLoad, !free)) break;
+        const __nv_bfloat16* qb =
+            static_cast<const __nv_bfloat16*>(A.q.data) + s.b * A.q.sb + (int64_t)s.kvh * A.G * A.q.sh + chunk * 8;
+#pragma unroll 4
+        for (int i = 0; i < NR / 8; ++i) {
+          const int r = r_first + 8 * i, rr = min(row0 + r, rows - 1);
+          const int g = rr / A.T, t = rr - g * A.T;
+          cp16(smem_addr(S.q) + (uint32_t)(chunk >> 3) * (NR * 128u) + slot0 + 1024u * i, qb + g * A.q.sh + t * A.q.sn,
+               r < nrows);
+        }
+        cp_commit();
+        q_due = true;
+        ++segs;
+      }
+      const int drafts_end = min(s.u1, s.span.draft_tiles);
+      for (int u = s.u0; u < drafts_end; ++u) {
+        if (!(ok = stage_free())) break;
+        gather(A.kn, A.vn, s, 2 * u + (u + 1 == s.u1), [&](int r, bool& live) {
+          const int j = u * kTrKeys + r;
+          live = j < A.T;
+          return live ? j : 0;
+        });
+      }
+      if (!ok) break;
+      if constexpr (!SEL) {
+        for (int u = max(s.u0, s.span.draft_tiles); u < s.u1; ++u) {
+          if (!(ok = stage_free())) break;
+          const uint32_t p0 = (uint32_t)s.span.lo + (uint32_t)(u - s.span.draft_tiles) * kTrKeys;
+          const int left = s.span.n - (int)p0;  // committed rows from here on
+          const int first = row_of(A, p0);
+          const int meta = 2 * u + (u + 1 == s.u1);
+          if (use_tma && left >= kTrKeys && A.N - first >= kTrKeys) {
+            const int st = it & 1;
+            if (lt == 0) {
+              S.meta[st] = meta;
+              mbar_expect_tx(&S.k_full[st], kTrTile);
+              tma_load_4d(S.k[st], &kmap, &S.k_full[st], 0, first, s.kvh, s.b);
+              tma_load_4d(S.k[st] + kTrHalf, &kmap, &S.k_full[st], 64, first, s.kvh, s.b);
+              mbar_expect_tx(&S.v_full[st], kTrTile);
+              tma_load_4d(S.v[st], &vmap, &S.v_full[st], 0, first, s.kvh, s.b);
+              tma_load_4d(S.v[st] + kTrHalf, &vmap, &S.v_full[st], 64, first, s.kvh, s.b);
+            }
+            if (q_due) {
+              cp_wait<0>();
+              fence_async();
+              named_sync(kBarLoad, kLoad);
+              if (lt == 0) mbar_arrive(&S.q_full);
+              q_due = false;
+            }
+            ++it;
+          } else {
+            gather(A.k, A.v, s, meta, [&](int r, bool& live) {
+              live = r < left;
+              return live ? row_of(A, p0 + (uint32_t)r) : 0;
+            });
+          }
+        }
+      } else {
+        const int rounds = s.span.tiles - s.span.draft_tiles;
+        if (s.u1 <= s.span.draft_tiles) continue;
+        int head = 0, count = 0, turn = 0;
+        // this lane's rows: their mask rows, and the first key position their window admits
+        const uint32_t* words[2];
+        int from[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = lane + 32 * i;
+          words[i] = nullptr;
+          from[i] = 0;
+          if (r < nrows) {
+            words[i] = A.sel + ((int64_t)(s.b * A.Hq + s.kvh * A.G) * A.T + row0 + r) * A.sel_words;
+            if (A.W > 0) {
+              const int age = oldest_age(A, draft_depth(A, s.b, (row0 + r) % A.T));
+              from[i] = age < 0 ? s.span.n : s.span.n - 1 - age;
+            }
+          }
+        }
+        auto emit = [&](int take, bool last) {
+          const int st = it & 1;
+          // one key per loader thread: its row bits for the softmax
+          uint2 bits = make_uint2(0u, 0u);
+          if (lt < take) bits = S.qbits[(head + lt) & (kTrQueue - 1)];
+          S.kmask[st][0][lt] = bits.x;
+          S.kmask[st][1][lt] = bits.y;
+          const int at = head;
+          gather(A.k, A.v, s, 2 * s.span.draft_tiles + last, [&](int r, bool& live) {
+            live = r < take;
+            return live ? S.qkey[(at + r) & (kTrQueue - 1)] : 0;
+          });
+          head = (head + take) & (kTrQueue - 1);
+          count -= take;
+        };
+        for (int u = max(s.u0, s.span.draft_tiles); u < s.u1 && ok; ++u) {
+          // neighbouring ranges take rounds from all over the context (a prime larger than their number),
+          // since selected keys come in clusters
+          const int i0 = u - s.span.draft_tiles;
+          const int round = (int)((uint64_t)i0 * 2654435761ull % (uint64_t)rounds);
+          const int key0 = s.span.lo + round * kTrRound + lw * 128;
+          uint32_t x[2][4], uni[4];
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int wb = key0 + 32 * w, rem = s.span.n - wb;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) x[i][w] = words[i] && rem > 0 ? __ldg(words[i] + (wb >> 5)) : 0u;
+          }
+          int mine = 0;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int wb = key0 + 32 * w, rem = s.span.n - wb;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (rem < 32) x[i][w] &= rem > 0 ? (1u << rem) - 1u : 0u;
+              const int cut = from[i] - wb;
+              if (cut > 0) x[i][w] &= cut < 32 ? ~0u << cut : 0u;
+            }
+            uni[w] = __reduce_or_sync(0xffffffffu, x[0][w] | x[1][w]);
+            mine += __popc(uni[w]);
+          }
+          if (lane == 0) S.cnt[turn & 1][lw] = mine;
+          named_sync(kBarLoad, kLoad);
+          int before = 0, all = 0;
+#pragma unroll
+          for (int w = 0; w < kTrLoadWarps; ++w) {
+            const int c = S.cnt[turn & 1][w];
+            before += w < lw ? c : 0;
+            all += c;
+          }
+          ++turn;
+          int at = head + count + before;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t left = uni[w];
+            while (left) {
+              const int bit = __ffs(left) - 1;
+              left &= left - 1;
+              const uint32_t b0 = __ballot_sync(0xffffffffu, (x[0][w] >> bit) & 1u);
+              const uint32_t b1 = __ballot_sync(0xffffffffu, (x[1][w] >> bit) & 1u);
+              if (lane == 0) {
+                S.qkey[at & (kTrQueue - 1)] = key0 + 32 * w + bit;
+                S.qbits[at & (kTrQueue - 1)] = make_uint2(b0, b1);
+              }
+              ++at;
+            }
+          }
+          count += all;
+          named_sync(kBarLoad, kLoad);
+          while (count > kTrKeys && (ok = stage_free())) emit(kTrKeys, false);
+        }
+        if (ok && (ok = stage_free())) emit(count, true);
+      }
+      if (!ok) break;
+    }
+    cp_wait<0>();
+    if (lt == 0)  // copies still in flight land before the CTA ends
+      for (uint32_t i = it > 2 ? it - 2 : 0; i < it; ++i) {
+        mbar_drain(&S.k_full[i & 1], (i >> 1) & 1u, A.err);
+        mbar_drain(&S.v_full[i & 1], (i >> 1) & 1u, A.err);
+      }
+  } else if (warp >= Smem::kSoftWarps + kTrLoadWarps) {
+    // ---------------- MMA issuer (one elected lane) ----------------
+    regs_dec<Smem::kMmaRegs>();
+    if (warp == Smem::kSoftWarps + kTrLoadWarps && lane == 0 && more) {
+      constexpr uint32_t idesc_s = umma_idesc_bf16_f32(kTrKeys, NR);
+      constexpr uint32_t idesc_o = umma_idesc_bf16_f32(kHeadDim, NR) | (1u << 15) | (1u << 16);  // both MN-major
+      uint32_t epochs = 0, segs = 0;
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity & 1u, alive, A.err, A.budget); };
+      // O^T += V^T P^T of tile j
+      auto issue_pv = [&](uint32_t j) -> bool {
+        const int st = j & 1, pb = j % kPBufs;
+        if (!wait(&S.p_full[pb], j / kPBufs)) return false;
+        const bool fresh = S.new_epoch[st] != 0;
+        if (fresh) {
+          if (epochs > 0 && !wait(&S.o_free, epochs - 1)) return false;
+          ++epochs;
+        }
+        if (!wait(&S.v_full[st], j >> 1)) return false;
+        tc_fence_after();
+        const uint32_t va = smem_addr(S.v[st]), ph = smem_addr(S.p[pb][0]), pl = smem_addr(S.p[pb][1]);
+#pragma unroll
+        for (int kk = 0; kk < kTrKeys / 16; ++kk) {
+          const uint64_t a = umma_desc_sw128(va + (uint32_t)kk * 2048u, kTrHalf);
+          umma_f16(tmem + kTmemOe, a, umma_desc_sw128(ph + (uint32_t)kk * 2048u, kTrHalf), idesc_o,
+                   fresh && kk == 0 ? 0u : 1u);
+          umma_f16(tmem + kTmemOe, a, umma_desc_sw128(pl + (uint32_t)kk * 2048u, kTrHalf), idesc_o, 1u);
+        }
+        umma_commit(&S.kv_empty[st]);
+        umma_commit(&S.p_free[pb]);
+        return true;
+      };
+      bool ok = true;
+      for (; more && ok; more = walk.next(A)) {
+        ok = wait(&S.q_full, segs++);
+        for (bool last = false, first = true; ok && !last; first = false) {
+          const int st = it & 1;
+          if (!(ok = wait(&S.k_full[st], it >> 1))) break;
+          last = S.meta[st] & 1;
+          if (!(ok = wait(&S.s_free[st], (it >> 1) ^ 1u))) break;
+          tc_fence_after();
+          const uint32_t ka = smem_addr(S.k[st]), qa = smem_addr(S.q);
+#pragma unroll
+          for (int kk = 0; kk < kHeadDim / 16; ++kk) {
+            const uint32_t h = (uint32_t)(kk >> 2), o = 32u * (uint32_t)(kk & 3);
+            umma_f16(tmem + (uint32_t)st * NR, umma_desc_sw128(ka + h * kTrHalf + o, 16),
+                     umma_desc_sw128(qa + h * (NR * 128u) + o, 16), idesc_s, kk > 0 ? 1u : 0u);
+          }
+          umma_commit(&S.s_full[st]);
+          if (last) umma_commit(&S.q_free);
+          ++it;
+          if (!first) ok = issue_pv(it - 2);
+        }
+        if (ok) ok = issue_pv(it - 1);
+      }
+      umma_commit(&S.fin);  // every product issued is done before TMEM is freed
+      mbar_drain(&S.fin, 0, A.err);
+    }
+  } else {
+    // ---------------- softmax, output ----------------
+    regs_inc<Smem::kSoftRegs>();
+    const int quad = warp & 3, col0 = 32 * (warp >> 2);  // this thread: key (then dim) 32 quad + lane, rows col0 ..
+    const int key = 32 * quad + lane;
+    const int act = max(0, min(2, (nrows - col0 + 15) / 16));  // its 16-row halves that hold rows
+    const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)col0;
+    uint64_t scale2;
+    asm("mov.b64 %0, {%1, %1};\n" : "=l"(scale2) : "f"(A.scale_log2));
+    const int g_first = (row0 + col0) / A.T, t_first = (row0 + col0) - g_first * A.T;
+    bool ok = true;
+    for (; more && ok; more = walk.next(A)) {
+      const TrSeg& s = walk.s;
+      int max_depth = 0;
+      if (A.W > 0) {
+        for (int t = lane; t < A.T; t += 32) max_depth = max(max_depth, draft_depth(A, s.b, t));
+        max_depth = __reduce_max_sync(0xffffffffu, max_depth);
+      }
+      float l[32];
+#pragma unroll
+      for (int c = 0; c < 32; ++c) l[c] = 0.f;
+      bool first = true, has_total = false;
+      int in_epoch = 0;
+      for (bool last = false; !last;) {
+        const int st = it & 1, pb = it % kPBufs;
+        bool live = mbar_wait(&S.k_full[st], (it >> 1) & 1u, alive, A.err, A.budget) &&
+                    mbar_wait(&S.s_full[st], (it >> 1) & 1u, alive, A.err, A.budget);
+        live = __all_sync(0xffffffffu, live);
+        if (!live) {
+          alive = false;
+          S.dead[st] = 1;
+        }
+        tc_fence_after();
+        const int u = S.meta[st] >> 1;
+        last = S.meta[st] & 1;
+
+        // ---- which of this thread's rows attend its key ----
+        uint32_t mw = ~0u;
+        if (u < s.span.draft_tiles) {
+          const int j = u * kTrKeys + key;
+          mw = 0u;
+          if (u * kTrKeys + 32 * quad < A.T) {
+            const int dj = j < A.T ? draft_depth(A, s.b, j) : 0;
+            int t = t_first;
+            for (int c = 0; c < 32 && col0 + c < nrows; ++c) {
+              const bool in = j < A.T && tree_bit(A, s.b, t, j) && (A.W <= 0 || dj > draft_depth(A, s.b, t) - A.W);
+              mw |= (uint32_t)in << c;
+              if (++t == A.T) t = 0;
+            }
+          }
+        } else if constexpr (SEL) {
+          mw = S.kmask[st][col0 >> 5][key];
+        } else {
+          const uint32_t p0 = (uint32_t)s.span.lo + (uint32_t)(u - s.span.draft_tiles) * kTrKeys;
+          const int age = s.span.n - 1 - (int)(p0 + (uint32_t)key);  // (below 0: past the end)
+          if (age < 0) mw = 0u;
+          if (A.W > 0 && s.span.n - 1 - (int)p0 > oldest_age(A, max_depth)) {
+            int t = t_first;
+            uint32_t in = 0u;
+            for (int c = 0; c < 32 && col0 + c < nrows; ++c) {
+              in |= (uint32_t)(age <= oldest_age(A, draft_depth(A, s.b, t))) << c;
+              if (++t == A.T) t = 0;
+            }
+            mw &= in;
+          }
+        }
+
+        // ---- logits less the reference (log2 units) ----
+        float d[32];
+        auto scores = [&](bool relative) {
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            if (hh >= act) continue;
+            uint32_t v[16];
+            tmem_ld16(lane_base + (uint32_t)st * NR + 16u * hh, v);
+            tmem_ld_wait();
+            const ulonglong2* nr = reinterpret_cast<const ulonglong2*>(S.nref + col0 + 16 * hh);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int c = 16 * hh + 4 * i;
+              const ulonglong2 r = relative ? nr[i] : make_ulonglong2(0ull, 0ull);
+              fma2c(v[4 * i], v[4 * i + 1], scale2, r.x, d[c], d[c + 1]);
+              fma2c(v[4 * i + 2], v[4 * i + 3], scale2, r.y, d[c + 2], d[c + 3]);
+            }
+          }
+          if (mw != ~0u) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) d[c] = (mw >> c) & 1u ? d[c] : -INFINITY;
+          }
+        };
+        float top = -INFINITY;
+        if (!first && act > 0) {
+          scores(true);
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            if (hh >= act) continue;
+#pragma unroll
+            for (int c = 16 * hh; c < 16 * hh + 16; c += 2) top = max3f(top, d[c], d[c + 1]);
+          }
+        }
+        const bool raise = bar_or(kBarSoft, kSoft, first || top > kTrSlack);
+        if (S.dead[st]) {
+          ok = false;
+          break;
+        }
+        if (raise) {
+          // the tile's maximum of every row, over its keys
+          if (act > 0) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) d[c] = -INFINITY;
+            scores(false);
+            const float m = reduce_columns<16>(d, lane, [](float a, float b) { return fmaxf(a, b); });
+            atomicMax(&S.colmax[col0 + lane], score_key(m));
+          }
+          named_sync(kBarSoft, kSoft);
+          if (tid < NR) {
+            const float old = first ? kTrNone : -S.nref[tid];
+            const float now = fmaxf(old, key_score(S.colmax[tid]));
+            S.nref[tid] = -now;
+            S.alpha[tid] = ex2a(old - now);
+            S.colmax[tid] = kTrNoKey;
+          }
+          named_sync(kBarSoft, kSoft);
+          if (act > 0) scores(true);
+          if (!first) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) l[c] *= S.alpha[col0 + c];
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.s_free[st]);
+
+        // ---- P = 2^d as bf16 hi + lo, key-major rows of 64 query rows (128 bytes, swizzled) ----
+        uint32_t hi_w[16], lo_w[16];
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          if (hh >= act) continue;
+#pragma unroll
+          for (int i = 8 * hh; i < 8 * hh + 8; ++i) {
+            const float p0 = ex2a(d[2 * i]), p1 = ex2a(d[2 * i + 1]);
+            add2(l[2 * i], l[2 * i + 1], p0, p1);
+            hi_w[i] = pack_bf16x2(p0, p1);
+            float r0, r1;
+            sub2p(p0, p1, bf16_lo(hi_w[i]), bf16_hi(hi_w[i]), r0, r1);
+            lo_w[i] = pack_bf16x2(r0, r1);
+          }
+        }
+        const uint32_t uses = it / kPBufs;  // of this P tile so far
+        if (!__all_sync(0xffffffffu, mbar_wait(&S.p_free[pb], (uses & 1u) ^ 1u, alive, A.err, A.budget))) alive = false;
+        {
+          const uint32_t off = (uint32_t)(col0 >> 6) * (uint32_t)kTrHalf + (uint32_t)key * 128u;
+          const int c8 = (col0 & 63) >> 3;  // first 16-byte chunk of these rows
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (i >= 2 * act) continue;
+            const uint32_t o = off + (uint32_t)(((c8 + i) ^ (key & 7)) << 4);
+            *reinterpret_cast<uint4*>(&S.p[pb][0][o]) =
+                make_uint4(hi_w[4 * i], hi_w[4 * i + 1], hi_w[4 * i + 2], hi_w[4 * i + 3]);
+            *reinterpret_cast<uint4*>(&S.p[pb][1][o]) =
+                make_uint4(lo_w[4 * i], lo_w[4 * i + 1], lo_w[4 * i + 2], lo_w[4 * i + 3]);
+          }
+        }
+        fence_async();
+        const bool fresh = raise || in_epoch == kTrEpoch;
+        if (tid == 0) S.new_epoch[st] = fresh;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.p_full[pb]);
+
+        // ---- the epoch before this tile joins the total ----
+        if (fresh && !first) {
+          const uint32_t j = it - 1;
+          if (!__all_sync(0xffffffffu, mbar_wait(&S.p_free[j % kPBufs], (j / kPBufs) & 1u, alive, A.err, A.budget)))
+            alive = false;
+          tc_fence_after();
+#pragma unroll 1
+          for (int hh = 0; hh < act; ++hh) {
+            uint32_t e[16], o[16];
+            tmem_ld16(lane_base + kTmemOe + 16u * hh, e);
+            if (has_total) tmem_ld16(lane_base + kTmemOt + 16u * hh, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              float y = __uint_as_float(e[c]);
+              if (has_total) y += __uint_as_float(o[c]);
+              if (raise) y *= S.alpha[col0 + 16 * hh + c];
+              o[c] = __float_as_uint(y);
+            }
+            tmem_st16(lane_base + kTmemOt + 16u * hh, o);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&S.o_free);
+          has_total = true;
+        }
+        in_epoch = fresh ? 1 : in_epoch + 1;
+        first = false;
+        ++it;
+      }
+      if (!ok) break;
+
+      // ---- the segment's end: row sums over all keys, then O ----
+      {
+        const uint32_t j = it - 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(&S.p_free[j % kPBufs], (j / kPBufs) & 1u, alive, A.err, A.budget)))
+          alive = false;
+        tc_fence_after();
+      }
+      const float lsum = reduce_columns<16>(l, lane, [](float a, float b) { return a + b; });
+      named_sync(kBarSoft, kSoft);  // (every warp is done with the last raise's factors)
+      for (int w = 0; w < 4; ++w) {   // the four warps of these rows, in order
+        if (quad == w) S.alpha[col0 + lane] = w == 0 ? lsum : S.alpha[col0 + lane] + lsum;
+        named_sync(kBarSoft, kSoft);
+      }
+      const bool whole = s.u0 == 0 && s.u1 == s.span.tiles;
+      const int grp = s.b * A.Hk + s.kvh;
+      const int64_t slot = (int64_t)rb * 2 * W.ranges + 2 * range + (s.u0 == 0 ? 1 : 0);
+      if (!whole && tid < nrows) W.ml[slot * NR + tid] = make_float2(-S.nref[tid], S.alpha[tid]);
+      if (s.u0 == 0 && rb == 0 && tid == 0)
+        W.table[grp] = make_int2(range, (int)((s.base + s.span.tiles - 1) / per) - range + 1);
+      uint32_t bad = 0u;
+      int g = g_first, t = t_first;
+#pragma unroll 1
+      for (int hh = 0; hh < act; ++hh) {
+        uint32_t e[16], o[16];
+        tmem_ld16(lane_base + kTmemOe + 16u * hh, e);
+        if (has_total) tmem_ld16(lane_base + kTmemOt + 16u * hh, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int c = col0 + 16 * hh + i;
+          float y = __uint_as_float(e[i]);
+          if (has_total) y += __uint_as_float(o[i]);
+          if (c < nrows) {
+            if (whole) {
+              const float sum = S.alpha[c];
+              y *= sum != 0.f ? 1.f / sum : 0.f;
+              bad |= (uint32_t)!isfinite(y) << (16 * hh + i);
+              const int64_t off = s.b * A.o.sb + (int64_t)(s.kvh * A.G + g) * A.o.sh + t * A.o.sn + key;
+              if (A.o_bf16)
+                static_cast<__nv_bfloat16*>(A.o.data)[off] = __float2bfloat16_rn(y);
+              else
+                static_cast<float*>(A.o.data)[off] = y;
+            } else {
+              W.o[(slot * NR + c) * kHeadDim + key] = y;
+            }
+          }
+          if (++t == A.T) {
+            t = 0;
+            ++g;
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.o_free);
+      if (whole) {
+        bad = __reduce_or_sync(0xffffffffu, bad);
+        if (lane == 0 && bad) atomicOr(&S.bad[col0 >> 5], bad);
+        named_sync(kBarSoft, kSoft);
+        for (int c = warp; c < nrows; c += Smem::kSoftWarps)
+          if ((S.bad[c >> 5] >> (c & 31)) & 1u) {
+            const int r = row0 + c, h = s.kvh * A.G + r / A.T;
+            float4 y;
+            scalar_row(A, s.b, h, r % A.T, y);
+            store_row4(A, s.b, h, r % A.T, lane, y);
+          }
+        named_sync(kBarSoft, kSoft);
+        if (tid < NR / 32) S.bad[tid] = 0u;
+      }
+      named_sync(kBarSoft, kSoft);  // (S.alpha, S.nref and S.bad are the next segment's from here on)
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_free(tmem, kTmemCols);
+}
+
+// Joins the pieces of groups that several CTAs worked on: WPR warps per query row, pieces in turn, four
+// head dims per lane.
+constexpr int kTrJoinThreads = 256;
+template <int WPR>
+__global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const __grid_constant__ TreeAttnArgs A,
+                                                                   const __grid_constant__ TrParts W) {
+  constexpr int kWarps = kTrJoinThreads / 32;
+  __shared__ float4 so[kWarps][32];
+  __shared__ float2 sml[kWarps];
+  pdl_wait();
+  pdl_release();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % WPR;
+  const int64_t rows = (int64_t)A.G * A.T, x = (int64_t)blockIdx.x * (kWarps / WPR) + warp / WPR;
+  const bool have = x < rows * A.B * A.Hk;
+  const int grp = have ? (int)(x / rows) : 0, r = have ? (int)(x % rows) : 0;
+  const int2 pieces = have ? W.table[grp] : make_int2(0, 1);
+  const bool join = pieces.y > 1;  // (one piece: its CTA has written the output)
+  float m = kTrNone, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (join) {
+    const int c = r % W.nr;
+    const int64_t slot0 = (int64_t)(r / W.nr) * 2 * W.ranges;
+    auto at = [&](int i) { return (slot0 + 2 * (pieces.x + i) + (i == 0)) * W.nr + c; };
+    constexpr int kUnroll = 4;
+    for (int i = part; i < pieces.y; i += WPR * kUnroll) {
+      float2 s[kUnroll];
+      float4 y[kUnroll];
+#pragma unroll
+      for (int q = 0; q < kUnroll; ++q) {
+        const int p = i + WPR * q;
+        s[q] = make_float2(kTrNone, 0.f);
+        y[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p < pieces.y) {
+          s[q] = W.ml[at(p)];
+          y[q] = reinterpret_cast<const float4*>(W.o + at(p) * kHeadDim)[lane];
+        }
+      }
+      float mn = m;
+#pragma unroll
+      for (int q = 0; q < kUnroll; ++q) mn = fmaxf(mn, s[q].x);
+      const float al = ex2a(m - mn);
+      m = mn;
+      l *= al;
+      o = make_float4(o.x * al, o.y * al, o.z * al, o.w * al);
+#pragma unroll
+      for (int q = 0; q < kUnroll; ++q) {
+        const float f = ex2a(s[q].x - mn);
+        l += f * s[q].y;
+        o = make_float4(o.x + f * y[q].x, o.y + f * y[q].y, o.z + f * y[q].z, o.w + f * y[q].w);
+      }
+    }
+  }
+  if (WPR > 1) {
+    so[warp][lane] = o;
+    if (lane == 0) sml[warp] = make_float2(m, l);
+    __syncthreads();
+    if (part != 0) return;
+    float M = kTrNone;
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) M = fmaxf(M, sml[warp + w].x);
+    l = 0.f;
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) {
+      const float f = ex2a(sml[warp + w].x - M);
+      const float4 y = so[warp + w][lane];
+      l += f * sml[warp + w].y;
+      o = make_float4(o.x + f * y.x, o.y + f * y.y, o.z + f * y.z, o.w + f * y.w);
+    }
+  }
+  if (!join) return;
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+  o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  const int b = grp / A.Hk, h = grp % A.Hk * A.G + r / A.T, t = r % A.T;
+  if (__any_sync(0xffffffffu, !finite4(o))) scalar_row(A, b, h, t, o);
+  store_row4(A, b, h, t, lane, o);
+}
+
+template <int NR, bool SEL>
+cudaError_t launch_tiles(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeAttnArgs& a, const TrParts& w,
+                         int use_tma, cudaStream_t stream) {
+  const size_t smem = sizeof(TrSmem<NR>) + 1024;
+  static_assert(sizeof(TrSmem<NR>) + 1024 <= 232448, "shared memory of one CTA");
+  cudaError_t e =
+      cudaFuncSetAttribute(tree_attn_kernel<NR, SEL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(tree_attn_kernel<NR, SEL>, dim3((unsigned)(w.rbs * w.ranges)), dim3(TrSmem<NR>::kThreads), smem,
+                    stream, 1, kmap, vmap, a, w, use_tma);
+}
+
+template <int WPR>
+cudaError_t launch_join(const TreeAttnArgs& a, const TrParts& w, cudaStream_t stream) {
+  const int64_t rows = (int64_t)a.B * a.Hq * a.T, per = kTrJoinThreads / 32 / WPR;
+  return launch_pdl(tree_join_kernel<WPR>, dim3((unsigned)((rows + per - 1) / per)), dim3(kTrJoinThreads), 0, stream, 1,
+                    a, w);
 }
 
 }  // namespace
 
 size_t tree_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t T, int64_t Hk, int64_t N) {
-  (void)B; (void)Hq; (void)T; (void)Hk; (void)N;
-  return 0;
+  (void)N;
+  const size_t plain = tree_layout(B, Hq, T, Hk, false).bytes(), sel = tree_layout(B, Hq, T, Hk, true).bytes();
+  return plain > sel ? plain : sel;
 }
 
 cudaError_t launch_tree_attn(const TreeAttnArgs& a, cudaStream_t stream) {
   if ((int64_t)a.B * a.Hq * a.T == 0) return cudaSuccess;
-  tree_attn_kernel<<<dim3((unsigned)a.T, (unsigned)(a.B * a.Hq)), kTrThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  const TrLayout L = tree_layout(a.B, a.Hq, a.T, a.Hk, a.sel != nullptr);
+  TrParts w;
+  char* ws = static_cast<char*>(a.ws);
+  w.table = reinterpret_cast<int2*>(ws);
+  w.o = reinterpret_cast<float*>(ws + L.table);
+  w.ml = reinterpret_cast<float2*>(ws + L.table + L.o);
+  w.nr = L.nr;
+  w.rbs = L.rbs;
+  w.ranges = L.ranges;
+  // strides that the tensor map's encoder refuses (0 in a dim of several rows): every tile by cp.async
+  CUtensorMap kmap{}, vmap{};
+  const int use_tma = !a.sel && a.N >= kTrKeys && make_row_map(&kmap, a.k, a.B, a.Hk, a.N, kTrKeys) &&
+                      make_row_map(&vmap, a.v, a.B, a.Hk, a.N, kTrKeys);
+  const cudaError_t e = a.sel          ? launch_tiles<64, true>(kmap, vmap, a, w, 0, stream)
+                        : L.nr == 64 ? launch_tiles<64, false>(kmap, vmap, a, w, use_tma, stream)
+                                     : launch_tiles<128, false>(kmap, vmap, a, w, use_tma, stream);
+  if (e != cudaSuccess) return e;
+  // about this many pieces in a group: one warp per row takes four at a time
+  const int64_t pieces = L.ranges / ((int64_t)a.B * a.Hk) + 1;
+  if (pieces <= 4) return launch_join<1>(a, w, stream);
+  if (pieces <= 16) return launch_join<4>(a, w, stream);
+  return launch_join<8>(a, w, stream);
 }
 
 }  // namespace rtp
