@@ -19,18 +19,24 @@
 //   S^T = K Q^T      [128 keys x NR rows], A = K tile, B = Q, both K-major
 //   O^T += V^T P^T   [128 dims x NR rows], A = V tile, B = P, both MN-major
 // With the rows on M, 64 rows would waste half of every instruction.
+// P and its rounding error go into one product as 128 columns (hi | lo).
 //   softmax  a thread holds one key and 32 query rows.  Exponentials are taken
 //            against a reference per row that is not the running maximum but
 //            some earlier maximum: it is raised (to the maximum, by a reduction
 //            over the tile's keys) only when a logit exceeds it by 2^16, which
 //            one vote per tile finds out.  Any reference within that range
 //            gives the same fp32 precision, and a tile needs no reduction over
-//            keys at all.  P goes to shared memory as a bf16 hi + lo pair.
+//            keys at all.
 //   O        is summed in TMEM over an epoch of up to 8 tiles (the tensor core
 //            truncates, so a long sum would drift), then added to a second TMEM
 //            tile by fp32 adds; a raised reference also ends an epoch, and the
 //            second tile is rescaled on that occasion.
-// Warps: softmax (NR / 8), 4 loaders, 1 MMA issuer.  Interior tiles come by TMA
+//   streams  two groups of 8 softmax warps, each with its own S, P, O and
+//            references for 64 rows, so that one exponentiates while the other
+//            waits, loads or stores.  Up to 64 rows the streams take every other
+//            tile of the same rows and their sums meet at the end; above, each
+//            takes 64 of a CTA's 128 rows of every tile.
+// Warps: 2 x 8 softmax, 4 loaders, 1 MMA issuer.  Interior tiles come by TMA
 // (128-byte swizzle), tiles with rows to leave out (past the end, a ring's seam,
 // drafts, selected keys) by 16-byte cp.async into the same layout, with zeros in
 // the rows that hold no token.
@@ -64,44 +70,58 @@ constexpr float kTrSlack = 16.f;             // log2 units a logit may lie above
 constexpr float kTrNone = -3.0e38f;          // reference of a row that has attended nothing yet
 constexpr uint32_t kTrNoKey = 0x007fffffu;   // score_key(-inf)
 constexpr int kTrRound = 512;                // keys whose selection bits are read at a time
-constexpr int kTrQueue = 1024;               // >= 128 left over + one round
+constexpr int kTrQueue = 640;                // 128 left over + one round
 constexpr int kTrSms = 148;
-constexpr int kBarSoft = 1, kBarLoad = 2;    // named barriers
+constexpr int kTrStream = 64;                // query rows of a stream
+constexpr int kTrSoft = 256;                 // threads of a stream
+constexpr int kTrLoad = kTrLoadWarps * 32;
+constexpr int kTrThreads = 2 * kTrSoft + kTrLoad + 128;  // (whole warpgroups; one warp issues the MMAs)
+constexpr int kTrRing = 8;                   // tiles (and segments) described ahead
+// registers per thread of each role; the launch's threads x registers hold them all
+constexpr int kTrLaunchRegs = 80, kTrSoftRegs = 96, kTrLoadRegs = 56, kTrMmaRegs = 40;
+static_assert(2 * kTrSoft * kTrSoftRegs + kTrLoad * kTrLoadRegs + 128 * kTrMmaRegs <= kTrThreads * kTrLaunchRegs,
+              "register split");
+constexpr int kBarLoad = 1, kBarStream = 2;  // named barriers (one per stream from kBarStream on)
+// TMEM columns of a stream: S, the epoch's O (hi | lo), the total O
+constexpr uint32_t kTmemStream = 256, kTmemOe = 64, kTmemOt = 192, kTmemCols = 512;
 
-// NR query rows per CTA.  64 rows leave room for two P tiles and the queue of selected keys.
+// What the softmax needs to know of a segment (a CTA's share of a group's tiles).
+struct TrSegInfo {
+  int b, kvh, n, lo, draft_tiles, max_depth;
+  int slot;   // where its partial result goes, or -1: the whole group
+  int pad;
+};
+
+// NR query rows per CTA: 64 (the streams take tiles in turn) or 128 (64 rows each).
 template <int NR>
 struct TrSmem {
-  static constexpr int kPBufs = NR == 64 ? 2 : 1;
-  static constexpr int kSoftWarps = NR / 8;
-  static constexpr int kThreads = (kSoftWarps + kTrLoadWarps + 4) * 32;  // (whole warpgroups: one warp issues the MMAs)
-  // registers per thread of each role; the launch's threads x registers hold them all
-  static constexpr int kSoftRegs = NR == 64 ? 168 : 96, kLoadRegs = NR == 64 ? 88 : 56, kMmaRegs = NR == 64 ? 88 : 40;
-  static constexpr int kLaunchRegs = NR == 64 ? 128 : 80;
-  static_assert(kSoftWarps * kSoftRegs + kTrLoadWarps * kLoadRegs + 4 * kMmaRegs <=
-                    (kSoftWarps + kTrLoadWarps + 4) * kLaunchRegs, "register split");
-  static constexpr int kQueue = NR == 64 ? kTrQueue : 1;
+  static constexpr int kQueue = NR == 64 ? kTrQueue : 1, kMasks = NR == 64 ? 4 : 1;
   alignas(1024) uint8_t q[NR * 256];
   alignas(1024) uint8_t k[kTrStages][kTrTile];
   alignas(1024) uint8_t v[kTrStages][kTrTile];
-  alignas(1024) uint8_t p[kPBufs][2][kTrKeys * NR * 2];  // hi, lo
-  alignas(16) float nref[NR];    // minus the reference of each row (log2 units)
-  alignas(16) float alpha[NR];   // 2^(old - new reference) of the last raise; a segment's row sums at its end
-  uint32_t colmax[NR];           // score_key of a tile's row maxima
-  uint64_t k_full[kTrStages], v_full[kTrStages], kv_empty[kTrStages];
-  uint64_t s_full[2], s_free[2], p_full[kPBufs], p_free[kPBufs];
-  uint64_t q_full, q_free, o_free, fin;
-  uint32_t bad[NR / 32];         // rows with a result that is not finite
-  int meta[kTrStages];           // tile number in the group, times two, plus 1 for the segment's last
+  alignas(1024) uint8_t p[2][2][kTrKeys * kTrStream * 2];  // [stream][hi, lo]
+  alignas(16) float nref[2][kTrStream];  // minus the reference of each row (log2 units)
+  // per row: a tile's maxima (as score_key), then 2^(old - new reference) of the last raise; at a segment's end
+  // the row sums
+  alignas(16) float alpha[2][kTrStream];
+  uint64_t k_full[kTrStages], k_empty[kTrStages], v_full[kTrStages], v_empty[kTrStages];
+  uint64_t s_full[2], s_free[2], p_full[2], p_free[2], o_free[2], sum_full[2], sum_free[2];
+  uint64_t q_full, q_free, fin;
+  uint32_t bad[2][2];            // rows with a result that is not finite
+  int2 meta[kTrRing];            // per tile: its number in the group; 4 * segment + 2 * (CTA's last) + (segment's last)
+  int cur[2];                    // tile of each stream's scores, or -1: no more
+  int end_seg;                   // segments of this CTA, once cur is -1
   int new_epoch[2];
-  int dead[2];
+  int state[2];                  // at a segment's end: 1 the stream has an O, 2 and a total
   uint32_t tmem_base;
-  unsigned long long total;
-  int64_t start_base;
   int start_b;
+  int64_t start_base;
+  unsigned long long total;
   int cnt[2][kTrLoadWarps];
+  TrSegInfo seg[kTrRing];
   int qkey[kQueue];              // selected keys waiting for a tile (ring)
   uint2 qbits[kQueue];           // and which rows selected them
-  uint32_t kmask[NR == 64 ? kTrStages : 1][2][NR == 64 ? kTrKeys : 1];  // row bits of the tile's keys
+  uint32_t kmask[kMasks][2][NR == 64 ? kTrKeys : 1];  // row bits of a tile's keys
 };
 
 // ---- small helpers --------------------------------------------------------------
@@ -154,6 +174,21 @@ RTP_DEVICE float reduce_columns(float (&x)[2 * O], int lane, F op) {
     return y[0];
   else
     return reduce_columns<O / 2>(y, lane, op);
+}
+
+// The same for 16 columns, left in lanes c and c + 16.
+template <typename F>
+RTP_DEVICE float reduce_columns16(float (&x)[16], int lane, F op) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = op(x[i], __shfl_xor_sync(0xffffffffu, x[i], 16));
+  return reduce_columns<8>(x, lane, op);
+}
+
+// 32 lanes x 8 consecutive columns.
+RTP_DEVICE void tmem_ld8(uint32_t taddr, float (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+               : "r"(taddr));
 }
 
 // ---- what a sequence's rows attend -------------------------------------------------
@@ -293,7 +328,7 @@ struct TrLayout {
 TrLayout tree_layout(int64_t B, int64_t Hq, int64_t T, int64_t Hk, bool sel) {
   TrLayout L;
   const int64_t rows = Hq / Hk * T;
-  // 128 rows read the keys once for 65 rows and more; 64 keep two P tiles in flight (and the queue of a selection)
+  // (a selection's queue and masks take the shared memory of the larger form)
   L.nr = sel || rows <= 64 ? 64 : 128;
   L.rbs = (int)((rows + L.nr - 1) / L.nr);
   L.ranges = L.rbs >= kTrSms ? 1 : kTrSms / L.rbs;
@@ -319,13 +354,11 @@ struct TrMaps {
 
 // ---- the kernel --------------------------------------------------------------------------
 template <int NR, bool SEL>
-__global__ void __launch_bounds__(TrSmem<NR>::kThreads, 1)
+__global__ void __launch_bounds__(kTrThreads, 1)
 tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                  const __grid_constant__ TreeAttnArgs A, const __grid_constant__ TrParts W, int use_tma) {
   using Smem = TrSmem<NR>;
-  constexpr int kSoft = Smem::kSoftWarps * 32, kLoad = kTrLoadWarps * 32;
-  constexpr int kPBufs = Smem::kPBufs;
-  constexpr uint32_t kTmemOe = 2 * NR, kTmemOt = 3 * NR, kTmemCols = 4 * NR;
+  constexpr bool kSplitRows = NR == 128;  // the streams share tiles (64 rows each), else they take tiles in turn
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   Smem& S = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -333,35 +366,31 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   const int rows = A.G * A.T, row0 = rb * NR, nrows = min(NR, rows - row0);
 
   if (tid == 0) {
-    for (int i = 0; i < kTrStages; ++i) {
-      mbar_init(&S.k_full[i], 1);
-      mbar_init(&S.v_full[i], 1);
-      mbar_init(&S.kv_empty[i], 1);
-      S.new_epoch[i] = 0;
-      S.dead[i] = 0;
-    }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&S.s_full[i], 1);
-      mbar_init(&S.s_free[i], Smem::kSoftWarps);
-    }
-    for (int i = 0; i < kPBufs; ++i) {
-      mbar_init(&S.p_full[i], Smem::kSoftWarps);
+      mbar_init(&S.k_full[i], 1);
+      mbar_init(&S.k_empty[i], 1);
+      mbar_init(&S.v_full[i], 1);
+      mbar_init(&S.v_empty[i], 1);
+      mbar_init(&S.s_full[i], 2);  // the products' commit, and the issuer (for S.cur)
+      mbar_init(&S.s_free[i], 8);
+      mbar_init(&S.p_full[i], 8);
       mbar_init(&S.p_free[i], 1);
+      mbar_init(&S.o_free[i], 8);
+      mbar_init(&S.sum_full[i], 8);
+      mbar_init(&S.sum_free[i], 8);
+      S.bad[i][0] = S.bad[i][1] = 0u;
     }
     mbar_init(&S.q_full, 1);
     mbar_init(&S.q_free, 1);
-    mbar_init(&S.o_free, Smem::kSoftWarps);
     mbar_init(&S.fin, 1);
     mbar_fence_init();
     S.total = 0;
   }
-  if (tid < NR) S.colmax[tid] = kTrNoKey;
-  if (tid < NR / 32) S.bad[tid] = 0u;
   if (warp == 0) tmem_alloc(&S.tmem_base, kTmemCols);
   // rows past the last one never get a P: zeros
   if (nrows < NR) {
     uint4* p = reinterpret_cast<uint4*>(&S.p[0][0][0]);
-    for (int i = tid; i < (int)(sizeof(S.p) / 16); i += Smem::kThreads) p[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = tid; i < (int)(sizeof(S.p) / 16); i += kTrThreads) p[i] = make_uint4(0u, 0u, 0u, 0u);
     fence_async();
   }
   pdl_wait();
@@ -371,7 +400,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   // ---- this CTA's range of the line of tiles ----
   {
     unsigned long long mine = 0;
-    for (int b = tid; b < A.B; b += Smem::kThreads) mine += (unsigned long long)span_of<SEL>(A, b).tiles;
+    for (int b = tid; b < A.B; b += kTrThreads) mine += (unsigned long long)span_of<SEL>(A, b).tiles;
     if (mine) atomicAdd(&S.total, mine);
   }
   tc_fence_before();
@@ -381,7 +410,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   const int64_t total = (int64_t)S.total * A.Hk;
   const int64_t per = (total + W.ranges - 1) / W.ranges;
   const int64_t lo = range * per, hi = min(lo + per, total);
-  if (lo < hi && warp == 0) {
+  const bool work = lo < hi;
+  if (work && warp == 0) {
     int64_t base = 0;
     for (int b0 = 0; b0 < A.B; b0 += 32) {
       const int64_t mine = b0 + lane < A.B ? (int64_t)span_of<SEL>(A, b0 + lane).tiles * A.Hk : 0;
@@ -405,75 +435,97 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   __syncthreads();
 
   bool alive = true;
-  TrWalk<SEL> walk;
-  bool more = lo < hi;
-  if (more) walk.start(A, lo, hi, S.start_b, S.start_base);
-  uint32_t it = 0;  // tiles of this CTA so far
 
-  if (warp >= Smem::kSoftWarps && warp < Smem::kSoftWarps + kTrLoadWarps) {
+  if (warp >= 2 * kTrSoft / 32 && warp < 2 * kTrSoft / 32 + kTrLoadWarps) {
     // ---------------- loaders ----------------
-    regs_dec<Smem::kLoadRegs>();
-    const int lt = tid - kSoft, lw = warp - Smem::kSoftWarps;
+    regs_dec<kTrLoadRegs>();
+    const int lt = tid - 2 * kTrSoft, lw = lt >> 5;
     const int chunk = lt & 15, r_first = lt >> 4;  // this thread's 16-byte column; rows r_first + 8 i
     // (8 rows on, the swizzle is the same)
     const uint32_t slot0 = (uint32_t)r_first * 128u + (uint32_t)(((chunk & 7) ^ r_first) << 4);
     const uint32_t slot_kv = slot0 + (uint32_t)(chunk >> 3) * (uint32_t)kTrHalf;
-    uint32_t segs = 0;
+    uint32_t it = 0;  // tiles so far
+    int segs = 0;
     bool q_due = false;
-    // Waits for a free stage; false (for all loaders alike) once any wait gave up.
-    auto stage_free = [&]() {
-      const bool ok = mbar_wait(&S.kv_empty[it & 1], ((it >> 1) & 1u) ^ 1u, alive, A.err, A.budget);
-      return !bar_or(kBarLoad, kLoad, !ok);
+    // Waits for a free K or V stage; false (for all loaders alike) once any wait gave up.
+    auto stage_free = [&](uint64_t* empty) {
+      const bool ok = mbar_wait(&empty[it & 1], ((it >> 1) & 1u) ^ 1u, alive, A.err, A.budget);
+      return !bar_or(kBarLoad, kTrLoad, !ok);
     };
-    // The tile's rows by cp.async: row_at(r, ok) gives the row of tile row r.
-    auto gather = [&](const View4& kv_k, const View4& kv_v, const TrSeg& s, int meta, auto&& row_at) {
-      const int st = it & 1;
-      const __nv_bfloat16* kb = static_cast<const __nv_bfloat16*>(kv_k.data) + s.b * kv_k.sb + s.kvh * kv_k.sh + chunk * 8;
-      const uint32_t ks = smem_addr(S.k[st]) + slot_kv;
-      const __nv_bfloat16* vb = static_cast<const __nv_bfloat16*>(kv_v.data) + s.b * kv_v.sb + s.kvh * kv_v.sh + chunk * 8;
-      const uint32_t vs = smem_addr(S.v[st]) + slot_kv;
-      int row[16];
-      uint32_t oks = 0;
-#pragma unroll
+    // 128 rows of K or V by cp.async: row_at(r, ok) gives the row of tile row r.
+    auto copy_rows = [&](const View4& x, uint8_t* tile, const TrSeg& s, auto&& row_at) {
+      const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(x.data) + s.b * x.sb + s.kvh * x.sh + chunk * 8;
+      const uint32_t dst = smem_addr(tile) + slot_kv;
+#pragma unroll 4
       for (int i = 0; i < 16; ++i) {
         bool ok;
-        row[i] = row_at(r_first + 8 * i, ok);
-        oks |= (uint32_t)ok << i;
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const bool ok = (oks >> i) & 1u;
-        cp16(ks + 1024u * i, ok ? (const void*)(kb + row[i] * kv_k.sn) : A.q.data, ok);
+        const int row = row_at(r_first + 8 * i, ok);
+        cp16(dst + 1024u * i, ok ? (const void*)(base + row * x.sn) : A.q.data, ok);
       }
       cp_commit();
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const bool ok = (oks >> i) & 1u;
-        cp16(vs + 1024u * i, ok ? (const void*)(vb + row[i] * kv_v.sn) : A.q.data, ok);
-      }
-      cp_commit();
-      if (lt == 0) S.meta[st] = meta;
-      cp_wait<1>();
+    };
+    auto landed = [&](uint64_t* full) {  // (after a cp_wait) every loader's copies are there
       fence_async();
-      named_sync(kBarLoad, kLoad);
+      named_sync(kBarLoad, kTrLoad);
       if (lt == 0) {
         if (q_due) mbar_arrive(&S.q_full);
-        mbar_arrive(&S.k_full[st]);
+        if (full) mbar_arrive(full);
       }
       q_due = false;
-      cp_wait<0>();
-      fence_async();
-      named_sync(kBarLoad, kLoad);
-      if (lt == 0) mbar_arrive(&S.v_full[st]);
-      ++it;
     };
-    bool ok = true;
-    for (; more && ok; more = walk.next(A)) {
-      const TrSeg& s = walk.s;
+    auto gather = [&](const View4& xk, const View4& xv, const TrSeg& s, int u, int flags, auto&& row_at) -> bool {
+      const int st = it & 1;
+      if (!stage_free(S.k_empty)) return false;
+      if (lt == 0) S.meta[it % kTrRing] = make_int2(u, flags);
+      copy_rows(xk, S.k[st], s, row_at);
+      const bool now = !bar_or(kBarLoad, kTrLoad, !mbar_try(&S.v_empty[st], ((it >> 1) & 1u) ^ 1u));
+      if (now) {
+        copy_rows(xv, S.v[st], s, row_at);
+        cp_wait<1>();
+        landed(&S.k_full[st]);
+      } else {
+        cp_wait<0>();
+        landed(&S.k_full[st]);
+        if (!stage_free(S.v_empty)) return false;
+        copy_rows(xv, S.v[st], s, row_at);
+      }
+      cp_wait<0>();
+      landed(&S.v_full[st]);
+      ++it;
+      return true;
+    };
+    TrWalk<SEL> walk;
+    bool more = work, ok = true;
+    if (more) walk.start(A, lo, hi, S.start_b, S.start_base);
+    while (more && ok) {
+      const TrSeg s = walk.s;
+      more = walk.next(A);
+      const int seg_flags = 4 * segs, last_flags = seg_flags + 1 + (more ? 0 : 2);
+      {
+        TrSegInfo info;
+        info.b = s.b;
+        info.kvh = s.kvh;
+        info.n = s.span.n;
+        info.lo = s.span.lo;
+        info.draft_tiles = s.span.draft_tiles;
+        info.max_depth = 0;
+        if (A.W > 0) {
+          for (int t = lane; t < A.T; t += 32) info.max_depth = max(info.max_depth, draft_depth(A, s.b, t));
+          info.max_depth = __reduce_max_sync(0xffffffffu, info.max_depth);
+        }
+        const bool whole = s.u0 == 0 && s.u1 == s.span.tiles;
+        info.slot = whole ? -1 : rb * 2 * W.ranges + 2 * range + (s.u0 == 0 ? 1 : 0);
+        info.pad = 0;
+        if (lt == 0) {
+          S.seg[segs % kTrRing] = info;
+          if (s.u0 == 0 && rb == 0)
+            W.table[s.b * A.Hk + s.kvh] = make_int2(range, (int)((s.base + s.span.tiles - 1) / per) - range + 1);
+        }
+      }
       // ---- the query rows (the previous segment's products are done with the buffer) ----
       {
         const bool free = segs == 0 || mbar_wait(&S.q_free, (segs - 1) & 1u, alive, A.err, A.budget);
-        if (bar_or(kBarLoad, kLoad, !free)) break;
+        if (bar_or(kBarLoad, kTrLoad, !free)) break;
         const __nv_bfloat16* qb =
             static_cast<const __nv_bfloat16*>(A.q.data) + s.b * A.q.sb + (int64_t)s.kvh * A.G * A.q.sh + chunk * 8;
 #pragma unroll 4
@@ -488,43 +540,41 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         ++segs;
       }
       const int drafts_end = min(s.u1, s.span.draft_tiles);
-      for (int u = s.u0; u < drafts_end; ++u) {
-        if (!(ok = stage_free())) break;
-        gather(A.kn, A.vn, s, 2 * u + (u + 1 == s.u1), [&](int r, bool& live) {
+      for (int u = s.u0; u < drafts_end && ok; ++u)
+        ok = gather(A.kn, A.vn, s, u, u + 1 == s.u1 ? last_flags : seg_flags, [&](int r, bool& live) {
           const int j = u * kTrKeys + r;
           live = j < A.T;
           return live ? j : 0;
         });
-      }
-      if (!ok) break;
+      if (!ok || s.u1 <= s.span.draft_tiles) continue;
       if constexpr (!SEL) {
-        for (int u = max(s.u0, s.span.draft_tiles); u < s.u1; ++u) {
-          if (!(ok = stage_free())) break;
+        for (int u = max(s.u0, s.span.draft_tiles); u < s.u1 && ok; ++u) {
           const uint32_t p0 = (uint32_t)s.span.lo + (uint32_t)(u - s.span.draft_tiles) * kTrKeys;
           const int left = s.span.n - (int)p0;  // committed rows from here on
           const int first = row_of(A, p0);
-          const int meta = 2 * u + (u + 1 == s.u1);
+          const int flags = u + 1 == s.u1 ? last_flags : seg_flags;
           if (use_tma && left >= kTrKeys && A.N - first >= kTrKeys) {
             const int st = it & 1;
+            if (!(ok = stage_free(S.k_empty))) break;
             if (lt == 0) {
-              S.meta[st] = meta;
+              S.meta[it % kTrRing] = make_int2(u, flags);
               mbar_expect_tx(&S.k_full[st], kTrTile);
               tma_load_4d(S.k[st], &kmap, &S.k_full[st], 0, first, s.kvh, s.b);
               tma_load_4d(S.k[st] + kTrHalf, &kmap, &S.k_full[st], 64, first, s.kvh, s.b);
+            }
+            if (q_due) {
+              cp_wait<0>();
+              landed(nullptr);
+            }
+            if (!(ok = stage_free(S.v_empty))) break;
+            if (lt == 0) {
               mbar_expect_tx(&S.v_full[st], kTrTile);
               tma_load_4d(S.v[st], &vmap, &S.v_full[st], 0, first, s.kvh, s.b);
               tma_load_4d(S.v[st] + kTrHalf, &vmap, &S.v_full[st], 64, first, s.kvh, s.b);
             }
-            if (q_due) {
-              cp_wait<0>();
-              fence_async();
-              named_sync(kBarLoad, kLoad);
-              if (lt == 0) mbar_arrive(&S.q_full);
-              q_due = false;
-            }
             ++it;
           } else {
-            gather(A.k, A.v, s, meta, [&](int r, bool& live) {
+            ok = gather(A.k, A.v, s, u, flags, [&](int r, bool& live) {
               live = r < left;
               return live ? row_of(A, p0 + (uint32_t)r) : 0;
             });
@@ -532,8 +582,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         }
       } else {
         const int rounds = s.span.tiles - s.span.draft_tiles;
-        if (s.u1 <= s.span.draft_tiles) continue;
         int head = 0, count = 0, turn = 0;
+        auto wrap = [](int i) { return i >= kTrQueue ? i - kTrQueue : i; };
         // this lane's rows: their mask rows, and the first key position their window admits
         const uint32_t* words[2];
         int from[2];
@@ -550,19 +600,18 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
             }
           }
         }
-        auto emit = [&](int take, bool last) {
-          const int st = it & 1;
+        auto emit = [&](int take, int flags) {
           // one key per loader thread: its row bits for the softmax
           uint2 bits = make_uint2(0u, 0u);
-          if (lt < take) bits = S.qbits[(head + lt) & (kTrQueue - 1)];
-          S.kmask[st][0][lt] = bits.x;
-          S.kmask[st][1][lt] = bits.y;
+          if (lt < take) bits = S.qbits[wrap(head + lt)];
+          S.kmask[it & 3][0][lt] = bits.x;
+          S.kmask[it & 3][1][lt] = bits.y;
           const int at = head;
-          gather(A.k, A.v, s, 2 * s.span.draft_tiles + last, [&](int r, bool& live) {
+          ok = gather(A.k, A.v, s, s.span.draft_tiles, flags, [&](int r, bool& live) {
             live = r < take;
-            return live ? S.qkey[(at + r) & (kTrQueue - 1)] : 0;
+            return live ? S.qkey[wrap(at + r)] : 0;
           });
-          head = (head + take) & (kTrQueue - 1);
+          head = wrap(head + take);
           count -= take;
         };
         for (int u = max(s.u0, s.span.draft_tiles); u < s.u1 && ok; ++u) {
@@ -592,7 +641,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
             mine += __popc(uni[w]);
           }
           if (lane == 0) S.cnt[turn & 1][lw] = mine;
-          named_sync(kBarLoad, kLoad);
+          named_sync(kBarLoad, kTrLoad);
           int before = 0, all = 0;
 #pragma unroll
           for (int w = 0; w < kTrLoadWarps; ++w) {
@@ -601,7 +650,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
             all += c;
           }
           ++turn;
-          int at = head + count + before;
+          int at = wrap(head + count + before);  // (head, count <= 128 and before < 512: one wrap at most)
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             uint32_t left = uni[w];
@@ -611,19 +660,18 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
               const uint32_t b0 = __ballot_sync(0xffffffffu, (x[0][w] >> bit) & 1u);
               const uint32_t b1 = __ballot_sync(0xffffffffu, (x[1][w] >> bit) & 1u);
               if (lane == 0) {
-                S.qkey[at & (kTrQueue - 1)] = key0 + 32 * w + bit;
-                S.qbits[at & (kTrQueue - 1)] = make_uint2(b0, b1);
+                S.qkey[at] = key0 + 32 * w + bit;
+                S.qbits[at] = make_uint2(b0, b1);
               }
-              ++at;
+              at = wrap(at + 1);
             }
           }
           count += all;
-          named_sync(kBarLoad, kLoad);
-          while (count > kTrKeys && (ok = stage_free())) emit(kTrKeys, false);
+          named_sync(kBarLoad, kTrLoad);
+          while (count > kTrKeys && ok) emit(kTrKeys, seg_flags);
         }
-        if (ok && (ok = stage_free())) emit(count, true);
+        if (ok) emit(count, last_flags);
       }
-      if (!ok) break;
     }
     cp_wait<0>();
     if (lt == 0)  // copies still in flight land before the CTA ends
@@ -631,335 +679,392 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         mbar_drain(&S.k_full[i & 1], (i >> 1) & 1u, A.err);
         mbar_drain(&S.v_full[i & 1], (i >> 1) & 1u, A.err);
       }
-  } else if (warp >= Smem::kSoftWarps + kTrLoadWarps) {
+  } else if (warp >= 2 * kTrSoft / 32 + kTrLoadWarps) {
     // ---------------- MMA issuer (one elected lane) ----------------
-    regs_dec<Smem::kMmaRegs>();
-    if (warp == Smem::kSoftWarps + kTrLoadWarps && lane == 0 && more) {
-      constexpr uint32_t idesc_s = umma_idesc_bf16_f32(kTrKeys, NR);
-      constexpr uint32_t idesc_o = umma_idesc_bf16_f32(kHeadDim, NR) | (1u << 15) | (1u << 16);  // both MN-major
-      uint32_t epochs = 0, segs = 0;
+    regs_dec<kTrMmaRegs>();
+    if (warp == 2 * kTrSoft / 32 + kTrLoadWarps && lane == 0 && work) {
+      constexpr uint32_t idesc_s = umma_idesc_bf16_f32(kTrKeys, kTrStream);
+      constexpr uint32_t idesc_o = umma_idesc_bf16_f32(kHeadDim, 2 * kTrStream) | (1u << 15) | (1u << 16);  // MN-major
       auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity & 1u, alive, A.err, A.budget); };
-      // O^T += V^T P^T of tile j
-      auto issue_pv = [&](uint32_t j) -> bool {
-        const int st = j & 1, pb = j % kPBufs;
-        if (!wait(&S.p_full[pb], j / kPBufs)) return false;
-        const bool fresh = S.new_epoch[st] != 0;
-        if (fresh) {
-          if (epochs > 0 && !wait(&S.o_free, epochs - 1)) return false;
-          ++epochs;
+      // Op o: the scores, later the product with V, of stream o % 2 and its tile.
+      auto tile_of = [](uint32_t o) { return kSplitRows ? o >> 1 : o; };
+      auto tile_done = [](uint32_t o) { return !kSplitRows || (o & 1u); };  // no later op of the other stream needs it
+      bool seg_start = true, end = false;
+      uint32_t segs = 0, epochs[2] = {0u, 0u};
+      auto issue_s = [&](uint32_t o) -> bool {
+        const uint32_t tile = tile_of(o), st = tile & 1, x = o & 1;
+        if (seg_start) {
+          if (!wait(&S.q_full, segs)) return false;
+          ++segs;
+          seg_start = false;
         }
-        if (!wait(&S.v_full[st], j >> 1)) return false;
+        if ((!kSplitRows || x == 0) && !wait(&S.k_full[st], tile >> 1)) return false;
+        if (!wait(&S.s_free[x], (o >> 1) ^ 1u)) return false;
         tc_fence_after();
-        const uint32_t va = smem_addr(S.v[st]), ph = smem_addr(S.p[pb][0]), pl = smem_addr(S.p[pb][1]);
+        const uint32_t ka = smem_addr(S.k[st]), qa = smem_addr(S.q) + (kSplitRows ? x * kTrStream * 128u : 0u);
 #pragma unroll
-        for (int kk = 0; kk < kTrKeys / 16; ++kk) {
-          const uint64_t a = umma_desc_sw128(va + (uint32_t)kk * 2048u, kTrHalf);
-          umma_f16(tmem + kTmemOe, a, umma_desc_sw128(ph + (uint32_t)kk * 2048u, kTrHalf), idesc_o,
-                   fresh && kk == 0 ? 0u : 1u);
-          umma_f16(tmem + kTmemOe, a, umma_desc_sw128(pl + (uint32_t)kk * 2048u, kTrHalf), idesc_o, 1u);
+        for (int kk = 0; kk < kHeadDim / 16; ++kk) {
+          const uint32_t h = (uint32_t)(kk >> 2), b = 32u * (uint32_t)(kk & 3);
+          umma_f16(tmem + x * kTmemStream, umma_desc_sw128(ka + h * kTrHalf + b, 16),
+                   umma_desc_sw128(qa + h * (NR * 128u) + b, 16), idesc_s, kk > 0 ? 1u : 0u);
         }
-        umma_commit(&S.kv_empty[st]);
-        umma_commit(&S.p_free[pb]);
+        umma_commit(&S.s_full[x]);
+        S.cur[x] = (int)tile;
+        mbar_arrive(&S.s_full[x]);
+        if (tile_done(o)) {
+          umma_commit(&S.k_empty[st]);
+          const int flags = S.meta[tile % kTrRing].y;
+          if (flags & 1) {
+            umma_commit(&S.q_free);
+            seg_start = true;
+          }
+          if (flags & 2) {
+            end = true;
+            S.end_seg = (flags >> 2) + 1;
+          }
+        }
         return true;
       };
-      bool ok = true;
-      for (; more && ok; more = walk.next(A)) {
-        ok = wait(&S.q_full, segs++);
-        for (bool last = false, first = true; ok && !last; first = false) {
-          const int st = it & 1;
-          if (!(ok = wait(&S.k_full[st], it >> 1))) break;
-          last = S.meta[st] & 1;
-          if (!(ok = wait(&S.s_free[st], (it >> 1) ^ 1u))) break;
-          tc_fence_after();
-          const uint32_t ka = smem_addr(S.k[st]), qa = smem_addr(S.q);
-#pragma unroll
-          for (int kk = 0; kk < kHeadDim / 16; ++kk) {
-            const uint32_t h = (uint32_t)(kk >> 2), o = 32u * (uint32_t)(kk & 3);
-            umma_f16(tmem + (uint32_t)st * NR, umma_desc_sw128(ka + h * kTrHalf + o, 16),
-                     umma_desc_sw128(qa + h * (NR * 128u) + o, 16), idesc_s, kk > 0 ? 1u : 0u);
-          }
-          umma_commit(&S.s_full[st]);
-          if (last) umma_commit(&S.q_free);
-          ++it;
-          if (!first) ok = issue_pv(it - 2);
+      auto issue_pv = [&](uint32_t o) -> bool {
+        const uint32_t tile = tile_of(o), st = tile & 1, x = o & 1;
+        if (!wait(&S.p_full[x], o >> 1)) return false;
+        const bool fresh = S.new_epoch[x] != 0;
+        uint32_t& ep = x ? epochs[1] : epochs[0];
+        if (fresh) {
+          if (ep > 0 && !wait(&S.o_free[x], ep - 1)) return false;
+          ++ep;
         }
-        if (ok) ok = issue_pv(it - 1);
+        if (!wait(&S.v_full[st], tile >> 1)) return false;
+        tc_fence_after();
+        const uint32_t va = smem_addr(S.v[st]), pa = smem_addr(S.p[x][0]);
+#pragma unroll
+        for (int kk = 0; kk < kTrKeys / 16; ++kk)
+          umma_f16(tmem + x * kTmemStream + kTmemOe, umma_desc_sw128(va + (uint32_t)kk * 2048u, kTrHalf),
+                   umma_desc_sw128(pa + (uint32_t)kk * 2048u, kTrHalf), idesc_o, fresh && kk == 0 ? 0u : 1u);
+        if (tile_done(o)) umma_commit(&S.v_empty[st]);
+        umma_commit(&S.p_free[x]);
+        return true;
+      };
+      // After the last op one more for each stream, that tells it so: the other may be waiting for its sums.
+      auto issue_end = [&](uint32_t o) -> bool {
+        const uint32_t x = o & 1;
+        if (!wait(&S.s_free[x], (o >> 1) ^ 1u)) return false;
+        S.cur[x] = -1;
+        mbar_arrive(&S.s_full[x]);
+        mbar_arrive(&S.s_full[x]);
+        return true;
+      };
+      // the scores of op o + 2 (the stream has read those of op o) before the product of op o
+      uint32_t so = 0, po = 0, ops = 0;
+      bool ok = true;
+      for (; ok && !(end && po == ops && so == ops + 2); ++po) {
+        for (; ok && so < po + 3 && !(end && so == ops + 2); ++so) {
+          if (end) {
+            ok = issue_end(so);
+          } else {
+            ok = issue_s(so);
+            if (end) ops = so + 1;
+          }
+        }
+        if (ok && !(end && po >= ops)) ok = issue_pv(po);
       }
       umma_commit(&S.fin);  // every product issued is done before TMEM is freed
       mbar_drain(&S.fin, 0, A.err);
     }
   } else {
     // ---------------- softmax, output ----------------
-    regs_inc<Smem::kSoftRegs>();
-    const int quad = warp & 3, col0 = 32 * (warp >> 2);  // this thread: key (then dim) 32 quad + lane, rows col0 ..
-    const int key = 32 * quad + lane;
-    const int act = max(0, min(2, (nrows - col0 + 15) / 16));  // its 16-row halves that hold rows
-    const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)col0;
+    regs_inc<kTrSoftRegs>();
+    const int x = tid / kTrSoft;                                 // stream
+    const int quad = warp & 3, col0 = 32 * ((warp >> 2) & 1);    // this thread: key (then dim) 32 quad + lane, rows col0 ..
+    const int key = 32 * quad + lane, bar = kBarStream + x;
+    const int row_base = row0 + (kSplitRows ? kTrStream * x : 0);
+    const int srows = max(0, min(kTrStream, rows - row_base));   // rows of the stream
+    const int act = max(0, min(2, (srows - col0 + 15) / 16));    // this thread's 16-row halves that hold rows
+    const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
+    const uint32_t my_base = lane_base + (uint32_t)x * kTmemStream + (uint32_t)col0;
+    const int t_first = (row_base + col0) % A.T;
+    float* alpha = S.alpha[x];
+    uint32_t* colmax = reinterpret_cast<uint32_t*>(alpha);
     uint64_t scale2;
     asm("mov.b64 %0, {%1, %1};\n" : "=l"(scale2) : "f"(A.scale_log2));
-    const int g_first = (row0 + col0) / A.T, t_first = (row0 + col0) - g_first * A.T;
-    bool ok = true;
-    for (; more && ok; more = walk.next(A)) {
-      const TrSeg& s = walk.s;
-      int max_depth = 0;
-      if (A.W > 0) {
-        for (int t = lane; t < A.T; t += 32) max_depth = max(max_depth, draft_depth(A, s.b, t));
-        max_depth = __reduce_max_sync(0xffffffffu, max_depth);
-      }
-      float l[32];
-#pragma unroll
-      for (int c = 0; c < 32; ++c) l[c] = 0.f;
-      bool first = true, has_total = false;
-      int in_epoch = 0;
-      for (bool last = false; !last;) {
-        const int st = it & 1, pb = it % kPBufs;
-        bool live = mbar_wait(&S.k_full[st], (it >> 1) & 1u, alive, A.err, A.budget) &&
-                    mbar_wait(&S.s_full[st], (it >> 1) & 1u, alive, A.err, A.budget);
-        live = __all_sync(0xffffffffu, live);
-        if (!live) {
-          alive = false;
-          S.dead[st] = 1;
-        }
-        tc_fence_after();
-        const int u = S.meta[st] >> 1;
-        last = S.meta[st] & 1;
+    auto wait_warp = [&](uint64_t* b, uint32_t parity) {
+      if (!__all_sync(0xffffffffu, mbar_wait(b, parity & 1u, alive, A.err, A.budget))) alive = false;
+    };
+    auto arrive_warp = [&](uint64_t* b) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b);
+    };
 
-        // ---- which of this thread's rows attend its key ----
-        uint32_t mw = ~0u;
-        if (u < s.span.draft_tiles) {
-          const int j = u * kTrKeys + key;
-          mw = 0u;
-          if (u * kTrKeys + 32 * quad < A.T) {
-            const int dj = j < A.T ? draft_depth(A, s.b, j) : 0;
-            int t = t_first;
-            for (int c = 0; c < 32 && col0 + c < nrows; ++c) {
-              const bool in = j < A.T && tree_bit(A, s.b, t, j) && (A.W <= 0 || dj > draft_depth(A, s.b, t) - A.W);
-              mw |= (uint32_t)in << c;
-              if (++t == A.T) t = 0;
-            }
-          }
-        } else if constexpr (SEL) {
-          mw = S.kmask[st][col0 >> 5][key];
-        } else {
-          const uint32_t p0 = (uint32_t)s.span.lo + (uint32_t)(u - s.span.draft_tiles) * kTrKeys;
-          const int age = s.span.n - 1 - (int)(p0 + (uint32_t)key);  // (below 0: past the end)
-          if (age < 0) mw = 0u;
-          if (A.W > 0 && s.span.n - 1 - (int)p0 > oldest_age(A, max_depth)) {
-            int t = t_first;
-            uint32_t in = 0u;
-            for (int c = 0; c < 32 && col0 + c < nrows; ++c) {
-              in |= (uint32_t)(age <= oldest_age(A, draft_depth(A, s.b, t))) << c;
-              if (++t == A.T) t = 0;
-            }
-            mw &= in;
-          }
-        }
-
-        // ---- logits less the reference (log2 units) ----
-        float d[32];
-        auto scores = [&](bool relative) {
+    float l[32];
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            if (hh >= act) continue;
-            uint32_t v[16];
-            tmem_ld16(lane_base + (uint32_t)st * NR + 16u * hh, v);
+    for (int c = 0; c < 32; ++c) l[c] = 0.f;
+    int seg = 0;                         // current segment
+    bool has = false, has_total = false;  // the stream has taken a tile of it; its epochs have a total
+    int in_epoch = 0;
+    uint32_t n = 0;  // ops of this stream so far
+    while (work) {
+      wait_warp(&S.s_full[x], n);
+      if (bar_or(bar, kTrSoft, !alive)) break;
+      const int tile = S.cur[x];
+      const int2 meta = tile >= 0 ? S.meta[tile % kTrRing] : make_int2(0, 4 * S.end_seg);
+
+      // ---- segments that ended before this tile: row sums over all keys, then O ----
+      for (; seg < (meta.y >> 2); ++seg) {
+        const TrSegInfo& info = S.seg[seg % kTrRing];
+        if (has) {
+          wait_warp(&S.p_free[x], n - 1);
+          tc_fence_after();
+        }
+        const float lsum = reduce_columns<16>(l, lane, [](float a, float b) { return a + b; });
+#pragma unroll
+        for (int c = 0; c < 32; ++c) l[c] = 0.f;
+        named_sync(bar, kTrSoft);       // (every warp is done with the last raise's factors)
+        for (int w = 0; w < 4; ++w) {   // the four warps of these rows, in order
+          if (quad == w) alpha[col0 + lane] = w == 0 ? lsum : alpha[col0 + lane] + lsum;
+          named_sync(bar, kTrSoft);
+        }
+        if constexpr (!kSplitRows) {  // the other stream's sums
+          if (tid % kTrSoft < kTrStream && !has) S.nref[x][tid % kTrSoft] = -kTrNone;
+          if (tid % kTrSoft == 0) S.state[x] = (has ? 1 : 0) + (has_total ? 2 : 0);
+          tc_fence_before();
+          named_sync(bar, kTrSoft);
+          arrive_warp(&S.sum_full[x]);
+          wait_warp(&S.sum_full[x ^ 1], (uint32_t)seg);
+          tc_fence_after();
+        }
+        // eight rows at a time: all 32 of this thread's, or 16 when the streams share them
+        const int c_first = kSplitRows ? col0 : col0 + 16 * x;
+        uint32_t bad = 0u;
+#pragma unroll 1
+        for (int c0 = c_first; c0 < c_first + (kSplitRows ? 32 : 16) && c0 < srows; c0 += 8) {
+          float y[8], m[8], sum[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            y[i] = sum[i] = 0.f;
+            m[i] = kSplitRows ? -S.nref[x][c0 + i] : fmaxf(-S.nref[0][c0 + i], -S.nref[1][c0 + i]);
+          }
+#pragma unroll 1
+          for (int src = kSplitRows ? x : 0; src < (kSplitRows ? x + 1 : 2); ++src) {
+            const int state = kSplitRows ? 1 + (has_total ? 2 : 0) : S.state[src];
+            if (!(state & 1)) continue;
+            const uint32_t at = lane_base + (uint32_t)src * kTmemStream + (uint32_t)c0;
+            float e[8], r[8];
+            tmem_ld8(at + kTmemOe, e);
+            tmem_ld8(at + kTmemOe + kTrStream, r);
             tmem_ld_wait();
-            const ulonglong2* nr = reinterpret_cast<const ulonglong2*>(S.nref + col0 + 16 * hh);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int c = 16 * hh + 4 * i;
-              const ulonglong2 r = relative ? nr[i] : make_ulonglong2(0ull, 0ull);
-              fma2c(v[4 * i], v[4 * i + 1], scale2, r.x, d[c], d[c + 1]);
-              fma2c(v[4 * i + 2], v[4 * i + 3], scale2, r.y, d[c + 2], d[c + 3]);
+            for (int i = 0; i < 8; ++i) e[i] += r[i];
+            if (state & 2) {
+              tmem_ld8(at + kTmemOt, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 8; ++i) e[i] += r[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float f = kSplitRows ? 1.f : ex2a(-S.nref[src][c0 + i] - m[i]);
+              y[i] = kSplitRows ? e[i] : __fmaf_rn(e[i], f, y[i]);
+              sum[i] = kSplitRows ? S.alpha[src][c0 + i] : __fmaf_rn(S.alpha[src][c0 + i], f, sum[i]);
             }
           }
-          if (mw != ~0u) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) d[c] = (mw >> c) & 1u ? d[c] : -INFINITY;
-          }
-        };
-        float top = -INFINITY;
-        if (!first && act > 0) {
-          scores(true);
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            if (hh >= act) continue;
-#pragma unroll
-            for (int c = 16 * hh; c < 16 * hh + 16; c += 2) top = max3f(top, d[c], d[c + 1]);
-          }
-        }
-        const bool raise = bar_or(kBarSoft, kSoft, first || top > kTrSlack);
-        if (S.dead[st]) {
-          ok = false;
-          break;
-        }
-        if (raise) {
-          // the tile's maximum of every row, over its keys
-          if (act > 0) {
-#pragma unroll
-            for (int c = 0; c < 32; ++c) d[c] = -INFINITY;
-            scores(false);
-            const float m = reduce_columns<16>(d, lane, [](float a, float b) { return fmaxf(a, b); });
-            atomicMax(&S.colmax[col0 + lane], score_key(m));
-          }
-          named_sync(kBarSoft, kSoft);
-          if (tid < NR) {
-            const float old = first ? kTrNone : -S.nref[tid];
-            const float now = fmaxf(old, key_score(S.colmax[tid]));
-            S.nref[tid] = -now;
-            S.alpha[tid] = ex2a(old - now);
-            S.colmax[tid] = kTrNoKey;
-          }
-          named_sync(kBarSoft, kSoft);
-          if (act > 0) scores(true);
-          if (!first) {
-#pragma unroll
-            for (int c = 0; c < 32; ++c) l[c] *= S.alpha[col0 + c];
+          for (int i = 0; i < 8; ++i) {
+            const int r = row_base + c0 + i;
+            if (c0 + i >= srows) continue;
+            if (info.slot < 0) {
+              const float o = y[i] * (sum[i] != 0.f ? 1.f / sum[i] : 0.f);
+              bad |= (uint32_t)!isfinite(o) << (c0 + i - c_first);
+              const int g = r / A.T, t = r - g * A.T;
+              const int64_t off = info.b * A.o.sb + (int64_t)(info.kvh * A.G + g) * A.o.sh + t * A.o.sn + key;
+              if (A.o_bf16)
+                static_cast<__nv_bfloat16*>(A.o.data)[off] = __float2bfloat16_rn(o);
+              else
+                static_cast<float*>(A.o.data)[off] = o;
+            } else {
+              const int64_t at = (int64_t)info.slot * NR + (r - row0);
+              W.o[at * kHeadDim + key] = y[i];
+              if (key == 0) W.ml[at] = make_float2(m[i], sum[i]);
+            }
           }
         }
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.s_free[st]);
+        if constexpr (!kSplitRows) {  // both streams are done with each other's sums
+          arrive_warp(&S.sum_free[x ^ 1]);
+          wait_warp(&S.sum_free[x], (uint32_t)seg);
+        }
+        if (has) arrive_warp(&S.o_free[x]);
+        if (info.slot < 0) {
+          bad = __reduce_or_sync(0xffffffffu, bad);
+          if (lane == 0 && bad) atomicOr(&S.bad[x][col0 >> 5], bad);
+          named_sync(bar, kTrSoft);
+          for (int i = warp & 7; i < 64; i += 8)
+            if ((S.bad[x][i >> 5] >> (i & 31)) & 1u) {
+              const int c = (kSplitRows ? 0 : 16 * x) + i, r = row_base + c, h = info.kvh * A.G + r / A.T;
+              float4 y;
+              scalar_row(A, info.b, h, r % A.T, y);
+              store_row4(A, info.b, h, r % A.T, lane, y);
+            }
+          named_sync(bar, kTrSoft);
+          if (tid % kTrSoft < 2) S.bad[x][tid % kTrSoft] = 0u;
+        }
+        has = has_total = false;
+        named_sync(bar, kTrSoft);  // (the stream's arrays are the next segment's from here on)
+      }
+      if (tile < 0) break;
 
-        // ---- P = 2^d as bf16 hi + lo, key-major rows of 64 query rows (128 bytes, swizzled) ----
-        uint32_t hi_w[16], lo_w[16];
+      // ---- which of this thread's rows attend its key ----
+      const TrSegInfo& info = S.seg[seg % kTrRing];
+      uint32_t mw = ~0u;
+      if (meta.x < info.draft_tiles) {
+        const int j = meta.x * kTrKeys + key;
+        mw = 0u;
+        if (meta.x * kTrKeys + 32 * quad < A.T) {
+          const int dj = j < A.T ? draft_depth(A, info.b, j) : 0;
+          int t = t_first;
+          for (int c = 0; c < 32 && col0 + c < srows; ++c) {
+            const bool in = j < A.T && tree_bit(A, info.b, t, j) && (A.W <= 0 || dj > draft_depth(A, info.b, t) - A.W);
+            mw |= (uint32_t)in << c;
+            if (++t == A.T) t = 0;
+          }
+        }
+      } else if constexpr (SEL) {
+        mw = S.kmask[tile & 3][col0 >> 5][key];
+      } else {
+        const uint32_t p0 = (uint32_t)info.lo + (uint32_t)(meta.x - info.draft_tiles) * kTrKeys;
+        const int age = info.n - 1 - (int)(p0 + (uint32_t)key);  // (below 0: past the end)
+        if (age < 0) mw = 0u;
+        if (A.W > 0 && info.n - 1 - (int)p0 > oldest_age(A, info.max_depth)) {
+          int t = t_first;
+          uint32_t in = 0u;
+          for (int c = 0; c < 32 && col0 + c < srows; ++c) {
+            in |= (uint32_t)(age <= oldest_age(A, draft_depth(A, info.b, t))) << c;
+            if (++t == A.T) t = 0;
+          }
+          mw &= in;
+        }
+      }
+
+      // ---- logits of 16 rows, less the reference if `relative` (log2 units); -inf where not attended ----
+      auto scores = [&](int hh, bool relative, float (&d)[16]) {
+        uint32_t v[16];
+        tmem_ld16(my_base + 16u * hh, v);
+        tmem_ld_wait();
+        const ulonglong2* nr = reinterpret_cast<const ulonglong2*>(S.nref[x] + col0 + 16 * hh);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const ulonglong2 r = relative ? nr[i] : make_ulonglong2(0ull, 0ull);
+          fma2c(v[4 * i], v[4 * i + 1], scale2, r.x, d[4 * i], d[4 * i + 1]);
+          fma2c(v[4 * i + 2], v[4 * i + 3], scale2, r.y, d[4 * i + 2], d[4 * i + 3]);
+        }
+        if (mw != ~0u) {
+          const uint32_t w = mw >> (16 * hh);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) d[c] = (w >> c) & 1u ? d[c] : -INFINITY;
+        }
+      };
+      tc_fence_after();
+      float top = -INFINITY;
+      if (has) {
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           if (hh >= act) continue;
+          float d[16];
+          scores(hh, true, d);
 #pragma unroll
-          for (int i = 8 * hh; i < 8 * hh + 8; ++i) {
-            const float p0 = ex2a(d[2 * i]), p1 = ex2a(d[2 * i + 1]);
-            add2(l[2 * i], l[2 * i + 1], p0, p1);
-            hi_w[i] = pack_bf16x2(p0, p1);
-            float r0, r1;
-            sub2p(p0, p1, bf16_lo(hi_w[i]), bf16_hi(hi_w[i]), r0, r1);
-            lo_w[i] = pack_bf16x2(r0, r1);
-          }
+          for (int c = 0; c < 16; c += 2) top = max3f(top, d[c], d[c + 1]);
         }
-        const uint32_t uses = it / kPBufs;  // of this P tile so far
-        if (!__all_sync(0xffffffffu, mbar_wait(&S.p_free[pb], (uses & 1u) ^ 1u, alive, A.err, A.budget))) alive = false;
-        {
-          const uint32_t off = (uint32_t)(col0 >> 6) * (uint32_t)kTrHalf + (uint32_t)key * 128u;
-          const int c8 = (col0 & 63) >> 3;  // first 16-byte chunk of these rows
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (i >= 2 * act) continue;
-            const uint32_t o = off + (uint32_t)(((c8 + i) ^ (key & 7)) << 4);
-            *reinterpret_cast<uint4*>(&S.p[pb][0][o]) =
-                make_uint4(hi_w[4 * i], hi_w[4 * i + 1], hi_w[4 * i + 2], hi_w[4 * i + 3]);
-            *reinterpret_cast<uint4*>(&S.p[pb][1][o]) =
-                make_uint4(lo_w[4 * i], lo_w[4 * i + 1], lo_w[4 * i + 2], lo_w[4 * i + 3]);
-          }
-        }
-        fence_async();
-        const bool fresh = raise || in_epoch == kTrEpoch;
-        if (tid == 0) S.new_epoch[st] = fresh;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.p_full[pb]);
-
-        // ---- the epoch before this tile joins the total ----
-        if (fresh && !first) {
-          const uint32_t j = it - 1;
-          if (!__all_sync(0xffffffffu, mbar_wait(&S.p_free[j % kPBufs], (j / kPBufs) & 1u, alive, A.err, A.budget)))
-            alive = false;
-          tc_fence_after();
+      }
+      const bool raise = bar_or(bar, kTrSoft, !has || top > kTrSlack);
+      if (raise) {
+        // the tile's maximum of every row, over its keys
+        if (tid % kTrSoft < kTrStream) colmax[tid % kTrSoft] = kTrNoKey;
+        named_sync(bar, kTrSoft);
 #pragma unroll 1
-          for (int hh = 0; hh < act; ++hh) {
-            uint32_t e[16], o[16];
-            tmem_ld16(lane_base + kTmemOe + 16u * hh, e);
-            if (has_total) tmem_ld16(lane_base + kTmemOt + 16u * hh, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              float y = __uint_as_float(e[c]);
-              if (has_total) y += __uint_as_float(o[c]);
-              if (raise) y *= S.alpha[col0 + 16 * hh + c];
-              o[c] = __float_as_uint(y);
-            }
-            tmem_st16(lane_base + kTmemOt + 16u * hh, o);
-          }
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&S.o_free);
-          has_total = true;
+        for (int hh = 0; hh < act; ++hh) {
+          float d[16];
+          scores(hh, false, d);
+          const float m = reduce_columns16(d, lane, [](float a, float b) { return fmaxf(a, b); });
+          if (lane < 16) atomicMax(&colmax[col0 + 16 * hh + lane], score_key(m));
         }
-        in_epoch = fresh ? 1 : in_epoch + 1;
-        first = false;
-        ++it;
-      }
-      if (!ok) break;
-
-      // ---- the segment's end: row sums over all keys, then O ----
-      {
-        const uint32_t j = it - 1;
-        if (!__all_sync(0xffffffffu, mbar_wait(&S.p_free[j % kPBufs], (j / kPBufs) & 1u, alive, A.err, A.budget)))
-          alive = false;
-        tc_fence_after();
-      }
-      const float lsum = reduce_columns<16>(l, lane, [](float a, float b) { return a + b; });
-      named_sync(kBarSoft, kSoft);  // (every warp is done with the last raise's factors)
-      for (int w = 0; w < 4; ++w) {   // the four warps of these rows, in order
-        if (quad == w) S.alpha[col0 + lane] = w == 0 ? lsum : S.alpha[col0 + lane] + lsum;
-        named_sync(kBarSoft, kSoft);
-      }
-      const bool whole = s.u0 == 0 && s.u1 == s.span.tiles;
-      const int grp = s.b * A.Hk + s.kvh;
-      const int64_t slot = (int64_t)rb * 2 * W.ranges + 2 * range + (s.u0 == 0 ? 1 : 0);
-      if (!whole && tid < nrows) W.ml[slot * NR + tid] = make_float2(-S.nref[tid], S.alpha[tid]);
-      if (s.u0 == 0 && rb == 0 && tid == 0)
-        W.table[grp] = make_int2(range, (int)((s.base + s.span.tiles - 1) / per) - range + 1);
-      uint32_t bad = 0u;
-      int g = g_first, t = t_first;
-#pragma unroll 1
-      for (int hh = 0; hh < act; ++hh) {
-        uint32_t e[16], o[16];
-        tmem_ld16(lane_base + kTmemOe + 16u * hh, e);
-        if (has_total) tmem_ld16(lane_base + kTmemOt + 16u * hh, o);
-        tmem_ld_wait();
+        named_sync(bar, kTrSoft);
+        if (tid % kTrSoft < kTrStream) {
+          const int c = tid % kTrSoft;
+          const float old = has ? -S.nref[x][c] : kTrNone;
+          const float now = fmaxf(old, key_score(colmax[c]));
+          S.nref[x][c] = -now;
+          alpha[c] = ex2a(old - now);
+        }
+        named_sync(bar, kTrSoft);
+        if (has) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int c = col0 + 16 * hh + i;
-          float y = __uint_as_float(e[i]);
-          if (has_total) y += __uint_as_float(o[i]);
-          if (c < nrows) {
-            if (whole) {
-              const float sum = S.alpha[c];
-              y *= sum != 0.f ? 1.f / sum : 0.f;
-              bad |= (uint32_t)!isfinite(y) << (16 * hh + i);
-              const int64_t off = s.b * A.o.sb + (int64_t)(s.kvh * A.G + g) * A.o.sh + t * A.o.sn + key;
-              if (A.o_bf16)
-                static_cast<__nv_bfloat16*>(A.o.data)[off] = __float2bfloat16_rn(y);
-              else
-                static_cast<float*>(A.o.data)[off] = y;
-            } else {
-              W.o[(slot * NR + c) * kHeadDim + key] = y;
-            }
-          }
-          if (++t == A.T) {
-            t = 0;
-            ++g;
-          }
+          for (int c = 0; c < 32; ++c) l[c] *= alpha[col0 + c];
+        }
+      }
+
+      // ---- P = 2^d as bf16 hi + lo, key-major rows of 64 query rows (128 bytes, swizzled) ----
+      wait_warp(&S.p_free[x], n ^ 1u);
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        if (hh >= act) continue;
+        float d[16];
+        scores(hh, true, d);
+        uint32_t hi_w[8], lo_w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float p0 = ex2a(d[2 * i]), p1 = ex2a(d[2 * i + 1]);
+          add2(l[16 * hh + 2 * i], l[16 * hh + 2 * i + 1], p0, p1);
+          hi_w[i] = pack_bf16x2(p0, p1);
+          float r0, r1;
+          sub2p(p0, p1, bf16_lo(hi_w[i]), bf16_hi(hi_w[i]), r0, r1);
+          lo_w[i] = pack_bf16x2(r0, r1);
+        }
+        const int c8 = (col0 + 16 * hh) >> 3;  // first 16-byte chunk of these rows
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t o = (uint32_t)key * 128u + (uint32_t)(((c8 + i) ^ (key & 7)) << 4);
+          *reinterpret_cast<uint4*>(&S.p[x][0][o]) =
+              make_uint4(hi_w[4 * i], hi_w[4 * i + 1], hi_w[4 * i + 2], hi_w[4 * i + 3]);
+          *reinterpret_cast<uint4*>(&S.p[x][1][o]) =
+              make_uint4(lo_w[4 * i], lo_w[4 * i + 1], lo_w[4 * i + 2], lo_w[4 * i + 3]);
         }
       }
       tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.o_free);
-      if (whole) {
-        bad = __reduce_or_sync(0xffffffffu, bad);
-        if (lane == 0 && bad) atomicOr(&S.bad[col0 >> 5], bad);
-        named_sync(kBarSoft, kSoft);
-        for (int c = warp; c < nrows; c += Smem::kSoftWarps)
-          if ((S.bad[c >> 5] >> (c & 31)) & 1u) {
-            const int r = row0 + c, h = s.kvh * A.G + r / A.T;
-            float4 y;
-            scalar_row(A, s.b, h, r % A.T, y);
-            store_row4(A, s.b, h, r % A.T, lane, y);
+      arrive_warp(&S.s_free[x]);
+      fence_async();
+      const bool fresh = raise || in_epoch == kTrEpoch;
+      if (tid % kTrSoft == 0) S.new_epoch[x] = fresh;
+      arrive_warp(&S.p_full[x]);
+
+      // ---- the epoch before this tile joins the total ----
+      if (fresh && has) {
+        tc_fence_after();  // (its last product is done: p_free above)
+#pragma unroll 1
+        for (int c0 = 0; c0 < 16 * act; c0 += 8) {
+          float e[8], r[8];
+          tmem_ld8(my_base + kTmemOe + c0, e);
+          tmem_ld8(my_base + kTmemOe + kTrStream + c0, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) e[i] += r[i];
+          if (has_total) {
+            tmem_ld8(my_base + kTmemOt + c0, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) e[i] += r[i];
           }
-        named_sync(kBarSoft, kSoft);
-        if (tid < NR / 32) S.bad[tid] = 0u;
+          uint32_t o[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(raise ? e[i] * alpha[col0 + c0 + i] : e[i]);
+          tmem_st8(my_base + kTmemOt + c0, o);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        arrive_warp(&S.o_free[x]);
+        has_total = true;
       }
-      named_sync(kBarSoft, kSoft);  // (S.alpha, S.nref and S.bad are the next segment's from here on)
+      in_epoch = fresh ? 1 : in_epoch + 1;
+      has = true;
+      ++n;
     }
   }
 
@@ -1054,8 +1159,8 @@ cudaError_t launch_tiles(const CUtensorMap& kmap, const CUtensorMap& vmap, const
   cudaError_t e =
       cudaFuncSetAttribute(tree_attn_kernel<NR, SEL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(tree_attn_kernel<NR, SEL>, dim3((unsigned)(w.rbs * w.ranges)), dim3(TrSmem<NR>::kThreads), smem,
-                    stream, 1, kmap, vmap, a, w, use_tma);
+  return launch_pdl(tree_attn_kernel<NR, SEL>, dim3((unsigned)(w.rbs * w.ranges)), dim3(kTrThreads), smem, stream, 1,
+                    kmap, vmap, a, w, use_tma);
 }
 
 template <int WPR>
