@@ -58,6 +58,18 @@ RTP_DEVICE bool mbar_try(uint64_t* bar, uint32_t parity) {
 #endif
   return ok != 0;
 }
+// Whether the phase has completed, without waiting.
+RTP_DEVICE bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // Wait for the phase with the given parity to complete; false on timeout
 // (the error word is set).  `budget` is the number of clock cycles the wait
 // may take (kWaitBudgetCycles unless the host set another budget).  Once any

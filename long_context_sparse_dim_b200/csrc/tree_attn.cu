@@ -21,16 +21,16 @@
 // With the rows on M, 64 rows would waste half of every instruction.
 // P and its rounding error go into one product as 128 columns (hi | lo).
 //   softmax  a thread holds one key and 32 query rows.  Exponentials are taken
-//            against a reference per row that is not the running maximum but
-//            some earlier maximum: it is raised (to the maximum, by a reduction
-//            over the tile's keys) only when a logit exceeds it by 2^16, which
-//            one vote per tile finds out.  Any reference within that range
-//            gives the same fp32 precision, and a tile needs no reduction over
-//            keys at all.
-//   O        is summed in TMEM over an epoch of up to 8 tiles (the tensor core
+//            against a reference per row that is not the running maximum: the
+//            maximum over the first tile's keys, attended or not, and raised
+//            every 8 tiles where the sums have grown past 2^16.  fp32 and bf16
+//            share their exponent range, so any reference within 2^60 above and
+//            2^100 below the row's maximum gives the same precision, and a tile
+//            needs no reduction over keys and no exchange between warps.  A row
+//            outside that range shows in its sum and goes the scalar way below.
+//   O        is summed in TMEM over an epoch of 8 tiles (the tensor core
 //            truncates, so a long sum would drift), then added to a second TMEM
-//            tile by fp32 adds; a raised reference also ends an epoch, and the
-//            second tile is rescaled on that occasion.
+//            tile by fp32 adds, and rescaled where references were raised.
 //   streams  two groups of 8 softmax warps, each with its own S, P, O and
 //            references for 64 rows, so that one exponentiates while the other
 //            waits, loads or stores.  Up to 64 rows the streams take every other
@@ -49,8 +49,9 @@
 // queues the keys that any row selected (a ballot per key transposes the bits:
 // the queue holds a key's row bits), and gathers only those, 128 to a tile.
 //
-// A row whose result is not finite is computed again by a scalar pass over the
-// keys it attends: 0 * inf in a product with P = 0 must not reach it.
+// A row whose result is not finite, or whose sum has left its range, is computed
+// again by a scalar pass over the keys it attends (0 * inf in a product with
+// P = 0 must not reach it).
 #include <math.h>
 
 #include "launch.h"
@@ -66,8 +67,9 @@ constexpr int kTrHalf = kTrKeys * 128;       // 128 rows x 64 bf16, 128-byte swi
 constexpr int kTrTile = 2 * kTrHalf;         // one K or V tile: 32 KB
 constexpr int kTrLoadWarps = 4;
 constexpr int kTrEpoch = 8;                  // tiles summed in TMEM before an fp32 add
-constexpr float kTrSlack = 16.f;             // log2 units a logit may lie above the reference
-constexpr float kTrNone = -3.0e38f;          // reference of a row that has attended nothing yet
+constexpr float kTrHigh = 65536.f;           // a sum above it raises the row's reference
+constexpr float kTrLow = 8.6736174e-19f;     // 2^-60: a sum below it has lost the row's largest terms
+constexpr float kTrNone = -3.0e38f;          // log2 of an empty sum
 constexpr uint32_t kTrNoKey = 0x007fffffu;   // score_key(-inf)
 constexpr int kTrRound = 512;                // keys whose selection bits are read at a time
 constexpr int kTrQueue = 640;                // 128 left over + one round
@@ -81,7 +83,7 @@ constexpr int kTrRing = 8;                   // tiles (and segments) described a
 constexpr int kTrLaunchRegs = 80, kTrSoftRegs = 96, kTrLoadRegs = 56, kTrMmaRegs = 40;
 static_assert(2 * kTrSoft * kTrSoftRegs + kTrLoad * kTrLoadRegs + 128 * kTrMmaRegs <= kTrThreads * kTrLaunchRegs,
               "register split");
-constexpr int kBarLoad = 1, kBarStream = 2;  // named barriers (one per stream from kBarStream on)
+constexpr int kBarLoad = 1;                  // named barrier
 // TMEM columns of a stream: S, the epoch's O (hi | lo), the total O
 constexpr uint32_t kTmemStream = 256, kTmemOe = 64, kTmemOt = 192, kTmemCols = 512;
 
@@ -101,17 +103,17 @@ struct TrSmem {
   alignas(1024) uint8_t v[kTrStages][kTrTile];
   alignas(1024) uint8_t p[2][2][kTrKeys * kTrStream * 2];  // [stream][hi, lo]
   alignas(16) float nref[2][kTrStream];  // minus the reference of each row (log2 units)
-  // per row: a tile's maxima (as score_key), then 2^(old - new reference) of the last raise; at a segment's end
-  // the row sums
-  alignas(16) float alpha[2][kTrStream];
+  alignas(16) float alpha[2][kTrStream];  // 2^(old - new reference) of the last raise; at a segment's end the row sums
+  uint32_t colmax[2][kTrStream];         // a tile's row maxima (as score_key), or the largest sums (float bits)
   uint64_t k_full[kTrStages], k_empty[kTrStages], v_full[kTrStages], v_empty[kTrStages];
-  uint64_t s_full[2], s_free[2], p_full[2], p_free[2], o_free[2], sum_full[2], sum_free[2];
+  uint64_t s_full[2], s_free[2], p_full[2], p_free[2], o_free[2], sum_full[2], sum_free[2], sync[2];
   uint64_t q_full, q_free, fin;
   uint32_t bad[2][2];            // rows with a result that is not finite
   int2 meta[kTrRing];            // per tile: its number in the group; 4 * segment + 2 * (CTA's last) + (segment's last)
-  int cur[2];                    // tile of each stream's scores, or -1: no more
-  int end_seg;                   // segments of this CTA, once cur is -1
+  int4 cur[2];                   // each stream's scores: tile (-1: no more), and its meta
   int new_epoch[2];
+  int raise[2][2];               // some sum has grown too large (alternating epochs)
+  uint32_t seen[2][2];           // rows that attend a key of the segment
   int state[2];                  // at a segment's end: 1 the stream has an O, 2 and a total
   uint32_t tmem_base;
   int start_b;
@@ -152,6 +154,24 @@ RTP_DEVICE bool bar_or(int id, int n, bool x) {
   return r != 0;
 }
 
+// Pairs of floats in one 64-bit word, and packed arithmetic on them.
+RTP_DEVICE uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+RTP_DEVICE void unpack2(uint64_t x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(x)); }
+RTP_DEVICE uint64_t add2u(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+RTP_DEVICE uint64_t sub2u(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("sub.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // (a * s + c.lo, b * s + c.hi), c a pair of floats in one 64-bit word.
 RTP_DEVICE void fma2c(uint32_t a, uint32_t b, uint64_t s, uint64_t c, float& ra, float& rb) {
   uint64_t x, r;
@@ -182,6 +202,17 @@ RTP_DEVICE float reduce_columns16(float (&x)[16], int lane, F op) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) x[i] = op(x[i], __shfl_xor_sync(0xffffffffu, x[i], 16));
   return reduce_columns<8>(x, lane, op);
+}
+
+// Waits for the loads that fill these registers (naming them keeps their uses behind it).
+RTP_DEVICE void tmem_wait(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
+RTP_DEVICE void tmem_wait(float (&r)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]));
 }
 
 // 32 lanes x 8 consecutive columns.
@@ -321,8 +352,8 @@ RTP_DEVICE bool finite4(const float4& y) {
 // ---- layout of the workspace -------------------------------------------------------------
 struct TrLayout {
   int nr, rbs, ranges;  // rows per CTA, row blocks per KV head, ranges of the line of tiles
-  size_t table, o, ml;  // byte sizes
-  size_t bytes() const { return table + o + ml; }
+  size_t table, o, lse;  // byte sizes
+  size_t bytes() const { return table + o + lse; }
 };
 
 TrLayout tree_layout(int64_t B, int64_t Hq, int64_t T, int64_t Hk, bool sel) {
@@ -336,7 +367,7 @@ TrLayout tree_layout(int64_t B, int64_t Hq, int64_t T, int64_t Hk, bool sel) {
   L.table = up((size_t)(B * Hk) * sizeof(int2));
   const size_t slots = (size_t)L.rbs * L.ranges * 2 * L.nr;
   L.o = up(slots * kHeadDim * sizeof(float));
-  L.ml = up(slots * sizeof(float2));
+  L.lse = up(slots * sizeof(float));
   return L;
 }
 
@@ -344,7 +375,7 @@ TrLayout tree_layout(int64_t B, int64_t Hq, int64_t T, int64_t Hk, bool sel) {
 struct TrParts {
   int2* table;  // [B * Hk] first range and number of pieces
   float* o;     // [row block][2 * ranges][nr][128]
-  float2* ml;   // [row block][2 * ranges][nr] reference (log2), sum
+  float* lse;   // [row block][2 * ranges][nr] log2 of the sum of 2^logit; o is normalised
   int nr, rbs, ranges;
 };
 
@@ -360,7 +391,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   using Smem = TrSmem<NR>;
   constexpr bool kSplitRows = NR == 128;  // the streams share tiles (64 rows each), else they take tiles in turn
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  Smem& S = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Smem& S = *reinterpret_cast<Smem*>(smem_raw);
+  if (smem_addr(smem_raw) % 1024u) {  // (the swizzle and the descriptors rest on the alignment declared above)
+    if (threadIdx.x == 0) atomicExch(A.err, kDevErrTimeout);
+    return;
+  }
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rb = blockIdx.x % W.rbs, range = blockIdx.x / W.rbs;
   const int rows = A.G * A.T, row0 = rb * NR, nrows = min(NR, rows - row0);
@@ -378,7 +413,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       mbar_init(&S.o_free[i], 8);
       mbar_init(&S.sum_full[i], 8);
       mbar_init(&S.sum_free[i], 8);
+      mbar_init(&S.sync[i], 8);
       S.bad[i][0] = S.bad[i][1] = 0u;
+      S.raise[i][0] = S.raise[i][1] = 0;
+      S.seen[i][0] = S.seen[i][1] = 0u;
     }
     mbar_init(&S.q_full, 1);
     mbar_init(&S.q_free, 1);
@@ -444,7 +482,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     // (8 rows on, the swizzle is the same)
     const uint32_t slot0 = (uint32_t)r_first * 128u + (uint32_t)(((chunk & 7) ^ r_first) << 4);
     const uint32_t slot_kv = slot0 + (uint32_t)(chunk >> 3) * (uint32_t)kTrHalf;
-    uint32_t it = 0;  // tiles so far
+    uint32_t it = 0, k_loads = 0;  // tiles so far; tiles whose K has been sent for
     int segs = 0;
     bool q_due = false;
     // Waits for a free K or V stage; false (for all loaders alike) once any wait gave up.
@@ -491,7 +529,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       }
       cp_wait<0>();
       landed(&S.v_full[st]);
-      ++it;
+      k_loads = ++it;
       return true;
     };
     TrWalk<SEL> walk;
@@ -548,33 +586,50 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         });
       if (!ok || s.u1 <= s.span.draft_tiles) continue;
       if constexpr (!SEL) {
+        auto by_tma = [&](int u, uint32_t& p0, int& left, int& first) {  // a whole tile of neighbouring rows
+          p0 = (uint32_t)s.span.lo + (uint32_t)(u - s.span.draft_tiles) * kTrKeys;
+          left = s.span.n - (int)p0;  // committed rows from here on
+          first = row_of(A, p0);
+          return use_tma && left >= kTrKeys && A.N - first >= kTrKeys;
+        };
+        auto load = [&](const CUtensorMap* map, uint8_t* tile, uint64_t* full, int first) {
+          mbar_expect_tx(full, kTrTile);
+          tma_load_4d(tile, map, full, 0, first, s.kvh, s.b);
+          tma_load_4d(tile + kTrHalf, map, full, 64, first, s.kvh, s.b);
+        };
+        bool ahead = false;  // this tile's K is already on its way
         for (int u = max(s.u0, s.span.draft_tiles); u < s.u1 && ok; ++u) {
-          const uint32_t p0 = (uint32_t)s.span.lo + (uint32_t)(u - s.span.draft_tiles) * kTrKeys;
-          const int left = s.span.n - (int)p0;  // committed rows from here on
-          const int first = row_of(A, p0);
-          const int flags = u + 1 == s.u1 ? last_flags : seg_flags;
-          if (use_tma && left >= kTrKeys && A.N - first >= kTrKeys) {
-            const int st = it & 1;
-            if (!(ok = stage_free(S.k_empty))) break;
-            if (lt == 0) {
-              S.meta[it % kTrRing] = make_int2(u, flags);
-              mbar_expect_tx(&S.k_full[st], kTrTile);
-              tma_load_4d(S.k[st], &kmap, &S.k_full[st], 0, first, s.kvh, s.b);
-              tma_load_4d(S.k[st] + kTrHalf, &kmap, &S.k_full[st], 64, first, s.kvh, s.b);
+          uint32_t p0;
+          int left, first;
+          const int st = it & 1;
+          if (by_tma(u, p0, left, first)) {
+            // the next tile's K before this one's V: scores are computed ahead of the products with V
+            for (int i = ahead ? 1 : 0; i < 2 && ok; ++i) {
+              uint32_t q0;
+              int rest, at;
+              if (u + i == s.u1 || !by_tma(u + i, q0, rest, at)) {
+                ahead = false;
+                break;
+              }
+              it += i;
+              ok = stage_free(S.k_empty);
+              it -= i;
+              if (lt == 0 && ok) {
+                S.meta[(it + i) % kTrRing] = make_int2(u + i, u + i + 1 == s.u1 ? last_flags : seg_flags);
+                load(&kmap, S.k[st ^ i], &S.k_full[st ^ i], at);
+                k_loads = it + i + 1;
+              }
+              ahead = i;
+              if (q_due) {
+                cp_wait<0>();
+                landed(nullptr);
+              }
             }
-            if (q_due) {
-              cp_wait<0>();
-              landed(nullptr);
-            }
-            if (!(ok = stage_free(S.v_empty))) break;
-            if (lt == 0) {
-              mbar_expect_tx(&S.v_full[st], kTrTile);
-              tma_load_4d(S.v[st], &vmap, &S.v_full[st], 0, first, s.kvh, s.b);
-              tma_load_4d(S.v[st] + kTrHalf, &vmap, &S.v_full[st], 64, first, s.kvh, s.b);
-            }
+            if (!ok || !(ok = stage_free(S.v_empty))) break;
+            if (lt == 0) load(&vmap, S.v[st], &S.v_full[st], first);
             ++it;
           } else {
-            ok = gather(A.k, A.v, s, u, flags, [&](int r, bool& live) {
+            ok = gather(A.k, A.v, s, u, u + 1 == s.u1 ? last_flags : seg_flags, [&](int r, bool& live) {
               live = r < left;
               return live ? row_of(A, p0 + (uint32_t)r) : 0;
             });
@@ -675,9 +730,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     }
     cp_wait<0>();
     if (lt == 0)  // copies still in flight land before the CTA ends
-      for (uint32_t i = it > 2 ? it - 2 : 0; i < it; ++i) {
-        mbar_drain(&S.k_full[i & 1], (i >> 1) & 1u, A.err);
-        mbar_drain(&S.v_full[i & 1], (i >> 1) & 1u, A.err);
+      {
+      for (uint32_t i = k_loads > 2 ? k_loads - 2 : 0; i < k_loads; ++i) mbar_drain(&S.k_full[i & 1], (i >> 1) & 1u, A.err);
+      for (uint32_t i = it > 2 ? it - 2 : 0; i < it; ++i) mbar_drain(&S.v_full[i & 1], (i >> 1) & 1u, A.err);
       }
   } else if (warp >= 2 * kTrSoft / 32 + kTrLoadWarps) {
     // ---------------- MMA issuer (one elected lane) ----------------
@@ -685,21 +740,23 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     if (warp == 2 * kTrSoft / 32 + kTrLoadWarps && lane == 0 && work) {
       constexpr uint32_t idesc_s = umma_idesc_bf16_f32(kTrKeys, kTrStream);
       constexpr uint32_t idesc_o = umma_idesc_bf16_f32(kHeadDim, 2 * kTrStream) | (1u << 15) | (1u << 16);  // MN-major
-      auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity & 1u, alive, A.err, A.budget); };
-      // Op o: the scores, later the product with V, of stream o % 2 and its tile.
+      auto ready = [&](uint64_t* bar, uint32_t parity) { return mbar_test(bar, parity & 1u); };
+      // Op o: the scores, later the product with V, of stream o % 2 and its tile.  Each of these returns false,
+      // having done nothing, while something it needs is missing.
       auto tile_of = [](uint32_t o) { return kSplitRows ? o >> 1 : o; };
       auto tile_done = [](uint32_t o) { return !kSplitRows || (o & 1u); };  // no later op of the other stream needs it
       bool seg_start = true, end = false;
       uint32_t segs = 0, epochs[2] = {0u, 0u};
+      int end_seg = 0;
       auto issue_s = [&](uint32_t o) -> bool {
         const uint32_t tile = tile_of(o), st = tile & 1, x = o & 1;
+        if (!ready(&S.s_free[x], (o >> 1) ^ 1u)) return false;
+        if ((!kSplitRows || x == 0) && !ready(&S.k_full[st], tile >> 1)) return false;
         if (seg_start) {
-          if (!wait(&S.q_full, segs)) return false;
+          if (!ready(&S.q_full, segs)) return false;
           ++segs;
           seg_start = false;
         }
-        if ((!kSplitRows || x == 0) && !wait(&S.k_full[st], tile >> 1)) return false;
-        if (!wait(&S.s_free[x], (o >> 1) ^ 1u)) return false;
         tc_fence_after();
         const uint32_t ka = smem_addr(S.k[st]), qa = smem_addr(S.q) + (kSplitRows ? x * kTrStream * 128u : 0u);
 #pragma unroll
@@ -709,32 +766,32 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
                    umma_desc_sw128(qa + h * (NR * 128u) + b, 16), idesc_s, kk > 0 ? 1u : 0u);
         }
         umma_commit(&S.s_full[x]);
-        S.cur[x] = (int)tile;
+        const int2 meta = S.meta[tile % kTrRing];
+        S.cur[x] = make_int4((int)tile, meta.x, meta.y, 0);
         mbar_arrive(&S.s_full[x]);
         if (tile_done(o)) {
           umma_commit(&S.k_empty[st]);
-          const int flags = S.meta[tile % kTrRing].y;
+          const int flags = meta.y;
           if (flags & 1) {
             umma_commit(&S.q_free);
             seg_start = true;
           }
           if (flags & 2) {
             end = true;
-            S.end_seg = (flags >> 2) + 1;
+            end_seg = (flags >> 2) + 1;
           }
         }
         return true;
       };
       auto issue_pv = [&](uint32_t o) -> bool {
         const uint32_t tile = tile_of(o), st = tile & 1, x = o & 1;
-        if (!wait(&S.p_full[x], o >> 1)) return false;
+        if (!ready(&S.p_full[x], o >> 1) || !ready(&S.v_full[st], tile >> 1)) return false;
         const bool fresh = S.new_epoch[x] != 0;
         uint32_t& ep = x ? epochs[1] : epochs[0];
         if (fresh) {
-          if (ep > 0 && !wait(&S.o_free[x], ep - 1)) return false;
+          if (ep > 0 && !ready(&S.o_free[x], ep - 1)) return false;
           ++ep;
         }
-        if (!wait(&S.v_full[st], tile >> 1)) return false;
         tc_fence_after();
         const uint32_t va = smem_addr(S.v[st]), pa = smem_addr(S.p[x][0]);
 #pragma unroll
@@ -748,25 +805,38 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       // After the last op one more for each stream, that tells it so: the other may be waiting for its sums.
       auto issue_end = [&](uint32_t o) -> bool {
         const uint32_t x = o & 1;
-        if (!wait(&S.s_free[x], (o >> 1) ^ 1u)) return false;
-        S.cur[x] = -1;
+        if (!ready(&S.s_free[x], (o >> 1) ^ 1u)) return false;
+        S.cur[x] = make_int4(-1, 0, 4 * end_seg, 0);
         mbar_arrive(&S.s_full[x]);
         mbar_arrive(&S.s_full[x]);
         return true;
       };
-      // the scores of op o + 2 (the stream has read those of op o) before the product of op o
-      uint32_t so = 0, po = 0, ops = 0;
-      bool ok = true;
-      for (; ok && !(end && po == ops && so == ops + 2); ++po) {
-        for (; ok && so < po + 3 && !(end && so == ops + 2); ++so) {
-          if (end) {
-            ok = issue_end(so);
-          } else {
-            ok = issue_s(so);
+      // Whichever is ready, in each line's order (a stream's scores come after it has read the ones before).
+      uint32_t so = 0, po = 0, ops = 0;  // (two more score ops than ops: the ends)
+      long long since = clock64();
+      while (!end || po < ops || so < ops + 2) {
+        bool moved = false;
+        if (!end) {
+          if (issue_s(so)) {
+            moved = true;
             if (end) ops = so + 1;
+            ++so;
           }
+        } else if (so < ops + 2 && issue_end(so)) {
+          moved = true;
+          ++so;
         }
-        if (ok && !(end && po >= ops)) ok = issue_pv(po);
+        if (po < so && (!end || po < ops) && issue_pv(po)) {
+          moved = true;
+          ++po;
+        }
+        const long long now = clock64();
+        if (moved) {
+          since = now;
+        } else if (now - since > A.budget) {
+          atomicExch(A.err, kDevErrTimeout);
+          break;
+        }
       }
       umma_commit(&S.fin);  // every product issued is done before TMEM is freed
       mbar_drain(&S.fin, 0, A.err);
@@ -776,7 +846,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     regs_inc<kTrSoftRegs>();
     const int x = tid / kTrSoft;                                 // stream
     const int quad = warp & 3, col0 = 32 * ((warp >> 2) & 1);    // this thread: key (then dim) 32 quad + lane, rows col0 ..
-    const int key = 32 * quad + lane, bar = kBarStream + x;
+    const int key = 32 * quad + lane;
     const int row_base = row0 + (kSplitRows ? kTrStream * x : 0);
     const int srows = max(0, min(kTrStream, rows - row_base));   // rows of the stream
     const int act = max(0, min(2, (srows - col0 + 15) / 16));    // this thread's 16-row halves that hold rows
@@ -784,7 +854,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     const uint32_t my_base = lane_base + (uint32_t)x * kTmemStream + (uint32_t)col0;
     const int t_first = (row_base + col0) % A.T;
     float* alpha = S.alpha[x];
-    uint32_t* colmax = reinterpret_cast<uint32_t*>(alpha);
+    uint32_t* colmax = S.colmax[x];
+    const int sc = tid % kTrSoft;                                // thread of the stream
     uint64_t scale2;
     asm("mov.b64 %0, {%1, %1};\n" : "=l"(scale2) : "f"(A.scale_log2));
     auto wait_warp = [&](uint64_t* b, uint32_t parity) {
@@ -795,43 +866,65 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       if (lane == 0) mbar_arrive(b);
     };
 
-    float l[32];
+    // The stream's barrier (bounded, as every wait here).
+    uint32_t syncs = 0;
+    auto sync = [&]() {
+      arrive_warp(&S.sync[x]);
+      wait_warp(&S.sync[x], syncs++);
+    };
+
+    uint64_t l2[16];  // row sums over this thread's keys, in pairs
 #pragma unroll
-    for (int c = 0; c < 32; ++c) l[c] = 0.f;
-    int seg = 0;                         // current segment
+    for (int i = 0; i < 16; ++i) l2[i] = 0ull;
+    uint32_t seen = 0u;                   // rows that attend any of them
+    int seg = 0;                          // current segment
+    int seg_b = 0, seg_n = 0, seg_lo = 0, seg_drafts = 0, seg_depth = 0;  // what its masks need
     bool has = false, has_total = false;  // the stream has taken a tile of it; its epochs have a total
     int in_epoch = 0;
-    uint32_t n = 0;  // ops of this stream so far
+    uint32_t n = 0, checks = 0;           // ops of this stream so far; epochs whose sums were looked at
     while (work) {
       wait_warp(&S.s_full[x], n);
-      if (bar_or(bar, kTrSoft, !alive)) break;
-      const int tile = S.cur[x];
-      const int2 meta = tile >= 0 ? S.meta[tile % kTrRing] : make_int2(0, 4 * S.end_seg);
+      if (!alive) break;
+      const int4 cur = S.cur[x];
+      const bool turn = n == 0 || seg < (cur.z >> 2);
 
       // ---- segments that ended before this tile: row sums over all keys, then O ----
-      for (; seg < (meta.y >> 2); ++seg) {
+      for (; seg < (cur.z >> 2); ++seg) {
         const TrSegInfo& info = S.seg[seg % kTrRing];
         if (has) {
           wait_warp(&S.p_free[x], n - 1);
           tc_fence_after();
         }
-        const float lsum = reduce_columns<16>(l, lane, [](float a, float b) { return a + b; });
+        seen = __reduce_or_sync(0xffffffffu, seen);
+        if (lane == 0 && seen) atomicOr(&S.seen[x][col0 >> 5], seen);
+        seen = 0u;
+        float l[32];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) l[c] = 0.f;
-        named_sync(bar, kTrSoft);       // (every warp is done with the last raise's factors)
-        for (int w = 0; w < 4; ++w) {   // the four warps of these rows, in order
+        for (int i = 0; i < 16; ++i) {
+          unpack2(l2[i], l[2 * i], l[2 * i + 1]);
+          l2[i] = 0ull;
+        }
+        const float lsum = reduce_columns<16>(l, lane, [](float a, float b) { return a + b; });
+        sync();  // (every warp is done with the last raise's factors)
+        for (int w = 0; w < 4; ++w) {  // the four warps of these rows, in order
           if (quad == w) alpha[col0 + lane] = w == 0 ? lsum : alpha[col0 + lane] + lsum;
-          named_sync(bar, kTrSoft);
+          sync();
         }
         if constexpr (!kSplitRows) {  // the other stream's sums
-          if (tid % kTrSoft < kTrStream && !has) S.nref[x][tid % kTrSoft] = -kTrNone;
-          if (tid % kTrSoft == 0) S.state[x] = (has ? 1 : 0) + (has_total ? 2 : 0);
+          if (sc == 0) S.state[x] = (has ? 1 : 0) + (has_total ? 2 : 0);
           tc_fence_before();
-          named_sync(bar, kTrSoft);
+          sync();
           arrive_warp(&S.sum_full[x]);
           wait_warp(&S.sum_full[x ^ 1], (uint32_t)seg);
           tc_fence_after();
         }
+        if (!alive) break;
+        // log2 of a row's sum in stream src; a NaN if it has lost the row's largest terms (or is one)
+        auto row_lse = [&](int src, int c) {
+          const float sum = S.alpha[src][c];
+          if (!((S.seen[src][c >> 5] >> (c & 31)) & 1u)) return kTrNone;
+          return sum >= kTrLow ? log2f(sum) - S.nref[src][c] : __int_as_float(0x7fffffff);
+        };
         // eight rows at a time: all 32 of this thread's, or 16 when the streams share them
         const int c_first = kSplitRows ? col0 : col0 + 16 * x;
         uint32_t bad = 0u;
@@ -840,8 +933,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
           float y[8], m[8], sum[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            y[i] = sum[i] = 0.f;
-            m[i] = kSplitRows ? -S.nref[x][c0 + i] : fmaxf(-S.nref[0][c0 + i], -S.nref[1][c0 + i]);
+            const float a = row_lse(kSplitRows ? x : 0, c0 + i), b = kSplitRows ? a : row_lse(1, c0 + i);
+            m[i] = a > b ? a : b;  // (a NaN of either stream makes the sum one)
+            sum[i] = kSplitRows ? ex2a(a - m[i]) : ex2a(a - m[i]) + ex2a(b - m[i]);
+            if (m[i] <= kTrNone) sum[i] = 0.f;
+            y[i] = 0.f;
           }
 #pragma unroll 1
           for (int src = kSplitRows ? x : 0; src < (kSplitRows ? x + 1 : 2); ++src) {
@@ -851,28 +947,26 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
             float e[8], r[8];
             tmem_ld8(at + kTmemOe, e);
             tmem_ld8(at + kTmemOe + kTrStream, r);
-            tmem_ld_wait();
+            tmem_wait(e);
+            tmem_wait(r);
 #pragma unroll
             for (int i = 0; i < 8; ++i) e[i] += r[i];
             if (state & 2) {
               tmem_ld8(at + kTmemOt, r);
-              tmem_ld_wait();
+              tmem_wait(r);
 #pragma unroll
               for (int i = 0; i < 8; ++i) e[i] += r[i];
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float f = kSplitRows ? 1.f : ex2a(-S.nref[src][c0 + i] - m[i]);
-              y[i] = kSplitRows ? e[i] : __fmaf_rn(e[i], f, y[i]);
-              sum[i] = kSplitRows ? S.alpha[src][c0 + i] : __fmaf_rn(S.alpha[src][c0 + i], f, sum[i]);
-            }
+            for (int i = 0; i < 8; ++i)
+              if (m[i] > kTrNone) y[i] = __fmaf_rn(e[i], ex2a(-S.nref[src][c0 + i] - m[i]), y[i]);
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int r = row_base + c0 + i;
             if (c0 + i >= srows) continue;
+            const float o = sum[i] == 0.f ? y[i] : y[i] * (1.f / sum[i]);
             if (info.slot < 0) {
-              const float o = y[i] * (sum[i] != 0.f ? 1.f / sum[i] : 0.f);
               bad |= (uint32_t)!isfinite(o) << (c0 + i - c_first);
               const int g = r / A.T, t = r - g * A.T;
               const int64_t off = info.b * A.o.sb + (int64_t)(info.kvh * A.G + g) * A.o.sh + t * A.o.sn + key;
@@ -882,8 +976,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
                 static_cast<float*>(A.o.data)[off] = o;
             } else {
               const int64_t at = (int64_t)info.slot * NR + (r - row0);
-              W.o[at * kHeadDim + key] = y[i];
-              if (key == 0) W.ml[at] = make_float2(m[i], sum[i]);
+              W.o[at * kHeadDim + key] = o;
+              if (key == 0) W.lse[at] = sum[i] == 0.f ? kTrNone : m[i] + log2f(sum[i]);
             }
           }
         }
@@ -893,10 +987,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
           wait_warp(&S.sum_free[x], (uint32_t)seg);
         }
         if (has) arrive_warp(&S.o_free[x]);
-        if (info.slot < 0) {
-          bad = __reduce_or_sync(0xffffffffu, bad);
-          if (lane == 0 && bad) atomicOr(&S.bad[x][col0 >> 5], bad);
-          named_sync(bar, kTrSoft);
+        bad = __reduce_or_sync(0xffffffffu, bad);
+        if (lane == 0 && bad) atomicOr(&S.bad[x][col0 >> 5], bad);
+        sync();
+        if (info.slot < 0)
           for (int i = warp & 7; i < 64; i += 8)
             if ((S.bad[x][i >> 5] >> (i & 31)) & 1u) {
               const int c = (kSplitRows ? 0 : 16 * x) + i, r = row_base + c, h = info.kvh * A.G + r / A.T;
@@ -904,55 +998,125 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
               scalar_row(A, info.b, h, r % A.T, y);
               store_row4(A, info.b, h, r % A.T, lane, y);
             }
-          named_sync(bar, kTrSoft);
-          if (tid % kTrSoft < 2) S.bad[x][tid % kTrSoft] = 0u;
-        }
+        sync();
+        if (sc < 2) S.bad[x][sc] = S.seen[x][sc] = 0u;
         has = has_total = false;
-        named_sync(bar, kTrSoft);  // (the stream's arrays are the next segment's from here on)
+        sync();  // (the stream's arrays are the next segment's from here on)
       }
-      if (tile < 0) break;
+      if (cur.x < 0 || !alive) break;
+      if (turn) {
+        const TrSegInfo& info = S.seg[seg % kTrRing];
+        seg_b = info.b;
+        seg_n = info.n;
+        seg_lo = info.lo;
+        seg_drafts = info.draft_tiles;
+        seg_depth = info.max_depth;
+      }
 
-      // ---- which of this thread's rows attend its key ----
-      const TrSegInfo& info = S.seg[seg % kTrRing];
+      // ---- which of this thread's rows attend its key, and whether it is one at all ----
       uint32_t mw = ~0u;
-      if (meta.x < info.draft_tiles) {
-        const int j = meta.x * kTrKeys + key;
+      bool is_key;
+      if (cur.y < seg_drafts) {
+        const int j = cur.y * kTrKeys + key;
+        is_key = j < A.T;
         mw = 0u;
-        if (meta.x * kTrKeys + 32 * quad < A.T) {
-          const int dj = j < A.T ? draft_depth(A, info.b, j) : 0;
+        if (cur.y * kTrKeys + 32 * quad < A.T) {
+          const int dj = is_key ? draft_depth(A, seg_b, j) : 0;
           int t = t_first;
           for (int c = 0; c < 32 && col0 + c < srows; ++c) {
-            const bool in = j < A.T && tree_bit(A, info.b, t, j) && (A.W <= 0 || dj > draft_depth(A, info.b, t) - A.W);
+            const bool in = is_key && tree_bit(A, seg_b, t, j) && (A.W <= 0 || dj > draft_depth(A, seg_b, t) - A.W);
             mw |= (uint32_t)in << c;
             if (++t == A.T) t = 0;
           }
         }
       } else if constexpr (SEL) {
-        mw = S.kmask[tile & 3][col0 >> 5][key];
+        mw = S.kmask[cur.x & 3][col0 >> 5][key];
+        is_key = mw != 0u;
       } else {
-        const uint32_t p0 = (uint32_t)info.lo + (uint32_t)(meta.x - info.draft_tiles) * kTrKeys;
-        const int age = info.n - 1 - (int)(p0 + (uint32_t)key);  // (below 0: past the end)
-        if (age < 0) mw = 0u;
-        if (A.W > 0 && info.n - 1 - (int)p0 > oldest_age(A, info.max_depth)) {
+        const uint32_t p0 = (uint32_t)seg_lo + (uint32_t)(cur.y - seg_drafts) * kTrKeys;
+        const int age = seg_n - 1 - (int)(p0 + (uint32_t)key);  // (below 0: past the end)
+        is_key = age >= 0;
+        if (!is_key) mw = 0u;
+        if (A.W > 0 && seg_n - 1 - (int)p0 > oldest_age(A, seg_depth)) {
           int t = t_first;
           uint32_t in = 0u;
           for (int c = 0; c < 32 && col0 + c < srows; ++c) {
-            in |= (uint32_t)(age <= oldest_age(A, draft_depth(A, info.b, t))) << c;
+            in |= (uint32_t)(age <= oldest_age(A, draft_depth(A, seg_b, t))) << c;
             if (++t == A.T) t = 0;
           }
           mw &= in;
         }
       }
+      seen |= mw;
 
-      // ---- logits of 16 rows, less the reference if `relative` (log2 units); -inf where not attended ----
-      auto scores = [&](int hh, bool relative, float (&d)[16]) {
-        uint32_t v[16];
-        tmem_ld16(my_base + 16u * hh, v);
-        tmem_ld_wait();
+      const bool fresh = !has || in_epoch == kTrEpoch;
+      bool raise = false;
+      tc_fence_after();
+      if (!has) {
+        // the references: each row's largest finite logit over the tile's keys
+        if (sc < kTrStream) colmax[sc] = kTrNoKey;
+        sync();
+#pragma unroll 1
+        for (int hh = 0; hh < act; ++hh) {
+          uint32_t v[16];
+          float d[16];
+          tmem_ld16(my_base + 16u * hh, v);
+          tmem_wait(v);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            d[c] = __uint_as_float(v[c]) * A.scale_log2;
+            if (!is_key || !(fabsf(d[c]) < 1e30f)) d[c] = -INFINITY;
+          }
+          const float m = reduce_columns16(d, lane, [](float a, float b) { return fmaxf(a, b); });
+          if (lane < 16) atomicMax(&colmax[col0 + 16 * hh + lane], score_key(m));
+        }
+        sync();
+        if (sc < kTrStream) {
+          S.nref[x][sc] = colmax[sc] == kTrNoKey ? 0.f : -key_score(colmax[sc]);
+          colmax[sc] = 0u;
+        }
+        sync();
+      } else if (fresh) {
+        // an epoch is over: raise the references of rows whose sums have grown large, by a power of two
+        float l[32], top = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          unpack2(l2[i], l[2 * i], l[2 * i + 1]);
+          top = max3f(top, l[2 * i], l[2 * i + 1]);
+        }
+        const uint32_t e = checks++ & 1u;
+        if (__any_sync(0xffffffffu, top > kTrHigh)) {
+          const float m = reduce_columns<16>(l, lane, [](float a, float b) { return fmaxf(a, b); });
+          atomicMax(&colmax[col0 + lane], __float_as_uint(fmaxf(m, 0.f)));
+          if (lane == 0) S.raise[x][e] = 1;
+        }
+        sync();
+        raise = S.raise[x][e] != 0;
+        if (sc == 0) S.raise[x][e ^ 1u] = 0;
+        if (raise) {
+          if (sc < kTrStream) {
+            const float up = __uint_as_float(colmax[sc]);
+            const float by = up > kTrHigh && up < INFINITY ? (float)ilogbf(up) : 0.f;
+            S.nref[x][sc] -= by;
+            alpha[sc] = ex2a(-by);
+          }
+          sync();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float a, b;
+            unpack2(l2[i], a, b);
+            l2[i] = pack2(a * alpha[col0 + 2 * i], b * alpha[col0 + 2 * i + 1]);
+          }
+        }
+        if (sc < kTrStream) colmax[sc] = 0u;  // (the next epoch's sums come after a wait of all)
+      }
+
+      // ---- P = 2^(logit - reference) as bf16 hi + lo, key-major rows of 64 query rows (128 bytes, swizzled) ----
+      auto scores = [&](int hh, const uint32_t (&v)[16], float (&d)[16]) {
         const ulonglong2* nr = reinterpret_cast<const ulonglong2*>(S.nref[x] + col0 + 16 * hh);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const ulonglong2 r = relative ? nr[i] : make_ulonglong2(0ull, 0ull);
+          const ulonglong2 r = nr[i];
           fma2c(v[4 * i], v[4 * i + 1], scale2, r.x, d[4 * i], d[4 * i + 1]);
           fma2c(v[4 * i + 2], v[4 * i + 3], scale2, r.y, d[4 * i + 2], d[4 * i + 3]);
         }
@@ -962,62 +1126,20 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
           for (int c = 0; c < 16; ++c) d[c] = (w >> c) & 1u ? d[c] : -INFINITY;
         }
       };
-      tc_fence_after();
-      float top = -INFINITY;
-      if (has) {
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          if (hh >= act) continue;
-          float d[16];
-          scores(hh, true, d);
-#pragma unroll
-          for (int c = 0; c < 16; c += 2) top = max3f(top, d[c], d[c + 1]);
-        }
-      }
-      const bool raise = bar_or(bar, kTrSoft, !has || top > kTrSlack);
-      if (raise) {
-        // the tile's maximum of every row, over its keys
-        if (tid % kTrSoft < kTrStream) colmax[tid % kTrSoft] = kTrNoKey;
-        named_sync(bar, kTrSoft);
-#pragma unroll 1
-        for (int hh = 0; hh < act; ++hh) {
-          float d[16];
-          scores(hh, false, d);
-          const float m = reduce_columns16(d, lane, [](float a, float b) { return fmaxf(a, b); });
-          if (lane < 16) atomicMax(&colmax[col0 + 16 * hh + lane], score_key(m));
-        }
-        named_sync(bar, kTrSoft);
-        if (tid % kTrSoft < kTrStream) {
-          const int c = tid % kTrSoft;
-          const float old = has ? -S.nref[x][c] : kTrNone;
-          const float now = fmaxf(old, key_score(colmax[c]));
-          S.nref[x][c] = -now;
-          alpha[c] = ex2a(old - now);
-        }
-        named_sync(bar, kTrSoft);
-        if (has) {
-#pragma unroll
-          for (int c = 0; c < 32; ++c) l[c] *= alpha[col0 + c];
-        }
-      }
-
-      // ---- P = 2^d as bf16 hi + lo, key-major rows of 64 query rows (128 bytes, swizzled) ----
-      wait_warp(&S.p_free[x], n ^ 1u);
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        if (hh >= act) continue;
-        float d[16];
-        scores(hh, true, d);
-        uint32_t hi_w[8], lo_w[8];
+      uint32_t hi_w[8], lo_w[8];
+      auto exps = [&](int hh, const float (&d)[16]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float p0 = ex2a(d[2 * i]), p1 = ex2a(d[2 * i + 1]);
-          add2(l[16 * hh + 2 * i], l[16 * hh + 2 * i + 1], p0, p1);
+          const uint64_t p = pack2(ex2a(d[2 * i]), ex2a(d[2 * i + 1]));
+          l2[8 * hh + i] = add2u(l2[8 * hh + i], p);
+          float p0, p1;
+          unpack2(p, p0, p1);
           hi_w[i] = pack_bf16x2(p0, p1);
-          float r0, r1;
-          sub2p(p0, p1, bf16_lo(hi_w[i]), bf16_hi(hi_w[i]), r0, r1);
-          lo_w[i] = pack_bf16x2(r0, r1);
+          unpack2(sub2u(p, pack2(bf16_lo(hi_w[i]), bf16_hi(hi_w[i]))), p0, p1);
+          lo_w[i] = pack_bf16x2(p0, p1);
         }
+      };
+      auto put = [&](int hh) {
         const int c8 = (col0 + 16 * hh) >> 3;  // first 16-byte chunk of these rows
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -1027,12 +1149,34 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
           *reinterpret_cast<uint4*>(&S.p[x][1][o]) =
               make_uint4(lo_w[4 * i], lo_w[4 * i + 1], lo_w[4 * i + 2], lo_w[4 * i + 3]);
         }
+      };
+      if (act > 0) {
+        uint32_t v[16];
+        float d[16];
+        tmem_ld16(my_base, v);
+        tmem_wait(v);
+        scores(0, v, d);
+        if (act > 1) tmem_ld16(my_base + 16u, v);
+        exps(0, d);
+        wait_warp(&S.p_free[x], n ^ 1u);
+        put(0);
+        if (act > 1) {
+          tmem_wait(v);
+          tc_fence_before();
+          arrive_warp(&S.s_free[x]);
+          scores(1, v, d);
+          exps(1, d);
+          put(1);
+        }
+      } else {
+        wait_warp(&S.p_free[x], n ^ 1u);
       }
-      tc_fence_before();
-      arrive_warp(&S.s_free[x]);
+      if (act < 2) {
+        tc_fence_before();
+        arrive_warp(&S.s_free[x]);
+      }
       fence_async();
-      const bool fresh = raise || in_epoch == kTrEpoch;
-      if (tid % kTrSoft == 0) S.new_epoch[x] = fresh;
+      if (sc == 0) S.new_epoch[x] = fresh;
       arrive_warp(&S.p_full[x]);
 
       // ---- the epoch before this tile joins the total ----
@@ -1043,12 +1187,13 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
           float e[8], r[8];
           tmem_ld8(my_base + kTmemOe + c0, e);
           tmem_ld8(my_base + kTmemOe + kTrStream + c0, r);
-          tmem_ld_wait();
+          tmem_wait(e);
+          tmem_wait(r);
 #pragma unroll
           for (int i = 0; i < 8; ++i) e[i] += r[i];
           if (has_total) {
             tmem_ld8(my_base + kTmemOt + c0, r);
-            tmem_ld_wait();
+            tmem_wait(r);
 #pragma unroll
             for (int i = 0; i < 8; ++i) e[i] += r[i];
           }
@@ -1062,9 +1207,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         arrive_warp(&S.o_free[x]);
         has_total = true;
       }
+
       in_epoch = fresh ? 1 : in_epoch + 1;
       has = true;
       ++n;
+      if (!alive) break;
     }
   }
 
@@ -1092,37 +1239,40 @@ __global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const __grid_
   const bool join = pieces.y > 1;  // (one piece: its CTA has written the output)
   float m = kTrNone, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  // one more piece (or partial join) of weight 2^s l (a NaN of either reaches the sum)
+  auto take = [&](float s, float w, const float4& y, float mn) {
+    const float f = s <= kTrNone ? 0.f : ex2a(s - mn);
+    if (f == 0.f) return;  // (what it holds may be anything)
+    l += f * w;
+    o = make_float4(o.x + f * y.x, o.y + f * y.y, o.z + f * y.z, o.w + f * y.w);
+  };
   if (join) {
     const int c = r % W.nr;
     const int64_t slot0 = (int64_t)(r / W.nr) * 2 * W.ranges;
     auto at = [&](int i) { return (slot0 + 2 * (pieces.x + i) + (i == 0)) * W.nr + c; };
     constexpr int kUnroll = 4;
     for (int i = part; i < pieces.y; i += WPR * kUnroll) {
-      float2 s[kUnroll];
+      float s[kUnroll];
       float4 y[kUnroll];
 #pragma unroll
       for (int q = 0; q < kUnroll; ++q) {
         const int p = i + WPR * q;
-        s[q] = make_float2(kTrNone, 0.f);
+        s[q] = kTrNone;
         y[q] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (p < pieces.y) {
-          s[q] = W.ml[at(p)];
+          s[q] = W.lse[at(p)];
           y[q] = reinterpret_cast<const float4*>(W.o + at(p) * kHeadDim)[lane];
         }
       }
       float mn = m;
 #pragma unroll
-      for (int q = 0; q < kUnroll; ++q) mn = fmaxf(mn, s[q].x);
+      for (int q = 0; q < kUnroll; ++q) mn = fmaxf(mn, s[q]);
       const float al = ex2a(m - mn);
       m = mn;
       l *= al;
       o = make_float4(o.x * al, o.y * al, o.z * al, o.w * al);
 #pragma unroll
-      for (int q = 0; q < kUnroll; ++q) {
-        const float f = ex2a(s[q].x - mn);
-        l += f * s[q].y;
-        o = make_float4(o.x + f * y[q].x, o.y + f * y[q].y, o.z + f * y[q].z, o.w + f * y[q].w);
-      }
+      for (int q = 0; q < kUnroll; ++q) take(s[q], 1.f, y[q], mn);
     }
   }
   if (WPR > 1) {
@@ -1136,12 +1286,7 @@ __global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const __grid_
     l = 0.f;
     o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < WPR; ++w) {
-      const float f = ex2a(sml[warp + w].x - M);
-      const float4 y = so[warp + w][lane];
-      l += f * sml[warp + w].y;
-      o = make_float4(o.x + f * y.x, o.y + f * y.y, o.z + f * y.z, o.w + f * y.w);
-    }
+    for (int w = 0; w < WPR; ++w) take(sml[warp + w].x, sml[warp + w].y, so[warp + w][lane], M);
   }
   if (!join) return;
   const float inv = l != 0.f ? 1.f / l : 0.f;
@@ -1154,8 +1299,8 @@ __global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const __grid_
 template <int NR, bool SEL>
 cudaError_t launch_tiles(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeAttnArgs& a, const TrParts& w,
                          int use_tma, cudaStream_t stream) {
-  const size_t smem = sizeof(TrSmem<NR>) + 1024;
-  static_assert(sizeof(TrSmem<NR>) + 1024 <= 232448, "shared memory of one CTA");
+  const size_t smem = sizeof(TrSmem<NR>);
+  static_assert(sizeof(TrSmem<NR>) <= 232448, "shared memory of one CTA");
   cudaError_t e =
       cudaFuncSetAttribute(tree_attn_kernel<NR, SEL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
@@ -1185,7 +1330,7 @@ cudaError_t launch_tree_attn(const TreeAttnArgs& a, cudaStream_t stream) {
   char* ws = static_cast<char*>(a.ws);
   w.table = reinterpret_cast<int2*>(ws);
   w.o = reinterpret_cast<float*>(ws + L.table);
-  w.ml = reinterpret_cast<float2*>(ws + L.table + L.o);
+  w.lse = reinterpret_cast<float*>(ws + L.table + L.o);
   w.nr = L.nr;
   w.rbs = L.rbs;
   w.ranges = L.ranges;
