@@ -104,6 +104,7 @@ struct TrSmem {
   alignas(1024) uint8_t p[2][2][kTrKeys * kTrStream * 2];  // [stream][hi, lo]
   alignas(16) float nref[2][kTrStream];  // minus the reference of each row (log2 units)
   alignas(16) float alpha[2][kTrStream];  // 2^(old - new reference) of the last raise; at a segment's end the row sums
+  float wt[NR == 64 ? 2 : 1][2][NR == 64 ? kTrStream : 1];  // [stream writing][stream summed]: factors of its O
   uint32_t colmax[2][kTrStream];         // a tile's row maxima (as score_key), or the largest sums (float bits)
   uint64_t k_full[kTrStages], k_empty[kTrStages], v_full[kTrStages], v_empty[kTrStages];
   uint64_t s_full[2], s_free[2], p_full[2], p_free[2], o_free[2], sum_full[2], sum_free[2], sync[2];
@@ -118,7 +119,7 @@ struct TrSmem {
   uint32_t tmem_base;
   int start_b;
   int64_t start_base;
-  unsigned long long total;
+  int64_t total, per;            // tiles of the whole line, and of a range
   int cnt[2][kTrLoadWarps];
   TrSegInfo seg[kTrRing];
   int qkey[kQueue];              // selected keys waiting for a tile (ring)
@@ -202,6 +203,18 @@ RTP_DEVICE float reduce_columns16(float (&x)[16], int lane, F op) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) x[i] = op(x[i], __shfl_xor_sync(0xffffffffu, x[i], 16));
   return reduce_columns<8>(x, lane, op);
+}
+
+// Bit c of lane k becomes bit k of lane c.
+RTP_DEVICE uint32_t transpose32(uint32_t x, int lane) {
+  uint32_t m = 0x0000ffffu;
+#pragma unroll
+  for (int j = 16; j > 0; j >>= 1) {
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, x, j);
+    x = lane & j ? (x & ~m) | ((y >> j) & m) : (x & m) | ((y & m) << j);
+    m ^= m << (j >> 1);
+  }
+  return x;
 }
 
 // Waits for the loads that fill these registers (naming them keeps their uses behind it).
@@ -422,7 +435,6 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     mbar_init(&S.q_free, 1);
     mbar_init(&S.fin, 1);
     mbar_fence_init();
-    S.total = 0;
   }
   if (warp == 0) tmem_alloc(&S.tmem_base, kTmemCols);
   // rows past the last one never get a P: zeros
@@ -433,26 +445,23 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   }
   pdl_wait();
   pdl_release();
-  __syncthreads();
 
   // ---- this CTA's range of the line of tiles ----
-  {
-    unsigned long long mine = 0;
-    for (int b = tid; b < A.B; b += kTrThreads) mine += (unsigned long long)span_of<SEL>(A, b).tiles;
-    if (mine) atomicAdd(&S.total, mine);
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = S.tmem_base;
-  const int64_t total = (int64_t)S.total * A.Hk;
-  const int64_t per = (total + W.ranges - 1) / W.ranges;
-  const int64_t lo = range * per, hi = min(lo + per, total);
-  const bool work = lo < hi;
-  if (work && warp == 0) {
+  if (warp == 0) {
+    int64_t sum = 0;
+    const int first = lane < A.B ? span_of<SEL>(A, lane).tiles : 0;
+    for (int b = lane; b < A.B; b += 32) sum += b == lane ? first : span_of<SEL>(A, b).tiles;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const int64_t total = sum * A.Hk, per = (total + W.ranges - 1) / W.ranges, lo = range * per;
+    if (lane == 0) {
+      S.total = total;
+      S.per = per;
+    }
     int64_t base = 0;
-    for (int b0 = 0; b0 < A.B; b0 += 32) {
-      const int64_t mine = b0 + lane < A.B ? (int64_t)span_of<SEL>(A, b0 + lane).tiles * A.Hk : 0;
+    for (int b0 = 0; b0 < A.B && lo < total; b0 += 32) {
+      const int b = b0 + lane;
+      const int64_t mine = (int64_t)(b0 == 0 ? first : b < A.B ? span_of<SEL>(A, b).tiles : 0) * A.Hk;
       int64_t incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -462,7 +471,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       const uint32_t past = __ballot_sync(0xffffffffu, base + incl > lo);
       if (past) {
         if (lane == __ffs(past) - 1) {
-          S.start_b = b0 + lane;
+          S.start_b = b;
           S.start_base = base + incl - mine;
         }
         break;
@@ -470,7 +479,12 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       base += __shfl_sync(0xffffffffu, incl, 31);
     }
   }
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = S.tmem_base;
+  const int64_t per = S.per, lo = range * per, hi = min(lo + per, S.total);
+  const bool work = lo < hi;
 
   bool alive = true;
 
@@ -539,6 +553,22 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       const TrSeg s = walk.s;
       more = walk.next(A);
       const int seg_flags = 4 * segs, last_flags = seg_flags + 1 + (more ? 0 : 2);
+      // ---- the query rows (the previous segment's products are done with the buffer) ----
+      {
+        const bool free = segs == 0 || mbar_wait(&S.q_free, (segs - 1) & 1u, alive, A.err, A.budget);
+        if (bar_or(kBarLoad, kTrLoad, !free)) break;
+        const __nv_bfloat16* qb =
+            static_cast<const __nv_bfloat16*>(A.q.data) + s.b * A.q.sb + (int64_t)s.kvh * A.G * A.q.sh + chunk * 8;
+#pragma unroll 4
+        for (int i = 0; i < NR / 8; ++i) {
+          const int r = r_first + 8 * i, rr = min(row0 + r, rows - 1);
+          const int g = rr / A.T, t = rr - g * A.T;
+          cp16(smem_addr(S.q) + (uint32_t)(chunk >> 3) * (NR * 128u) + slot0 + 1024u * i, qb + g * A.q.sh + t * A.q.sn,
+               r < nrows);
+        }
+        cp_commit();
+        q_due = true;
+      }
       {
         TrSegInfo info;
         info.b = s.b;
@@ -559,22 +589,6 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
           if (s.u0 == 0 && rb == 0)
             W.table[s.b * A.Hk + s.kvh] = make_int2(range, (int)((s.base + s.span.tiles - 1) / per) - range + 1);
         }
-      }
-      // ---- the query rows (the previous segment's products are done with the buffer) ----
-      {
-        const bool free = segs == 0 || mbar_wait(&S.q_free, (segs - 1) & 1u, alive, A.err, A.budget);
-        if (bar_or(kBarLoad, kTrLoad, !free)) break;
-        const __nv_bfloat16* qb =
-            static_cast<const __nv_bfloat16*>(A.q.data) + s.b * A.q.sb + (int64_t)s.kvh * A.G * A.q.sh + chunk * 8;
-#pragma unroll 4
-        for (int i = 0; i < NR / 8; ++i) {
-          const int r = r_first + 8 * i, rr = min(row0 + r, rows - 1);
-          const int g = rr / A.T, t = rr - g * A.T;
-          cp16(smem_addr(S.q) + (uint32_t)(chunk >> 3) * (NR * 128u) + slot0 + 1024u * i, qb + g * A.q.sh + t * A.q.sn,
-               r < nrows);
-        }
-        cp_commit();
-        q_due = true;
         ++segs;
       }
       const int drafts_end = min(s.u1, s.span.draft_tiles);
@@ -655,6 +669,22 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
             }
           }
         }
+        // a round's mask words, on their way while the round before is worked on; neighbouring ranges take rounds
+        // from all over the context (a prime larger than their number), since selected keys come in clusters
+        uint32_t ahead[2][4];
+        int next_key = 0;
+        auto fetch = [&](int u) {
+          const int i0 = u - s.span.draft_tiles;
+          const int round = (int)((uint64_t)i0 * 2654435761ull % (uint64_t)rounds);
+          next_key = s.span.lo + round * kTrRound + lw * 128;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int wb = next_key + 32 * w, rem = s.span.n - wb;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) ahead[i][w] = words[i] && rem > 0 ? __ldg(words[i] + (wb >> 5)) : 0u;
+          }
+        };
+        fetch(max(s.u0, s.span.draft_tiles));
         auto emit = [&](int take, int flags) {
           // one key per loader thread: its row bits for the softmax
           uint2 bits = make_uint2(0u, 0u);
@@ -670,18 +700,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
           count -= take;
         };
         for (int u = max(s.u0, s.span.draft_tiles); u < s.u1 && ok; ++u) {
-          // neighbouring ranges take rounds from all over the context (a prime larger than their number),
-          // since selected keys come in clusters
-          const int i0 = u - s.span.draft_tiles;
-          const int round = (int)((uint64_t)i0 * 2654435761ull % (uint64_t)rounds);
-          const int key0 = s.span.lo + round * kTrRound + lw * 128;
           uint32_t x[2][4], uni[4];
+          const int key0 = next_key;
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            const int wb = key0 + 32 * w, rem = s.span.n - wb;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) x[i][w] = words[i] && rem > 0 ? __ldg(words[i] + (wb >> 5)) : 0u;
+            x[0][w] = ahead[0][w];
+            x[1][w] = ahead[1][w];
           }
+          if (u + 1 < s.u1) fetch(u + 1);
           int mine = 0;
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
@@ -879,6 +905,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     uint32_t seen = 0u;                   // rows that attend any of them
     int seg = 0;                          // current segment
     int seg_b = 0, seg_n = 0, seg_lo = 0, seg_drafts = 0, seg_depth = 0;  // what its masks need
+    int row_depth = 0;                    // (lane c: of row col0 + c)
     bool has = false, has_total = false;  // the stream has taken a tile of it; its epochs have a total
     int in_epoch = 0;
     uint32_t n = 0, checks = 0;           // ops of this stream so far; epochs whose sums were looked at
@@ -905,79 +932,87 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
           l2[i] = 0ull;
         }
         const float lsum = reduce_columns<16>(l, lane, [](float a, float b) { return a + b; });
-        sync();  // (every warp is done with the last raise's factors)
-        for (int w = 0; w < 4; ++w) {  // the four warps of these rows, in order
-          if (quad == w) alpha[col0 + lane] = w == 0 ? lsum : alpha[col0 + lane] + lsum;
-          sync();
-        }
-        if constexpr (!kSplitRows) {  // the other stream's sums
+        // (the stream's P tile is free: the four warps of a row leave their sums in it)
+        auto part = [&](int w, int c) {
+          const int r = 16 * w + (c >> 2);
+          return reinterpret_cast<float*>(&S.p[x][0][r * 128 + ((r & 7) << 4) + 4 * (c & 3)]);
+        };
+        if (has) *part(quad, col0 + lane) = lsum;
+        sync();
+        float sum = 0.f;
+        if (sc < kTrStream && has) sum = ((*part(0, sc) + *part(1, sc)) + *part(2, sc)) + *part(3, sc);
+        const bool seen_row = sc < kTrStream && ((S.seen[x][sc >> 5] >> (sc & 31)) & 1u);
+        // log2 of a row's sum (a NaN if it has lost the row's largest terms, or is one)
+        const float lse = !seen_row ? kTrNone : sum >= kTrLow ? log2f(sum) - S.nref[x][sc] : __int_as_float(0x7fffffff);
+        float whole_lse = lse;
+        if constexpr (kSplitRows) {
+          if (sc < kTrStream) alpha[sc] = !seen_row ? 0.f : sum >= kTrLow ? 1.f / sum : __int_as_float(0x7fffffff);
+        } else {  // the other stream's
+          if (sc < kTrStream) alpha[sc] = lse;
           if (sc == 0) S.state[x] = (has ? 1 : 0) + (has_total ? 2 : 0);
           tc_fence_before();
-          sync();
           arrive_warp(&S.sum_full[x]);
+          wait_warp(&S.sum_full[x], (uint32_t)seg);
           wait_warp(&S.sum_full[x ^ 1], (uint32_t)seg);
           tc_fence_after();
+          if (sc < kTrStream) {
+            const float a = S.alpha[0][sc], b = S.alpha[1][sc], m = a > b ? a : b;  // (a NaN of either stays one)
+            const float both = ex2a(a - m) + ex2a(b - m), inv = 1.f / both;
+            S.wt[x][0][sc] = a <= kTrNone ? 0.f : ex2a(-S.nref[0][sc] - m) * inv;
+            S.wt[x][1][sc] = b <= kTrNone ? 0.f : ex2a(-S.nref[1][sc] - m) * inv;
+            whole_lse = m <= kTrNone && both >= 0.f ? kTrNone : m + log2f(both);
+          }
         }
         if (!alive) break;
-        // log2 of a row's sum in stream src; a NaN if it has lost the row's largest terms (or is one)
-        auto row_lse = [&](int src, int c) {
-          const float sum = S.alpha[src][c];
-          if (!((S.seen[src][c >> 5] >> (c & 31)) & 1u)) return kTrNone;
-          return sum >= kTrLow ? log2f(sum) - S.nref[src][c] : __int_as_float(0x7fffffff);
-        };
+        if (info.slot >= 0 && sc < srows && (kSplitRows || x == 0))
+          W.lse[(int64_t)info.slot * NR + row_base - row0 + sc] = whole_lse;
+        sync();
         // eight rows at a time: all 32 of this thread's, or 16 when the streams share them
         const int c_first = kSplitRows ? col0 : col0 + 16 * x;
         uint32_t bad = 0u;
+        int g = (row_base + c_first) / A.T, t = row_base + c_first - g * A.T;
 #pragma unroll 1
         for (int c0 = c_first; c0 < c_first + (kSplitRows ? 32 : 16) && c0 < srows; c0 += 8) {
-          float y[8], m[8], sum[8];
+          float y[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float a = row_lse(kSplitRows ? x : 0, c0 + i), b = kSplitRows ? a : row_lse(1, c0 + i);
-            m[i] = a > b ? a : b;  // (a NaN of either stream makes the sum one)
-            sum[i] = kSplitRows ? ex2a(a - m[i]) : ex2a(a - m[i]) + ex2a(b - m[i]);
-            if (m[i] <= kTrNone) sum[i] = 0.f;
-            y[i] = 0.f;
-          }
+          for (int i = 0; i < 8; ++i) y[i] = 0.f;
 #pragma unroll 1
           for (int src = kSplitRows ? x : 0; src < (kSplitRows ? x + 1 : 2); ++src) {
             const int state = kSplitRows ? 1 + (has_total ? 2 : 0) : S.state[src];
             if (!(state & 1)) continue;
             const uint32_t at = lane_base + (uint32_t)src * kTmemStream + (uint32_t)c0;
-            float e[8], r[8];
+            const float* wt = kSplitRows ? alpha : S.wt[kSplitRows ? 0 : x][src];
+            float e[8], r[8], q[8];
             tmem_ld8(at + kTmemOe, e);
             tmem_ld8(at + kTmemOe + kTrStream, r);
+            if (state & 2) tmem_ld8(at + kTmemOt, q);
             tmem_wait(e);
             tmem_wait(r);
+            if (state & 2) tmem_wait(q);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) e[i] += r[i];
-            if (state & 2) {
-              tmem_ld8(at + kTmemOt, r);
-              tmem_wait(r);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) e[i] += r[i];
+            for (int i = 0; i < 8; ++i) {
+              e[i] += r[i];
+              if (state & 2) e[i] += q[i];
+              y[i] = __fmaf_rn(e[i], wt[c0 + i], y[i]);
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (m[i] > kTrNone) y[i] = __fmaf_rn(e[i], ex2a(-S.nref[src][c0 + i] - m[i]), y[i]);
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const int r = row_base + c0 + i;
-            if (c0 + i >= srows) continue;
-            const float o = sum[i] == 0.f ? y[i] : y[i] * (1.f / sum[i]);
-            if (info.slot < 0) {
-              bad |= (uint32_t)!isfinite(o) << (c0 + i - c_first);
-              const int g = r / A.T, t = r - g * A.T;
-              const int64_t off = info.b * A.o.sb + (int64_t)(info.kvh * A.G + g) * A.o.sh + t * A.o.sn + key;
-              if (A.o_bf16)
-                static_cast<__nv_bfloat16*>(A.o.data)[off] = __float2bfloat16_rn(o);
-              else
-                static_cast<float*>(A.o.data)[off] = o;
-            } else {
-              const int64_t at = (int64_t)info.slot * NR + (r - row0);
-              W.o[at * kHeadDim + key] = o;
-              if (key == 0) W.lse[at] = sum[i] == 0.f ? kTrNone : m[i] + log2f(sum[i]);
+            if (c0 + i < srows) {
+              if (info.slot < 0) {
+                bad |= (uint32_t)!isfinite(y[i]) << (c0 + i - c_first);
+                const int64_t off = info.b * A.o.sb + (int64_t)(info.kvh * A.G + g) * A.o.sh + t * A.o.sn + key;
+                if (A.o_bf16)
+                  static_cast<__nv_bfloat16*>(A.o.data)[off] = __float2bfloat16_rn(y[i]);
+                else
+                  static_cast<float*>(A.o.data)[off] = y[i];
+              } else {
+                W.o[((int64_t)info.slot * NR + row_base - row0 + c0 + i) * kHeadDim + key] = y[i];
+              }
+            }
+            if (++t == A.T) {
+              t = 0;
+              ++g;
             }
           }
         }
@@ -989,8 +1024,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         if (has) arrive_warp(&S.o_free[x]);
         bad = __reduce_or_sync(0xffffffffu, bad);
         if (lane == 0 && bad) atomicOr(&S.bad[x][col0 >> 5], bad);
-        sync();
-        if (info.slot < 0)
+        sync();  // (from here on the stream's arrays are the next segment's)
+        if (S.bad[x][0] | S.bad[x][1]) {
           for (int i = warp & 7; i < 64; i += 8)
             if ((S.bad[x][i >> 5] >> (i & 31)) & 1u) {
               const int c = (kSplitRows ? 0 : 16 * x) + i, r = row_base + c, h = info.kvh * A.G + r / A.T;
@@ -998,10 +1033,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
               scalar_row(A, info.b, h, r % A.T, y);
               store_row4(A, info.b, h, r % A.T, lane, y);
             }
-        sync();
+          sync();
+        }
         if (sc < 2) S.bad[x][sc] = S.seen[x][sc] = 0u;
         has = has_total = false;
-        sync();  // (the stream's arrays are the next segment's from here on)
       }
       if (cur.x < 0 || !alive) break;
       if (turn) {
@@ -1011,6 +1046,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         seg_lo = info.lo;
         seg_drafts = info.draft_tiles;
         seg_depth = info.max_depth;
+        row_depth = draft_depth(A, seg_b, (t_first + lane) % A.T);
       }
 
       // ---- which of this thread's rows attend its key, and whether it is one at all ----
@@ -1019,15 +1055,18 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       if (cur.y < seg_drafts) {
         const int j = cur.y * kTrKeys + key;
         is_key = j < A.T;
-        mw = 0u;
-        if (cur.y * kTrKeys + 32 * quad < A.T) {
+        // lane c reads the tree word of row c; transposed, a lane has its key's bits over the rows
+        const bool words = cur.y * kTrKeys + 32 * quad < A.T && col0 + lane < srows;
+        mw = transpose32(words ? __ldg(A.tree + ((int64_t)seg_b * A.T + (t_first + lane) % A.T) * A.tree_words +
+                                       4 * cur.y + quad)
+                               : 0u,
+                         lane);
+        if (!is_key) mw = 0u;
+        if (A.W > 0 && seg_depth >= A.W) {
           const int dj = is_key ? draft_depth(A, seg_b, j) : 0;
-          int t = t_first;
-          for (int c = 0; c < 32 && col0 + c < srows; ++c) {
-            const bool in = is_key && tree_bit(A, seg_b, t, j) && (A.W <= 0 || dj > draft_depth(A, seg_b, t) - A.W);
-            mw |= (uint32_t)in << c;
-            if (++t == A.T) t = 0;
-          }
+          uint32_t in = 0u;
+          for (int c = 0; c < 32; ++c) in |= (uint32_t)(dj > __shfl_sync(0xffffffffu, row_depth, c) - A.W) << c;
+          mw &= in;
         }
       } else if constexpr (SEL) {
         mw = S.kmask[cur.x & 3][col0 >> 5][key];
@@ -1038,12 +1077,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         is_key = age >= 0;
         if (!is_key) mw = 0u;
         if (A.W > 0 && seg_n - 1 - (int)p0 > oldest_age(A, seg_depth)) {
-          int t = t_first;
           uint32_t in = 0u;
-          for (int c = 0; c < 32 && col0 + c < srows; ++c) {
-            in |= (uint32_t)(age <= oldest_age(A, draft_depth(A, seg_b, t))) << c;
-            if (++t == A.T) t = 0;
-          }
+          for (int c = 0; c < 32; ++c)
+            in |= (uint32_t)(age <= oldest_age(A, __shfl_sync(0xffffffffu, row_depth, c))) << c;
           mw &= in;
         }
       }
