@@ -5,6 +5,8 @@
 Each ``csrc/*.cu`` compiles to an object under ``_build/`` (skipped when the
 object is newer than its sources), then all objects link into
 ``long_context_sparse_dim_b200/librtp.so`` with the static CUDA runtime.
+``csrc/py_calls.cpp`` (the native part of the Python binding) becomes
+``_calls.so`` beside it, against librtp.so and torch.
 """
 from __future__ import annotations
 
@@ -15,6 +17,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,6 +25,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "librtp.so")
+CALLS = os.path.join(PKG, "_calls.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -70,13 +74,33 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
         objs = list(ex.map(lambda s: _compile(s, extra, verbose or ptxas_info), srcs))
     newest = max(os.path.getmtime(o) for o in objs)
     if not os.path.exists(LIB) or os.path.getmtime(LIB) < newest:
-        cmd = [nvcc()] + ARCH + ["-shared", "-Xcompiler", "-fPIC", "-o", LIB] + objs
+        cmd = [nvcc()] + ARCH + ["-shared", "-Xcompiler", "-fPIC", "-Xlinker", "-soname=librtp.so", "-o", LIB] + objs
         if verbose:
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _build_calls(verbose)
     return LIB
+
+
+def _build_calls(verbose: bool) -> None:
+    src, header = os.path.join(CSRC, "py_calls.cpp"), os.path.join(INCLUDE, "rtp.h")
+    if os.path.exists(CALLS) and os.path.getmtime(CALLS) >= max(os.path.getmtime(p) for p in (src, header, __file__)):
+        return
+    import torch
+    tdir = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(tdir, "include"), "-I", os.path.join(cuda, "include"),
+           src, "-o", CALLS, LIB, "-L", os.path.join(tdir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
 
 
 def main(argv=None):

@@ -1,0 +1,217 @@
+// The short calls of a speculative step for Python: rtp_qk_norm_rope,
+// rtp_tree_attn and rtp_kv_accept straight from torch tensors.
+//
+// Their kernels take a few microseconds, and a call through ctypes spends 10 to
+// 15 on describing the tensors in Python (shape, strides and address are a
+// Python call each).  Here a description costs some 50 ns.  Everything else of
+// the binding stays in rtp.py; each function here returns the rtp_status.
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <ATen/core/Tensor.h>
+#include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAStream.h>
+
+#include <cstring>
+
+#include "rtp.h"
+
+namespace {
+
+// A Python exception that is already set.
+struct PyErrorSet {};
+
+[[noreturn]] void fail(PyObject* type, const std::string& what) {
+  PyErr_SetString(type, what.c_str());
+  throw PyErrorSet{};
+}
+
+std::string shape_text(c10::IntArrayRef s) {
+  std::string r = "(";
+  for (size_t i = 0; i < s.size(); ++i) r += (i ? ", " : "") + std::to_string(s[i]);
+  return r + (s.size() == 1 ? ",)" : ")");
+}
+
+const at::Tensor& tensor(PyObject* o, const char* name) {
+  if (!THPVariable_Check(o)) fail(PyExc_TypeError, std::string(name) + ": need a tensor");
+  return THPVariable_Unpack(o);
+}
+
+void check_device(const at::Tensor& t, int device, const char* name) {
+  if (!t.is_cuda() || t.get_device() != device)
+    fail(PyExc_ValueError, std::string(name) + ": tensor on " + t.device().str() +
+                               ": the call takes tensors of the current CUDA device");
+}
+
+// The current device, which every tensor of the call has to be on.
+int device_of(PyObject* o, const char* name) {
+  const at::Tensor& t = tensor(o, name);
+  if (!t.is_cuda()) check_device(t, -1, name);
+  return (int)c10::cuda::current_device();
+}
+
+// The description of an optional tensor of `ndim` dims.
+struct Desc {
+  rtp_tensor d;
+  const rtp_tensor* p = nullptr;
+  Desc(PyObject* o, int device, const char* name, int ndim = 4, bool optional = true) {
+    if (o == Py_None && optional) return;
+    const at::Tensor& t = tensor(o, name);
+    check_device(t, device, name);
+    if (t.dim() != ndim)
+      fail(PyExc_ValueError, std::string(name) + ": expected a " + std::to_string(ndim) + "-D tensor, got " +
+                                 shape_text(t.sizes()));
+    const at::ScalarType s = t.scalar_type();
+    if (s != at::kFloat && s != at::kBFloat16)
+      fail(PyExc_TypeError, std::string(name) + ": unsupported dtype " + c10::toString(s));
+    std::memset(&d, 0, sizeof(d));
+    d.data = t.data_ptr();
+    d.dtype = s == at::kBFloat16 ? RTP_BF16 : RTP_F32;
+    d.ndim = ndim;
+    for (int i = 0; i < ndim; ++i) {
+      d.shape[i] = t.size(i);
+      d.stride[i] = t.stride(i);
+    }
+    p = &d;
+  }
+};
+
+// The address of a contiguous array of one type and shape, which the C call describes by nothing else.
+void* array(PyObject* o, int device, const char* name, std::initializer_list<int64_t> shape,
+            at::ScalarType type = at::kInt, bool optional = true) {
+  if (o == Py_None && optional) return nullptr;
+  const at::Tensor& t = tensor(o, name);
+  check_device(t, device, name);
+  const c10::IntArrayRef want(shape.begin(), shape.size());
+  if (t.scalar_type() != type || t.sizes() != want || !t.is_contiguous())
+    fail(PyExc_ValueError, std::string(name) + ": need a contiguous " + c10::toString(type) + " tensor of shape " +
+                               shape_text(want) + ", got " + c10::toString(t.scalar_type()) + " " +
+                               shape_text(t.sizes()));
+  return t.data_ptr();
+}
+
+int32_t int32_of(PyObject* o, const char* name) {
+  const long long v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) throw PyErrorSet{};
+  if (v < INT32_MIN || v > INT32_MAX) fail(PyExc_ValueError, std::string(name) + ": outside int32");
+  return (int32_t)v;
+}
+
+float float_of(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw PyErrorSet{};
+  return (float)v;
+}
+
+// None: the current stream; a torch.cuda.Stream; or a raw handle.
+rtp_stream_t stream_of(PyObject* o) {
+  if (o == Py_None) return (rtp_stream_t)c10::cuda::getCurrentCUDAStream().stream();
+  PyObject* h = PyLong_Check(o) ? (Py_INCREF(o), o) : PyObject_GetAttrString(o, "cuda_stream");
+  if (!h) throw PyErrorSet{};
+  void* p = PyLong_AsVoidPtr(h);
+  Py_DECREF(h);
+  if (!p && PyErr_Occurred()) throw PyErrorSet{};
+  return (rtp_stream_t)p;
+}
+
+// Runs f, with its exceptions turned into Python's.
+template <typename F>
+PyObject* guarded(const char* name, Py_ssize_t got, Py_ssize_t want, F&& f) {
+  if (got != want) {
+    PyErr_Format(PyExc_TypeError, "%s: %zd arguments, need %zd", name, got, want);
+    return nullptr;
+  }
+  try {
+    return PyLong_FromLong(f());
+  } catch (const PyErrorSet&) {
+    return nullptr;
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+    return nullptr;
+  }
+}
+
+PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("qk_norm_rope", n, 12, [&]() -> rtp_status {
+    const int dev = device_of(a[0], "q");
+    const Desc q(a[0], dev, "q", 4, false), k(a[1], dev, "k"), qw(a[2], dev, "q_weight", 2),
+        kw(a[3], dev, "k_weight", 2), qo(a[7], dev, "q_out", 4, false), ko(a[8], dev, "k_out");
+    const int64_t B = q.d.shape[0], T = q.d.shape[2];
+    return rtp_qk_norm_rope(q.p, k.p, qw.p, kw.p, float_of(a[4]), (const int32_t*)array(a[5], dev, "pos", {B}),
+                            (const int32_t*)array(a[9], dev, "offs", {B, T}),
+                            (const double*)array(a[6], dev, "inv_freq", {64}, at::kDouble), int32_of(a[10], "pairing"),
+                            qo.p, ko.p, stream_of(a[11]));
+  });
+}
+
+PyObject* tree_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("tree_attn", n, 15, [&]() -> rtp_status {
+    const int dev = device_of(a[0], "q");
+    const Desc q(a[0], dev, "q", 4, false), k(a[1], dev, "k", 4, false), v(a[2], dev, "v", 4, false),
+        kn(a[4], dev, "k_new", 4, false), vn(a[5], dev, "v_new", 4, false), o(a[8], dev, "o", 4, false);
+    const int64_t B = q.d.shape[0], Hq = q.d.shape[1], T = q.d.shape[2];
+    const at::Tensor& mask = tensor(a[6], "tree_mask");
+    if (mask.dim() != 3)
+      fail(PyExc_ValueError, "tree_mask: need [B, T, words], got " + shape_text(mask.sizes()));
+    rtp_tree tree;
+    tree.mask_words = mask.size(2);
+    tree.mask = (const uint32_t*)array(a[6], dev, "tree_mask", {B, T, tree.mask_words});
+    tree.depth = (const int32_t*)array(a[10], dev, "depth", {B, T});
+    rtp_selection sel;
+    std::memset(&sel, 0, sizeof(sel));
+    if (a[13] != Py_None) {
+      const at::Tensor& m = tensor(a[13], "sel.mask");
+      sel.mask_words = m.dim() ? m.size(-1) : 0;
+      sel.mask = (uint32_t*)array(a[13], dev, "sel.mask", {B * Hq * T, sel.mask_words});
+    }
+    void* ws = nullptr;
+    size_t ws_bytes = 0;
+    if (a[9] != Py_None) {
+      const at::Tensor& w = tensor(a[9], "ws");
+      check_device(w, dev, "ws");
+      if (!w.is_contiguous()) fail(PyExc_ValueError, "ws: need a contiguous tensor");
+      ws = w.data_ptr();
+      ws_bytes = w.nbytes();
+    }
+    const int ring = PyObject_IsTrue(a[12]);
+    if (ring < 0) throw PyErrorSet{};
+    return rtp_tree_attn(q.p, k.p, v.p, (const int32_t*)array(a[3], dev, "lens", {B}), kn.p, vn.p, &tree,
+                         int32_of(a[11], "W"), ring, a[13] == Py_None ? nullptr : &sel, float_of(a[7]), o.p, ws,
+                         ws_bytes, stream_of(a[14]));
+  });
+}
+
+PyObject* kv_accept(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("kv_accept", n, 15, [&]() -> rtp_status {
+    const int dev = device_of(a[0], "k_new");
+    const Desc kn(a[0], dev, "k_new", 4, false), vn(a[1], dev, "v_new", 4, false), P(a[6], dev, "P", 3),
+        kc(a[7], dev, "k_cache"), vc(a[8], dev, "v_cache"), ki(a[9], dev, "k_idx"), kr(a[10], dev, "k_ring"),
+        vr(a[11], dev, "v_ring");
+    const int64_t B = kn.d.shape[0];
+    const at::Tensor& path = tensor(a[3], "path");
+    if (path.dim() != 2) fail(PyExc_ValueError, "path: need [B, A], got " + shape_text(path.sizes()));
+    const int64_t A = path.size(1);
+    if (A > INT32_MAX) fail(PyExc_ValueError, "path: too long");
+    return rtp_kv_accept(kn.p, vn.p, (const int32_t*)array(a[2], dev, "pos", {B}),
+                         (const int32_t*)array(a[3], dev, "path", {B, A}), (int32_t)A,
+                         (const int32_t*)array(a[4], dev, "count", {B}), int32_of(a[5], "R"), P.p, kc.p, vc.p, ki.p,
+                         kr.p, vr.p, (int32_t*)array(a[12], dev, "lens_out", {B}),
+                         (int32_t*)array(a[13], dev, "ring_lens", {B}), stream_of(a[14]));
+  });
+}
+
+PyMethodDef kMethods[] = {
+    {"qk_norm_rope", (PyCFunction)(void (*)())qk_norm_rope, METH_FASTCALL,
+     "(q, k, q_weight, k_weight, eps, pos, inv_freq, q_out, k_out, offs, pairing, stream) -> rtp_status"},
+    {"tree_attn", (PyCFunction)(void (*)())tree_attn, METH_FASTCALL,
+     "(q, k, v, lens, k_new, v_new, tree_mask, scale, o, ws, depth, W, ring, sel_mask, stream) -> rtp_status"},
+    {"kv_accept", (PyCFunction)(void (*)())kv_accept, METH_FASTCALL,
+     "(k_new, v_new, pos, path, count, R, P, k_cache, v_cache, k_idx, k_ring, v_ring, lens_out, ring_lens, stream)"
+     " -> rtp_status"},
+    {nullptr, nullptr, 0, nullptr}};
+
+PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_calls", "Short rtp calls on torch tensors.", -1, kMethods,
+                       nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__calls(void) { return PyModule_Create(&kModule); }

@@ -22,12 +22,12 @@
 // P and its rounding error go into one product as 128 columns (hi | lo).
 //   softmax  a thread holds one key and 32 query rows.  Exponentials are taken
 //            against a reference per row that is not the running maximum: the
-//            maximum over the first tile's keys, attended or not, and raised
-//            every 8 tiles where the sums have grown past 2^16.  fp32 and bf16
-//            share their exponent range, so any reference within 2^60 above and
-//            2^100 below the row's maximum gives the same precision, and a tile
-//            needs no reduction over keys and no exchange between warps.  A row
-//            outside that range shows in its sum and goes the scalar way below.
+//            logit of the first tile's first key, attended or not, raised every
+//            8 tiles where a sum has grown past 2^40.  fp32 and bf16 share their
+//            exponent range, so any reference within 2^60 above and 2^80 below
+//            the row's maximum gives the same precision, and a tile needs no
+//            reduction over keys and no exchange between warps.  A row outside
+//            that range shows in its sum and goes the scalar way below.
 //   O        is summed in TMEM over an epoch of 8 tiles (the tensor core
 //            truncates, so a long sum would drift), then added to a second TMEM
 //            tile by fp32 adds, and rescaled where references were raised.
@@ -67,10 +67,10 @@ constexpr int kTrHalf = kTrKeys * 128;       // 128 rows x 64 bf16, 128-byte swi
 constexpr int kTrTile = 2 * kTrHalf;         // one K or V tile: 32 KB
 constexpr int kTrLoadWarps = 4;
 constexpr int kTrEpoch = 8;                  // tiles summed in TMEM before an fp32 add
-constexpr float kTrHigh = 65536.f;           // a sum above it raises the row's reference
+constexpr float kTrHigh = 1.0995116e12f;     // 2^40: a sum above it raises the row's reference
 constexpr float kTrLow = 8.6736174e-19f;     // 2^-60: a sum below it has lost the row's largest terms
+constexpr float kTrTop = 1.2676506e30f;      // 2^100: a sum above it is past what a factor can scale down
 constexpr float kTrNone = -3.0e38f;          // log2 of an empty sum
-constexpr uint32_t kTrNoKey = 0x007fffffu;   // score_key(-inf)
 constexpr int kTrRound = 512;                // keys whose selection bits are read at a time
 constexpr int kTrQueue = 640;                // 128 left over + one round
 constexpr int kTrSms = 148;
@@ -105,11 +105,10 @@ struct TrSmem {
   alignas(16) float nref[2][kTrStream];  // minus the reference of each row (log2 units)
   alignas(16) float alpha[2][kTrStream];  // 2^(old - new reference) of the last raise; at a segment's end the row sums
   float wt[NR == 64 ? 2 : 1][2][NR == 64 ? kTrStream : 1];  // [stream writing][stream summed]: factors of its O
-  uint32_t colmax[2][kTrStream];         // a tile's row maxima (as score_key), or the largest sums (float bits)
+  uint32_t colmax[2][kTrStream];         // the largest sum of a row in any thread (float bits)
   uint64_t k_full[kTrStages], k_empty[kTrStages], v_full[kTrStages], v_empty[kTrStages];
   uint64_t s_full[2], s_free[2], p_full[2], p_free[2], o_free[2], sum_full[2], sum_free[2], sync[2];
   uint64_t q_full, q_free, fin;
-  uint32_t bad[2][2];            // rows with a result that is not finite
   int2 meta[kTrRing];            // per tile: its number in the group; 4 * segment + 2 * (CTA's last) + (segment's last)
   int4 cur[2];                   // each stream's scores: tile (-1: no more), and its meta
   int new_epoch[2];
@@ -118,8 +117,8 @@ struct TrSmem {
   int state[2];                  // at a segment's end: 1 the stream has an O, 2 and a total
   uint32_t tmem_base;
   int start_b;
-  int64_t start_base;
-  int64_t total, per;            // tiles of the whole line, and of a range
+  int start_base;
+  int total, per;                // tiles of the whole line, and of a range
   int cnt[2][kTrLoadWarps];
   TrSegInfo seg[kTrRing];
   int qkey[kQueue];              // selected keys waiting for a tile (ring)
@@ -140,6 +139,21 @@ template <int N>
 RTP_DEVICE void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
 template <int N>
 RTP_DEVICE void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
+
+// mbar_wait, kept small: the code of a CTA has to stay in the instruction cache, and most of it runs once or twice.
+RTP_DEVICE bool wait_bar(uint64_t* bar, uint32_t parity, bool& alive, const TreeAttnArgs& A) {
+  if (!alive) return false;
+  if (mbar_try(bar, parity)) return true;
+  const long long t0 = clock64();
+#pragma unroll 1
+  while (!mbar_try(bar, parity))
+    if (clock64() - t0 > A.budget) {
+      atomicExch(A.err, kDevErrTimeout);
+      alive = false;
+      break;
+    }
+  return alive;
+}
 
 // Barrier of n threads that also ORs a predicate.
 RTP_DEVICE bool bar_or(int id, int n, bool x) {
@@ -195,14 +209,6 @@ RTP_DEVICE float reduce_columns(float (&x)[2 * O], int lane, F op) {
     return y[0];
   else
     return reduce_columns<O / 2>(y, lane, op);
-}
-
-// The same for 16 columns, left in lanes c and c + 16.
-template <typename F>
-RTP_DEVICE float reduce_columns16(float (&x)[16], int lane, F op) {
-#pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = op(x[i], __shfl_xor_sync(0xffffffffu, x[i], 16));
-  return reduce_columns<8>(x, lane, op);
 }
 
 // Bit c of lane k becomes bit k of lane c.
@@ -276,33 +282,33 @@ struct TrSeg {
   int b, kvh;
   TrSpan span;
   int u0, u1;
-  int64_t base;  // the line's tile number of the group's tile 0
+  int base;  // the line's tile number of the group's tile 0
 };
 
 // Walks the segments of the range [lo, hi) of the line of tiles.
 template <bool SEL>
 struct TrWalk {
-  int64_t pos, hi, base_b;
+  int pos, hi, base_b;
   TrSeg s;
-  RTP_DEVICE void start(const TreeAttnArgs& A, int64_t lo, int64_t end, int b, int64_t base) {
+  RTP_DEVICE void start(const TreeAttnArgs& A, int lo, int end, int b, int base) {
     pos = lo;
     hi = end;
     base_b = base;
     s.b = b;
     s.span = span_of<SEL>(A, b);
-    s.kvh = (int)((lo - base) / s.span.tiles);
+    s.kvh = (lo - base) / s.span.tiles;
     fill();
   }
   RTP_DEVICE void fill() {
-    s.base = base_b + (int64_t)s.kvh * s.span.tiles;
-    s.u0 = (int)(pos - s.base);
-    s.u1 = (int)min((int64_t)s.span.tiles, hi - s.base);
+    s.base = base_b + s.kvh * s.span.tiles;
+    s.u0 = pos - s.base;
+    s.u1 = min(s.span.tiles, hi - s.base);
   }
   RTP_DEVICE bool next(const TreeAttnArgs& A) {
     pos = s.base + s.u1;
     if (pos >= hi) return false;
     if (++s.kvh == A.Hk) {
-      base_b += (int64_t)A.Hk * s.span.tiles;
+      base_b += A.Hk * s.span.tiles;
       s.kvh = 0;
       s.span = span_of<SEL>(A, ++s.b);
     }
@@ -335,11 +341,13 @@ __device__ __noinline__ void scalar_row(const TreeAttnArgs& A, int b, int h, int
   const int lo = A.W > 0 ? max(0, n - 1 - oldest_age(A, depth)) : 0;  // (past n when the window holds none)
   const uint32_t* sel = A.sel ? A.sel + ((int64_t)(b * A.Hq + h) * A.T + t) * A.sel_words : nullptr;
   if (A.W <= 0 || oldest_age(A, depth) >= 0)
+#pragma unroll 1
     for (int p = lo; p < n; ++p) {
       if (sel && !((__ldg(sel + (p >> 5)) >> (p & 31)) & 1u)) continue;
       const int r = row_of(A, (uint32_t)p);
       take(row(A.k, kvh, r), row(A.v, kvh, r));
     }
+#pragma unroll 1
   for (int j = 0; j < A.T; ++j) {
     if (!tree_bit(A, b, t, j)) continue;
     if (A.W > 0 && draft_depth(A, b, j) <= depth - A.W) continue;
@@ -414,6 +422,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   const int rows = A.G * A.T, row0 = rb * NR, nrows = min(NR, rows - row0);
 
   if (tid == 0) {
+#pragma unroll 1
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.k_full[i], 1);
       mbar_init(&S.k_empty[i], 1);
@@ -427,7 +436,6 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       mbar_init(&S.sum_full[i], 8);
       mbar_init(&S.sum_free[i], 8);
       mbar_init(&S.sync[i], 8);
-      S.bad[i][0] = S.bad[i][1] = 0u;
       S.raise[i][0] = S.raise[i][1] = 0;
       S.seen[i][0] = S.seen[i][1] = 0u;
     }
@@ -436,10 +444,12 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     mbar_init(&S.fin, 1);
     mbar_fence_init();
   }
+  if (tid < 2 * kTrStream) S.colmax[0][tid] = 0u;
   if (warp == 0) tmem_alloc(&S.tmem_base, kTmemCols);
   // rows past the last one never get a P: zeros
   if (nrows < NR) {
     uint4* p = reinterpret_cast<uint4*>(&S.p[0][0][0]);
+#pragma unroll 1
     for (int i = tid; i < (int)(sizeof(S.p) / 16); i += kTrThreads) p[i] = make_uint4(0u, 0u, 0u, 0u);
     fence_async();
   }
@@ -448,24 +458,26 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
 
   // ---- this CTA's range of the line of tiles ----
   if (warp == 0) {
-    int64_t sum = 0;
+    int sum = 0;
     const int first = lane < A.B ? span_of<SEL>(A, lane).tiles : 0;
+#pragma unroll 1
     for (int b = lane; b < A.B; b += 32) sum += b == lane ? first : span_of<SEL>(A, b).tiles;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const int64_t total = sum * A.Hk, per = (total + W.ranges - 1) / W.ranges, lo = range * per;
+    const int total = sum * A.Hk, per = (total + W.ranges - 1) / W.ranges, lo = range * per;
     if (lane == 0) {
       S.total = total;
       S.per = per;
     }
-    int64_t base = 0;
+    int base = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < A.B && lo < total; b0 += 32) {
       const int b = b0 + lane;
-      const int64_t mine = (int64_t)(b0 == 0 ? first : b < A.B ? span_of<SEL>(A, b).tiles : 0) * A.Hk;
-      int64_t incl = mine;
+      const int mine = (b0 == 0 ? first : b < A.B ? span_of<SEL>(A, b).tiles : 0) * A.Hk;
+      int incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += y;
       }
       const uint32_t past = __ballot_sync(0xffffffffu, base + incl > lo);
@@ -483,7 +495,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = S.tmem_base;
-  const int64_t per = S.per, lo = range * per, hi = min(lo + per, S.total);
+  const int per = S.per, lo = range * per, hi = min(lo + per, S.total);
   const bool work = lo < hi;
 
   bool alive = true;
@@ -501,14 +513,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     bool q_due = false;
     // Waits for a free K or V stage; false (for all loaders alike) once any wait gave up.
     auto stage_free = [&](uint64_t* empty) {
-      const bool ok = mbar_wait(&empty[it & 1], ((it >> 1) & 1u) ^ 1u, alive, A.err, A.budget);
+      const bool ok = wait_bar(&empty[it & 1], ((it >> 1) & 1u) ^ 1u, alive, A);
       return !bar_or(kBarLoad, kTrLoad, !ok);
     };
     // 128 rows of K or V by cp.async: row_at(r, ok) gives the row of tile row r.
     auto copy_rows = [&](const View4& x, uint8_t* tile, const TrSeg& s, auto&& row_at) {
       const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(x.data) + s.b * x.sb + s.kvh * x.sh + chunk * 8;
       const uint32_t dst = smem_addr(tile) + slot_kv;
-#pragma unroll 4
+#pragma unroll 2
       for (int i = 0; i < 16; ++i) {
         bool ok;
         const int row = row_at(r_first + 8 * i, ok);
@@ -527,19 +539,22 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     };
     auto gather = [&](const View4& xk, const View4& xv, const TrSeg& s, int u, int flags, auto&& row_at) -> bool {
       const int st = it & 1;
-      if (!stage_free(S.k_empty)) return false;
-      if (lt == 0) S.meta[it % kTrRing] = make_int2(u, flags);
-      copy_rows(xk, S.k[st], s, row_at);
-      const bool now = !bar_or(kBarLoad, kTrLoad, !mbar_try(&S.v_empty[st], ((it >> 1) & 1u) ^ 1u));
-      if (now) {
-        copy_rows(xv, S.v[st], s, row_at);
+      bool k_there = false;
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i) {
+        // K is handed on before a wait for V's stage, else with V on its way
+        if (i == 1 && bar_or(kBarLoad, kTrLoad, !mbar_try(&S.v_empty[st], ((it >> 1) & 1u) ^ 1u))) {
+          cp_wait<0>();
+          landed(&S.k_full[st]);
+          k_there = true;
+        }
+        if (!stage_free(i ? S.v_empty : S.k_empty)) return false;
+        if (i == 0 && lt == 0) S.meta[it % kTrRing] = make_int2(u, flags);
+        copy_rows(i ? xv : xk, i ? S.v[st] : S.k[st], s, row_at);
+      }
+      if (!k_there) {
         cp_wait<1>();
         landed(&S.k_full[st]);
-      } else {
-        cp_wait<0>();
-        landed(&S.k_full[st]);
-        if (!stage_free(S.v_empty)) return false;
-        copy_rows(xv, S.v[st], s, row_at);
       }
       cp_wait<0>();
       landed(&S.v_full[st]);
@@ -549,17 +564,18 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     TrWalk<SEL> walk;
     bool more = work, ok = true;
     if (more) walk.start(A, lo, hi, S.start_b, S.start_base);
+#pragma unroll 1
     while (more && ok) {
       const TrSeg s = walk.s;
       more = walk.next(A);
       const int seg_flags = 4 * segs, last_flags = seg_flags + 1 + (more ? 0 : 2);
       // ---- the query rows (the previous segment's products are done with the buffer) ----
       {
-        const bool free = segs == 0 || mbar_wait(&S.q_free, (segs - 1) & 1u, alive, A.err, A.budget);
+        const bool free = segs == 0 || wait_bar(&S.q_free, (segs - 1) & 1u, alive, A);
         if (bar_or(kBarLoad, kTrLoad, !free)) break;
         const __nv_bfloat16* qb =
             static_cast<const __nv_bfloat16*>(A.q.data) + s.b * A.q.sb + (int64_t)s.kvh * A.G * A.q.sh + chunk * 8;
-#pragma unroll 4
+#pragma unroll 2
         for (int i = 0; i < NR / 8; ++i) {
           const int r = r_first + 8 * i, rr = min(row0 + r, rows - 1);
           const int g = rr / A.T, t = rr - g * A.T;
@@ -578,6 +594,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         info.draft_tiles = s.span.draft_tiles;
         info.max_depth = 0;
         if (A.W > 0) {
+#pragma unroll 1
           for (int t = lane; t < A.T; t += 32) info.max_depth = max(info.max_depth, draft_depth(A, s.b, t));
           info.max_depth = __reduce_max_sync(0xffffffffu, info.max_depth);
         }
@@ -587,7 +604,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         if (lt == 0) {
           S.seg[segs % kTrRing] = info;
           if (s.u0 == 0 && rb == 0)
-            W.table[s.b * A.Hk + s.kvh] = make_int2(range, (int)((s.base + s.span.tiles - 1) / per) - range + 1);
+            W.table[s.b * A.Hk + s.kvh] = make_int2(range, (s.base + s.span.tiles - 1) / per - range + 1);
         }
         ++segs;
       }
@@ -612,12 +629,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
           tma_load_4d(tile + kTrHalf, map, full, 64, first, s.kvh, s.b);
         };
         bool ahead = false;  // this tile's K is already on its way
+#pragma unroll 1
         for (int u = max(s.u0, s.span.draft_tiles); u < s.u1 && ok; ++u) {
           uint32_t p0;
           int left, first;
           const int st = it & 1;
           if (by_tma(u, p0, left, first)) {
             // the next tile's K before this one's V: scores are computed ahead of the products with V
+#pragma unroll 1
             for (int i = ahead ? 1 : 0; i < 2 && ok; ++i) {
               uint32_t q0;
               int rest, at;
@@ -840,6 +859,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       // Whichever is ready, in each line's order (a stream's scores come after it has read the ones before).
       uint32_t so = 0, po = 0, ops = 0;  // (two more score ops than ops: the ends)
       long long since = clock64();
+#pragma unroll 1
       while (!end || po < ops || so < ops + 2) {
         bool moved = false;
         if (!end) {
@@ -885,7 +905,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     uint64_t scale2;
     asm("mov.b64 %0, {%1, %1};\n" : "=l"(scale2) : "f"(A.scale_log2));
     auto wait_warp = [&](uint64_t* b, uint32_t parity) {
-      if (!__all_sync(0xffffffffu, mbar_wait(b, parity & 1u, alive, A.err, A.budget))) alive = false;
+      if (!__all_sync(0xffffffffu, wait_bar(b, parity & 1u, alive, A))) alive = false;
     };
     auto arrive_warp = [&](uint64_t* b) {
       __syncwarp();
@@ -909,6 +929,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     bool has = false, has_total = false;  // the stream has taken a tile of it; its epochs have a total
     int in_epoch = 0;
     uint32_t n = 0, checks = 0;           // ops of this stream so far; epochs whose sums were looked at
+#pragma unroll 1
     while (work) {
       wait_warp(&S.s_full[x], n);
       if (!alive) break;
@@ -916,6 +937,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       const bool turn = n == 0 || seg < (cur.z >> 2);
 
       // ---- segments that ended before this tile: row sums over all keys, then O ----
+#pragma unroll 1
       for (; seg < (cur.z >> 2); ++seg) {
         const TrSegInfo& info = S.seg[seg % kTrRing];
         if (has) {
@@ -925,52 +947,50 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         seen = __reduce_or_sync(0xffffffffu, seen);
         if (lane == 0 && seen) atomicOr(&S.seen[x][col0 >> 5], seen);
         seen = 0u;
-        float l[32];
+        // (the stream's P tile is free: 128 keys x 64 rows of partial sums, pairs of rows by key)
+        float* scratch = reinterpret_cast<float*>(&S.p[x][0][0]);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          unpack2(l2[i], l[2 * i], l[2 * i + 1]);
+          reinterpret_cast<uint64_t*>(scratch)[(col0 / 2 + i) * kTrKeys + key] = l2[i];
           l2[i] = 0ull;
         }
-        const float lsum = reduce_columns<16>(l, lane, [](float a, float b) { return a + b; });
-        // (the stream's P tile is free: the four warps of a row leave their sums in it)
-        auto part = [&](int w, int c) {
-          const int r = 16 * w + (c >> 2);
-          return reinterpret_cast<float*>(&S.p[x][0][r * 128 + ((r & 7) << 4) + 4 * (c & 3)]);
-        };
-        if (has) *part(quad, col0 + lane) = lsum;
         sync();
+        const int row = sc >> 2;  // four threads a row, 32 keys each
         float sum = 0.f;
-        if (sc < kTrStream && has) sum = ((*part(0, sc) + *part(1, sc)) + *part(2, sc)) + *part(3, sc);
-        const bool seen_row = sc < kTrStream && ((S.seen[x][sc >> 5] >> (sc & 31)) & 1u);
-        // log2 of a row's sum (a NaN if it has lost the row's largest terms, or is one)
-        const float lse = !seen_row ? kTrNone : sum >= kTrLow ? log2f(sum) - S.nref[x][sc] : __int_as_float(0x7fffffff);
+#pragma unroll 4
+        for (int i = 0; i < 32; ++i)
+          sum += scratch[((row >> 1) * kTrKeys + 32 * (sc & 3) + ((i + lane) & 31)) * 2 + (row & 1)];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        const bool mine = (sc & 3) == 0, seen_row = (S.seen[x][row >> 5] >> (row & 31)) & 1u;
+        // log2 of a row's sum (infinite if that has left its range, or is a NaN: all that it meets becomes a NaN)
+        const bool fits = sum >= kTrLow && sum <= kTrTop;
+        const float lse = !seen_row ? kTrNone : fits ? log2f(sum) - S.nref[x][row] : INFINITY;
         float whole_lse = lse;
         if constexpr (kSplitRows) {
-          if (sc < kTrStream) alpha[sc] = !seen_row ? 0.f : sum >= kTrLow ? 1.f / sum : __int_as_float(0x7fffffff);
+          if (mine) alpha[row] = !seen_row ? 0.f : fits ? 1.f / sum : __int_as_float(0x7fffffff);
         } else {  // the other stream's
-          if (sc < kTrStream) alpha[sc] = lse;
+          if (mine) alpha[row] = lse;
           if (sc == 0) S.state[x] = (has ? 1 : 0) + (has_total ? 2 : 0);
           tc_fence_before();
           arrive_warp(&S.sum_full[x]);
           wait_warp(&S.sum_full[x], (uint32_t)seg);
           wait_warp(&S.sum_full[x ^ 1], (uint32_t)seg);
           tc_fence_after();
-          if (sc < kTrStream) {
-            const float a = S.alpha[0][sc], b = S.alpha[1][sc], m = a > b ? a : b;  // (a NaN of either stays one)
+          if (mine) {
+            const float a = S.alpha[0][row], b = S.alpha[1][row], m = fmaxf(a, b);
             const float both = ex2a(a - m) + ex2a(b - m), inv = 1.f / both;
-            S.wt[x][0][sc] = a <= kTrNone ? 0.f : ex2a(-S.nref[0][sc] - m) * inv;
-            S.wt[x][1][sc] = b <= kTrNone ? 0.f : ex2a(-S.nref[1][sc] - m) * inv;
-            whole_lse = m <= kTrNone && both >= 0.f ? kTrNone : m + log2f(both);
+            S.wt[x][0][row] = a <= kTrNone ? 0.f : ex2a(-S.nref[0][row] - m) * inv;
+            S.wt[x][1][row] = b <= kTrNone ? 0.f : ex2a(-S.nref[1][row] - m) * inv;
+            whole_lse = m <= kTrNone || m == INFINITY ? m : m + log2f(both);
           }
         }
         if (!alive) break;
-        if (info.slot >= 0 && sc < srows && (kSplitRows || x == 0))
-          W.lse[(int64_t)info.slot * NR + row_base - row0 + sc] = whole_lse;
+        if (info.slot >= 0 && mine && row < srows && (kSplitRows || x == 0))
+          W.lse[(int64_t)info.slot * NR + row_base - row0 + row] = whole_lse;
         sync();
         // eight rows at a time: all 32 of this thread's, or 16 when the streams share them
         const int c_first = kSplitRows ? col0 : col0 + 16 * x;
-        uint32_t bad = 0u;
-        int g = (row_base + c_first) / A.T, t = row_base + c_first - g * A.T;
 #pragma unroll 1
         for (int c0 = c_first; c0 < c_first + (kSplitRows ? 32 : 16) && c0 < srows; c0 += 8) {
           float y[8];
@@ -997,24 +1017,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
             }
           }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (c0 + i < srows) {
-              if (info.slot < 0) {
-                bad |= (uint32_t)!isfinite(y[i]) << (c0 + i - c_first);
-                const int64_t off = info.b * A.o.sb + (int64_t)(info.kvh * A.G + g) * A.o.sh + t * A.o.sn + key;
-                if (A.o_bf16)
-                  static_cast<__nv_bfloat16*>(A.o.data)[off] = __float2bfloat16_rn(y[i]);
-                else
-                  static_cast<float*>(A.o.data)[off] = y[i];
-              } else {
-                W.o[((int64_t)info.slot * NR + row_base - row0 + c0 + i) * kHeadDim + key] = y[i];
-              }
-            }
-            if (++t == A.T) {
-              t = 0;
-              ++g;
-            }
-          }
+          for (int i = 0; i < 8; ++i) scratch[(c0 + i) * kHeadDim + key] = y[i];
         }
         tc_fence_before();
         if constexpr (!kSplitRows) {  // both streams are done with each other's sums
@@ -1022,21 +1025,31 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
           wait_warp(&S.sum_free[x], (uint32_t)seg);
         }
         if (has) arrive_warp(&S.o_free[x]);
-        bad = __reduce_or_sync(0xffffffffu, bad);
-        if (lane == 0 && bad) atomicOr(&S.bad[x][col0 >> 5], bad);
-        sync();  // (from here on the stream's arrays are the next segment's)
-        if (S.bad[x][0] | S.bad[x][1]) {
-          for (int i = warp & 7; i < 64; i += 8)
-            if ((S.bad[x][i >> 5] >> (i & 31)) & 1u) {
-              const int c = (kSplitRows ? 0 : 16 * x) + i, r = row_base + c, h = info.kvh * A.G + r / A.T;
-              float4 y;
-              scalar_row(A, info.b, h, r % A.T, y);
-              store_row4(A, info.b, h, r % A.T, lane, y);
-            }
-          sync();
+        sync();
+        // a warp per row: out, or to where the pieces of the group meet
+#pragma unroll 1
+        for (int i = warp & 7; i < (kSplitRows ? 64 : 32); i += 8) {
+          const int c = kSplitRows ? i : (i & 15) + 32 * (i >> 4) + 16 * x;  // (the rows whose columns were this stream's)
+          if (c >= srows) continue;
+          float4 y = reinterpret_cast<const float4*>(scratch)[c * 32 + lane];
+          const int r = row_base + c, h = info.kvh * A.G + r / A.T, t = r % A.T;
+          if (info.slot >= 0) {
+            reinterpret_cast<float4*>(W.o)[((int64_t)info.slot * NR + row_base - row0 + c) * 32 + lane] = y;
+          } else {
+            if (__any_sync(0xffffffffu, !finite4(y))) scalar_row(A, info.b, h, t, y);
+            store_row4(A, info.b, h, t, lane, y);
+          }
         }
-        if (sc < 2) S.bad[x][sc] = S.seen[x][sc] = 0u;
+        if (srows < kTrStream) {  // P's columns past the last row are zeros again
+          sync();
+#pragma unroll 1
+          for (int i = sc; i < kTrKeys * kTrStream / 4; i += kTrSoft)
+            reinterpret_cast<uint4*>(scratch)[i] = make_uint4(0u, 0u, 0u, 0u);
+          fence_async();
+        }
+        if (sc < 2) S.seen[x][sc] = 0u;
         has = has_total = false;
+        sync();  // (from here on the stream's arrays are the next segment's)
       }
       if (cur.x < 0 || !alive) break;
       if (turn) {
@@ -1065,6 +1078,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         if (A.W > 0 && seg_depth >= A.W) {
           const int dj = is_key ? draft_depth(A, seg_b, j) : 0;
           uint32_t in = 0u;
+#pragma unroll 4
           for (int c = 0; c < 32; ++c) in |= (uint32_t)(dj > __shfl_sync(0xffffffffu, row_depth, c) - A.W) << c;
           mw &= in;
         }
@@ -1078,6 +1092,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         if (!is_key) mw = 0u;
         if (A.W > 0 && seg_n - 1 - (int)p0 > oldest_age(A, seg_depth)) {
           uint32_t in = 0u;
+#pragma unroll 4
           for (int c = 0; c < 32; ++c)
             in |= (uint32_t)(age <= oldest_age(A, __shfl_sync(0xffffffffu, row_depth, c))) << c;
           mw &= in;
@@ -1089,27 +1104,21 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       bool raise = false;
       tc_fence_after();
       if (!has) {
-        // the references: each row's largest finite logit over the tile's keys
-        if (sc < kTrStream) colmax[sc] = kTrNoKey;
-        sync();
+        // the references: each row's logit of the tile's first key
+        if (quad == 0) {
 #pragma unroll 1
-        for (int hh = 0; hh < act; ++hh) {
-          uint32_t v[16];
-          float d[16];
-          tmem_ld16(my_base + 16u * hh, v);
-          tmem_wait(v);
+          for (int hh = 0; hh < act; ++hh) {
+            uint32_t v[16];
+            tmem_ld16(my_base + 16u * hh, v);
+            tmem_wait(v);
+            if (lane == 0) {
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            d[c] = __uint_as_float(v[c]) * A.scale_log2;
-            if (!is_key || !(fabsf(d[c]) < 1e30f)) d[c] = -INFINITY;
+              for (int c = 0; c < 16; ++c) {
+                const float y = __uint_as_float(v[c]) * A.scale_log2;
+                S.nref[x][col0 + 16 * hh + c] = is_key && fabsf(y) < 1e30f ? -y : 0.f;
+              }
+            }
           }
-          const float m = reduce_columns16(d, lane, [](float a, float b) { return fmaxf(a, b); });
-          if (lane < 16) atomicMax(&colmax[col0 + 16 * hh + lane], score_key(m));
-        }
-        sync();
-        if (sc < kTrStream) {
-          S.nref[x][sc] = colmax[sc] == kTrNoKey ? 0.f : -key_score(colmax[sc]);
-          colmax[sc] = 0u;
         }
         sync();
       } else if (fresh) {
@@ -1132,9 +1141,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         if (raise) {
           if (sc < kTrStream) {
             const float up = __uint_as_float(colmax[sc]);
-            const float by = up > kTrHigh && up < INFINITY ? (float)ilogbf(up) : 0.f;
+            const float by = up > kTrHigh ? (float)ilogbf(up) : 0.f;
             S.nref[x][sc] -= by;
-            alpha[sc] = ex2a(-by);
+            alpha[sc] = up <= kTrTop ? ex2a(-by) : __int_as_float(0x7fffffff);  // (out of range: the scalar way)
           }
           sync();
 #pragma unroll
@@ -1275,10 +1284,10 @@ __global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const __grid_
   const bool join = pieces.y > 1;  // (one piece: its CTA has written the output)
   float m = kTrNone, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  // one more piece (or partial join) of weight 2^s l (a NaN of either reaches the sum)
+  // one more piece (or partial join) of weight 2^s l (an infinite s makes the sum a NaN)
   auto take = [&](float s, float w, const float4& y, float mn) {
     const float f = s <= kTrNone ? 0.f : ex2a(s - mn);
-    if (f == 0.f) return;  // (what it holds may be anything)
+    if (f == 0.f && w == w) return;  // (what it holds may be anything)
     l += f * w;
     o = make_float4(o.x + f * y.x, o.y + f * y.y, o.z + f * y.z, o.w + f * y.w);
   };

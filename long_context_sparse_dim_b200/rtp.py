@@ -1,4 +1,5 @@
-"""ctypes binding of librtp.so (include/rtp.h): argument marshalling only.
+"""Binding of librtp.so (include/rtp.h): argument marshalling only, by ctypes (and
+natively, csrc/py_calls.cpp, for the calls whose kernels take a few microseconds).
 
 Every function here has the C name without the ``rtp_`` prefix, takes torch
 tensors that already live on the GPU, turns them into ``rtp_tensor``
@@ -10,7 +11,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -78,10 +78,9 @@ def _load() -> ctypes.CDLL:
         "rtp_sparse_attn_decode_range": ([T, T, T, vp, S, i64, f32, T, T, vp, sz, vp], i32),
         "rtp_attn_combine": ([T, T, T, vp], i32),
         "rtp_kv_append": ([T, T, vp, i32, T, T, T, T, T, T, vp, vp, vp], i32),
-        # (structures by address: the binding packs them as bytes)
-        "rtp_kv_accept": ([vp, vp, vp, vp, i32, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp], i32),
-        "rtp_qk_norm_rope": ([vp, vp, vp, vp, f32, vp, vp, vp, i32, vp, vp, vp], i32),
-        "rtp_tree_attn": ([vp, vp, vp, vp, vp, vp, vp, i32, i32, vp, f32, vp, vp, sz, vp], i32),
+        "rtp_kv_accept": ([T, T, vp, vp, i32, vp, i32, T, T, T, T, T, T, vp, vp, vp], i32),
+        "rtp_qk_norm_rope": ([T, T, T, T, f32, vp, vp, vp, i32, T, T, vp], i32),
+        "rtp_tree_attn": ([T, T, T, vp, T, T, P(RtpTree), i32, i32, S, f32, T, vp, sz, vp], i32),
         "rtp_tree_attn_workspace_size": ([i64, i64, i64, i64, i64], sz),
         "rtp_poll_device_error": ([P(i32)], i32),
         "rtp_set_wait_budget_cycles": ([i64], i32),
@@ -97,6 +96,9 @@ def _load() -> ctypes.CDLL:
 
 
 _lib = _load()
+
+# The short calls of a speculative step marshal natively (csrc/py_calls.cpp).
+from long_context_sparse_dim_b200 import _calls  # noqa: E402  (after librtp.so, which it links)
 
 
 def lib() -> ctypes.CDLL:
@@ -219,84 +221,22 @@ def kv_append(k_new, v_new, pos, R: int, P=None, k_cache=None, v_cache=None, k_i
                                                lens_out, ring_lens, stream, keep)), "rtp_kv_append")
 
 
-# The calls of a speculative step are short (a few microseconds on the GPU), so their descriptors are packed
-# in one go (an RtpTensor is ten 64-bit words) instead of field by field: 0.8 us a tensor against 3.3 us.
-_PACK = struct.Struct("10q").pack
-_PAD = {2: (0, 0), 3: (0,), 4: ()}
-_PACK3, _PACK5 = struct.Struct("3q").pack, struct.Struct("5q").pack  # rtp_tree, rtp_selection
-_DTYPES = {torch.float32: RTP_F32, torch.bfloat16: RTP_BF16}
-
-
-def _packed(t: Optional[torch.Tensor], dev: int, ndim: int = 4):
-    """An rtp_tensor as bytes; the tensor must be on CUDA device ``dev``."""
-    if t is None:
-        return None
-    if t.get_device() != dev:
-        raise ValueError(f"tensor on {t.device}: the call takes tensors of the current CUDA device")
-    if t.dim() != ndim:
-        raise ValueError(f"expected a {ndim}-D tensor, got {tuple(t.shape)}")
-    dt = _DTYPES.get(t.dtype)
-    if dt is None:
-        raise TypeError(f"unsupported dtype {t.dtype}")
-    if ndim == 4:
-        return _PACK(t.data_ptr(), dt | ndim << 32, *t.shape, *t.stride())
-    pad = _PAD[ndim]
-    return _PACK(t.data_ptr(), dt | ndim << 32, *t.shape, *pad, *t.stride(), *pad)
-
-
-def _ints(t: Optional[torch.Tensor], dev: int, shape, name: str, dtype=torch.int32):
-    """Address of a plain device array, which the C call describes by nothing else."""
-    if t is None:
-        return None
-    if t.get_device() != dev:
-        raise ValueError(f"{name} on {t.device}: the call takes tensors of the current CUDA device")
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name}: need a contiguous {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
-                         f"{tuple(t.shape)}")
-    return t.data_ptr()
-
-
-def _device_of(t: torch.Tensor) -> int:
-    """The current CUDA device, which the call's tensors have to be on."""
-    if not t.is_cuda:
-        raise ValueError(f"tensor on {t.device}: the call takes tensors of the current CUDA device")
-    return torch.cuda.current_device()
-
-
-def _kv_accept_args(k_new, v_new, pos, path, count, R, P, k_cache, v_cache, k_idx, k_ring, v_ring, lens_out,
-                    ring_lens, stream):
-    d = _device_of(k_new)
-    B = k_new.shape[0]
-    if path.dim() != 2:
-        raise ValueError(f"path: need [B, A], got {tuple(path.shape)}")
-    A = path.shape[1]
-    return [_packed(k_new, d), _packed(v_new, d), _ints(pos, d, (B,), "pos"), _ints(path, d, (B, A), "path"), A,
-            _ints(count, d, (B,), "count"), R, _packed(P, d, 3), _packed(k_cache, d), _packed(v_cache, d),
-            _packed(k_idx, d), _packed(k_ring, d), _packed(v_ring, d), _ints(lens_out, d, (B,), "lens_out"),
-            _ints(ring_lens, d, (B,), "ring_lens"), _stream(stream)]
-
-
 def kv_accept(k_new, v_new, pos, path, count, R: int, P=None, k_cache=None, v_cache=None, k_idx=None, k_ring=None,
               v_ring=None, lens_out=None, ring_lens=None, stream=None) -> None:
     """Append the accepted drafts of each sequence: rows path[b, :count[b]] (path
     int32 [B, A], count int32 [B]) of k_new, v_new [B, H, T, 128], in that order, to
     the caches, projected keys and rings, as kv_append appends whole rows."""
-    _check(_lib.rtp_kv_accept(*_kv_accept_args(k_new, v_new, pos, path, count, R, P, k_cache, v_cache, k_idx, k_ring,
-                                               v_ring, lens_out, ring_lens, stream)), "rtp_kv_accept")
+    _check(_calls.kv_accept(k_new, v_new, pos, path, count, R, P, k_cache, v_cache, k_idx, k_ring, v_ring, lens_out,
+                            ring_lens, stream), "rtp_kv_accept")
 
 
 ROPE_PAIRING = {"half": 0, "adjacent": 1}
 
 
-def _qk_norm_rope_args(q, k, q_weight, k_weight, eps, pos, inv_freq, q_out, k_out, offs, pairing, stream):
-    d = _device_of(q)
-    if pairing not in ROPE_PAIRING:
-        raise ValueError(f"pairing must be one of {tuple(ROPE_PAIRING)}, got {pairing!r}")
-    B, T = q.shape[0], q.shape[2]
-    return [_packed(q, d), _packed(k, d), _packed(q_weight, d, 2), _packed(k_weight, d, 2), eps,
-            _ints(pos, d, (B,), "pos"), _ints(offs, d, (B, T), "offs"),
-            _ints(inv_freq, d, (64,), "inv_freq", torch.float64), ROPE_PAIRING[pairing], _packed(q_out, d),
-            _packed(k_out, d), _stream(stream)]
+def _pairing(name: str) -> int:
+    if name not in ROPE_PAIRING:
+        raise ValueError(f"pairing must be one of {tuple(ROPE_PAIRING)}, got {name!r}")
+    return ROPE_PAIRING[name]
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, eps: float, pos, inv_freq, q_out, k_out, offs=None,
@@ -306,32 +246,18 @@ def qk_norm_rope(q, k, q_weight, k_weight, eps: float, pos, inv_freq, q_out, k_o
     (may be q, k).  Token t sits at pos[b] + t, or pos[b] + offs[b, t]; inv_freq is
     float64 [64] in radians per position; pairing "half" turns dims (i, i + 64),
     "adjacent" (2i, 2i + 1)."""
-    _check(_lib.rtp_qk_norm_rope(*_qk_norm_rope_args(q, k, q_weight, k_weight, eps, pos, inv_freq, q_out, k_out, offs,
-                                                     pairing, stream)), "rtp_qk_norm_rope")
+    _check(_calls.qk_norm_rope(q, k, q_weight, k_weight, eps, pos, inv_freq, q_out, k_out, offs, _pairing(pairing),
+                               stream), "rtp_qk_norm_rope")
 
 
 def tree_attn_workspace_size(B, Hq, T, Hk, N) -> int:
     return int(_lib.rtp_tree_attn_workspace_size(B, Hq, T, Hk, N))
 
 
-def _tree_attn_args(q, k, v, lens, k_new, v_new, tree_mask, scale, o, ws, depth, W, ring, sel, stream):
-    d = _device_of(q)
-    B, Hq, T = q.shape[:3]
-    if tree_mask.dim() != 3:
-        raise ValueError(f"tree_mask: need [B, T, words], got {tuple(tree_mask.shape)}")
-    words = tree_mask.shape[2]
-    tree = _PACK3(_ints(tree_mask, d, (B, T, words), "tree_mask"), words, _ints(depth, d, (B, T), "depth") or 0)
-    chosen = None
-    if sel is not None:
-        if sel.mask is None:
-            raise ValueError("sel: the selection needs its mask")
-        words = sel.mask.shape[-1]
-        chosen = _PACK5(0, 0, 0, _ints(sel.mask, d, (B * Hq * T, words), "sel.mask"), words)
-    if ws is not None and (ws.get_device() != d or not ws.is_contiguous()):
-        raise ValueError("ws: need a contiguous tensor on the current CUDA device")
-    w, nb = (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
-    return [_packed(q, d), _packed(k, d), _packed(v, d), _ints(lens, d, (B,), "lens"), _packed(k_new, d),
-            _packed(v_new, d), tree, W, 1 if ring else 0, chosen, scale, _packed(o, d), w, nb, _stream(stream)]
+def _sel_mask(sel: Optional[Selection]):
+    if sel is not None and sel.mask is None:
+        raise ValueError("sel: the selection needs its mask")
+    return None if sel is None else sel.mask
 
 
 def tree_attn(q, k, v, lens, k_new, v_new, tree_mask, scale: float, o, ws=None, depth=None, W: int = 0,
@@ -341,8 +267,8 @@ def tree_attn(q, k, v, lens, k_new, v_new, tree_mask, scale: float, o, ws=None, 
     ``ring``) and over the drafted rows k_new, v_new [B, Hk, T, 128] that tree_mask
     int32 [B, T, words] names (bit j: token t attends draft j).  W > 0 is a window
     and needs depth int32 [B, T]; ``sel`` keeps only selected committed keys."""
-    _check(_lib.rtp_tree_attn(*_tree_attn_args(q, k, v, lens, k_new, v_new, tree_mask, scale, o, ws, depth, W, ring,
-                                               sel, stream)), "rtp_tree_attn")
+    _check(_calls.tree_attn(q, k, v, lens, k_new, v_new, tree_mask, scale, o, ws, depth, W, ring, _sel_mask(sel),
+                            stream), "rtp_tree_attn")
 
 
 def topp_select_workspace_size(B, Hq, T, Hk, N) -> int:
@@ -458,6 +384,19 @@ class Bound:
             raise RtpError(status, self._name)
 
 
+class BoundNative(Bound):
+    """The same for a native call: the tensors are held and described again by every
+    call (well below a microsecond), on the stream that was current when it was bound."""
+
+    __slots__ = ()
+
+    def __init__(self, name: str, *args, stream):
+        self._fn = getattr(_calls, name[4:])
+        self._args = (*args, _stream(stream).value or 0)
+        self._name = name
+        self._keep = None
+
+
 def _ref(struct, keep):
     keep.append(struct)
     return ctypes.byref(struct)
@@ -504,23 +443,20 @@ def bind_kv_append(k_new, v_new, pos, R: int, P=None, k_cache=None, v_cache=None
 
 def bind_kv_accept(k_new, v_new, pos, path, count, R: int, P=None, k_cache=None, v_cache=None, k_idx=None,
                    k_ring=None, v_ring=None, lens_out=None, ring_lens=None, stream=None) -> Bound:
-    keep = [k_new, v_new, pos, path, count, P, k_cache, v_cache, k_idx, k_ring, v_ring, lens_out, ring_lens]
-    return Bound("rtp_kv_accept", _kv_accept_args(k_new, v_new, pos, path, count, R, P, k_cache, v_cache, k_idx,
-                                                  k_ring, v_ring, lens_out, ring_lens, stream), keep)
+    return BoundNative("rtp_kv_accept", k_new, v_new, pos, path, count, R, P, k_cache, v_cache, k_idx, k_ring, v_ring,
+                       lens_out, ring_lens, stream=stream)
 
 
 def bind_qk_norm_rope(q, k, q_weight, k_weight, eps: float, pos, inv_freq, q_out, k_out, offs=None,
                       pairing: str = "half", stream=None) -> Bound:
-    keep = [q, k, q_weight, k_weight, pos, inv_freq, q_out, k_out, offs]
-    return Bound("rtp_qk_norm_rope", _qk_norm_rope_args(q, k, q_weight, k_weight, eps, pos, inv_freq, q_out, k_out,
-                                                        offs, pairing, stream), keep)
+    return BoundNative("rtp_qk_norm_rope", q, k, q_weight, k_weight, eps, pos, inv_freq, q_out, k_out, offs,
+                       _pairing(pairing), stream=stream)
 
 
 def bind_tree_attn(q, k, v, lens, k_new, v_new, tree_mask, scale: float, o, ws=None, depth=None, W: int = 0,
                    ring: bool = False, sel: Optional[Selection] = None, stream=None) -> Bound:
-    keep = [q, k, v, lens, k_new, v_new, tree_mask, o, ws, depth, sel]
-    return Bound("rtp_tree_attn", _tree_attn_args(q, k, v, lens, k_new, v_new, tree_mask, scale, o, ws, depth, W,
-                                                  ring, sel, stream), keep)
+    return BoundNative("rtp_tree_attn", q, k, v, lens, k_new, v_new, tree_mask, scale, o, ws, depth, W, ring,
+                       _sel_mask(sel), stream=stream)
 
 
 def bind_sparse_attn_decode_range(q, k, v, lens, sel: Selection, key_lo: int, scale: float, o, lse, ws=None,

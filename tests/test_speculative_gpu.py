@@ -531,3 +531,46 @@ def test_tree_step_selects_by_top_p():
     ref = _tree_ref(q[:, R * G:], k[:, R:], v[:, R:], lens, kn[:, R:], vn[:, R:], anc, depth, w.W, False, None,
                     D ** -0.5)
     _check_tree(o[:, R * G:], *ref, "local")
+
+
+# ---- the binding -------------------------------------------------------------------------
+
+def test_binding_refuses_wrong_arrays():
+    """Plain device arrays are described by their address alone, so the binding checks type, shape and layout."""
+    z = lambda *s, dtype=BF: torch.zeros(*s, dtype=dtype, device="cuda")  # noqa: E731
+    i32 = lambda *s: z(*s, dtype=torch.int32)  # noqa: E731
+    q, kv, freq = z(2, 4, 3, D), z(2, 2, 3, D), _freqs("cuda")
+
+    def rope(pos=i32(2), f=freq, offs=None, eps=1e-6):
+        rtp.qk_norm_rope(q, kv, None, None, eps, pos, f, q, kv, offs=offs)
+
+    for bad in (dict(pos=i32(3)), dict(pos=i32(2).long()), dict(pos=i32(2, 2)[:, 0]), dict(f=freq.float()),
+                dict(f=freq[:63]), dict(offs=i32(2, 2)), dict(offs=i32(2, 6)[:, ::2])):
+        with pytest.raises(ValueError, match="need a contiguous"):
+            rope(**bad)
+    with pytest.raises(TypeError):
+        rope(eps="x")
+    with pytest.raises(rtp.RtpError):
+        rope(eps=-1.0)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        rope(pos=torch.zeros(2, dtype=torch.int32))
+    ws = rtp.workspace(rtp.tree_attn_workspace_size(2, 4, 3, 2, 8), "cuda")
+
+    def attn(lens=None, mask=i32(2, 3, 1), depth=None, sel=None, ws=ws, o=q, W=0):
+        s = None if sel is None else rtp.Selection(tau_bits=sel, tiepos=sel, count=sel, mask=sel)
+        rtp.tree_attn(q, z(2, 2, 8, D), z(2, 2, 8, D), lens, kv, kv, mask, 0.1, o, ws, depth=depth, sel=s, W=W)
+
+    for bad in (dict(lens=i32(1)), dict(mask=i32(2, 2, 1)), dict(depth=i32(2, 4), W=1), dict(sel=i32(23, 1)),
+                dict(ws=ws[::2]), dict(ws=ws.cpu()), dict(mask=i32(2, 3)), dict(o=z(2, 4, 3))):
+        with pytest.raises(ValueError):
+            attn(**bad)
+    with pytest.raises(TypeError, match="unsupported dtype"):
+        attn(o=q.half())
+    with pytest.raises(rtp.RtpError):
+        attn(ws=None)
+    for bad in (dict(path=i32(2)), dict(path=i32(1, 2)), dict(count=i32(3)), dict(lens_out=i32(2).float())):
+        a = dict(path=i32(2, 2), count=i32(2), lens_out=i32(2))
+        a.update(bad)
+        with pytest.raises(ValueError):
+            rtp.kv_accept(kv, kv, i32(2), a["path"], a["count"], 0, k_ring=z(2, 2, 4, D), v_ring=z(2, 2, 4, D),
+                          lens_out=a["lens_out"])
