@@ -196,7 +196,7 @@ struct NormRopeArgs {
   const int32_t* offs;       // [B, T] or null: token t sits at pos[b] + offs[b][t], or pos[b] + t
   const double* inv_freq;    // [64]
   int B, Hq, Hk, T;
-  int heads_per_group;       // set by the launcher
+  int heads_per_group, q_parts;  // set by the launcher
 };
 cudaError_t launch_qk_norm_rope(NormRopeArgs a, bool in_bf16, bool out_bf16, bool half, cudaStream_t stream);
 

@@ -10,11 +10,13 @@
 // model).
 //
 // Bound: HBM (each row is read once and written once, about 10 operations per
-// element).  Eight lanes hold a row, 8 pairs each, so that every access is a
-// 16-byte vector, the sum of squares takes three shuffles, and the rotation
-// needs no exchange at all: a lane holds both members of its pairs.  A lane
-// group stays on one token and walks over heads, so the cosines and sines of
-// the token (8 pairs per lane) are computed once and kept in registers.
+// element).  Sixteen lanes hold a row, 4 pairs each: accesses of 8 or 16 bytes,
+// four shuffles for the sum of squares, and no exchange for the rotation, since
+// a lane holds both members of its pairs.  A lane group stays on one token and
+// walks over heads, so the cosines and sines of the token are computed once and
+// kept in registers, multiplied with the norm's weights, and the rows of the
+// next four heads are on their way while one is worked on (a copy of this kind
+// lives on reads in flight).  Arithmetic is packed, two pairs to an instruction.
 //
 // The angle is formed in fp64 as a fraction of a turn (position * inv_freq /
 // 2 pi, less its nearest integer): in fp32 the product alone is off by 0.03
@@ -28,49 +30,56 @@ namespace rtp {
 namespace {
 
 constexpr int kNrThreads = 256;
-constexpr int kNrLanes = 8;   // lanes per row
-constexpr int kNrPairs = 8;   // pairs per lane
-constexpr int kNrUnroll = 2;  // heads in flight per lane group
+constexpr int kNrLanes = 16;     // lanes per row
+constexpr int kNrPairs = 4;      // pairs per lane
+constexpr int kNrAhead = 4;      // rows on their way per lane group
+constexpr int kNrBlocks = 148 * 8;
 
-// A lane's 16 elements of a row as raw 16-byte vectors: a = first members of its pairs, b = second (half
-// pairing: dims 8l .. and 64 + 8l ..), or all in one run (adjacent pairing: dims 16l ..).
+// A lane's 8 elements of a row as raw words: half pairing, dims 4l .. 4l + 3 and 64 + 4l ..; adjacent
+// pairing, dims 8l .. 8l + 7.
 template <typename T, bool kHalf>
 struct LaneRow {
-  static constexpr int kVec = sizeof(T) == 2 ? 1 : 2;  // 16-byte vectors per 8 elements
-  uint4 v[2][kVec];
-  RTP_DEVICE static int64_t offset(int part, int lane) { return kHalf ? part * 64 + 8 * lane : 16 * lane + 8 * part; }
+  static constexpr int kWords = sizeof(T) == 2 ? 2 : 4;  // 32-bit words per 4 elements
+  uint32_t w[2][kWords];
+  RTP_DEVICE static int offset(int part, int lane) { return kHalf ? part * 64 + 4 * lane : 8 * lane + 4 * part; }
   // (plain loads: the output may be the input)
   RTP_DEVICE void load(const T* row, int lane) {
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) v[p][i] = reinterpret_cast<const uint4*>(row + offset(p, lane))[i];
-  }
-  RTP_DEVICE void to_float(float (&a)[kNrPairs], float (&b)[kNrPairs]) const {
-    float x[2][8];
-#pragma unroll
     for (int p = 0; p < 2; ++p) {
       if constexpr (sizeof(T) == 2) {
-        const uint32_t w[4] = {v[p][0].x, v[p][0].y, v[p][0].z, v[p][0].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[p][2 * i] = bf16_lo(w[i]);
-          x[p][2 * i + 1] = bf16_hi(w[i]);
-        }
+        const uint2 x = *reinterpret_cast<const uint2*>(row + offset(p, lane));
+        w[p][0] = x.x;
+        w[p][1] = x.y;
       } else {
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          x[p][4 * i] = __uint_as_float(v[p][i].x);
-          x[p][4 * i + 1] = __uint_as_float(v[p][i].y);
-          x[p][4 * i + 2] = __uint_as_float(v[p][i].z);
-          x[p][4 * i + 3] = __uint_as_float(v[p][i].w);
-        }
+        const uint4 x = *reinterpret_cast<const uint4*>(row + offset(p, lane));
+        w[p][0] = x.x;
+        w[p][1] = x.y;
+        w[p][2] = x.z;
+        w[p][3] = x.w;
       }
     }
+  }
+  // first (a) and second (b) members of the lane's pairs
+  RTP_DEVICE void to_float(float (&a)[kNrPairs], float (&b)[kNrPairs]) const {
+    float x[2][4];
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        if constexpr (sizeof(T) == 2) {
+          x[p][2 * i] = bf16_lo(w[p][i]);
+          x[p][2 * i + 1] = bf16_hi(w[p][i]);
+        } else {
+          x[p][i] = __uint_as_float(w[p][i]);
+        }
+      }
+    split(x, a, b);
+  }
+  RTP_DEVICE static void split(const float (&x)[2][4], float (&a)[kNrPairs], float (&b)[kNrPairs]) {
 #pragma unroll
     for (int i = 0; i < kNrPairs; ++i) {
-      a[i] = kHalf ? x[0][i] : x[i >> 2][2 * (i & 3)];
-      b[i] = kHalf ? x[1][i] : x[i >> 2][2 * (i & 3) + 1];
+      a[i] = kHalf ? x[0][i] : x[i >> 1][2 * (i & 1)];
+      b[i] = kHalf ? x[1][i] : x[i >> 1][2 * (i & 1) + 1];
     }
   }
 };
@@ -79,152 +88,178 @@ template <typename T, bool kHalf>
 RTP_DEVICE void store_row(T* row, int lane, const float (&a)[kNrPairs], const float (&b)[kNrPairs]) {
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
-    float x[8];
+    float x[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = kHalf ? (p ? b[2 * i] : a[2 * i]) : a[4 * p + i];
-      x[2 * i + 1] = kHalf ? (p ? b[2 * i + 1] : a[2 * i + 1]) : b[4 * p + i];
+    for (int i = 0; i < 2; ++i) {
+      x[2 * i] = kHalf ? (p ? b[2 * i] : a[2 * i]) : a[2 * p + i];
+      x[2 * i + 1] = kHalf ? (p ? b[2 * i + 1] : a[2 * i + 1]) : b[2 * p + i];
     }
-    T* dst = row + (kHalf ? p * 64 + 8 * lane : 16 * lane + 8 * p);
-    if constexpr (sizeof(T) == 2) {
-      uint4 w;
-      w.x = pack_bf16x2(x[0], x[1]);
-      w.y = pack_bf16x2(x[2], x[3]);
-      w.z = pack_bf16x2(x[4], x[5]);
-      w.w = pack_bf16x2(x[6], x[7]);
-      *reinterpret_cast<uint4*>(dst) = w;
-    } else {
-      reinterpret_cast<float4*>(dst)[0] = make_float4(x[0], x[1], x[2], x[3]);
-      reinterpret_cast<float4*>(dst)[1] = make_float4(x[4], x[5], x[6], x[7]);
-    }
+    T* dst = row + LaneRow<T, kHalf>::offset(p, lane);
+    if constexpr (sizeof(T) == 2)
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+    else
+      *reinterpret_cast<float4*>(dst) = make_float4(x[0], x[1], x[2], x[3]);
   }
 }
 
-template <bool kHalf>
-RTP_DEVICE void load_weight(const void* w, int64_t row_off, bool bf16, int lane, float (&a)[kNrPairs],
-                            float (&b)[kNrPairs]) {
-  if (bf16) {
-    LaneRow<__nv_bfloat16, kHalf> r;
-    r.load(static_cast<const __nv_bfloat16*>(w) + row_off, lane);
-    r.to_float(a, b);
-  } else {
-    LaneRow<float, kHalf> r;
-    r.load(static_cast<const float*>(w) + row_off, lane);
-    r.to_float(a, b);
-  }
-}
-
-RTP_DEVICE float group_sum(float v) {
+template <typename V>
+RTP_DEVICE V group_sum(V v) {
 #pragma unroll
   for (int o = 1; o < kNrLanes; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-// x <- x * rsqrt(mean(x^2) + eps) * w.  Rows whose sum of squares leaves the range of fp32 (elements past
+// Two pairs in one 64-bit word, for packed fp32 arithmetic.
+RTP_DEVICE uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+RTP_DEVICE void unpack2(uint64_t x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(x)); }
+RTP_DEVICE uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+RTP_DEVICE uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+constexpr int kNrWords = kNrPairs / 2;  // packed words of a lane's first (or second) members
+
+// x <- x * rsqrt(mean(x^2) + eps).  Rows whose sum of squares leaves the range of fp32 (elements past
 // about 1e15, or all tiny with an eps as tiny) are summed in fp64.
-RTP_DEVICE void norm_row(float (&a)[kNrPairs], float (&b)[kNrPairs], const float (&wa)[kNrPairs],
-                         const float (&wb)[kNrPairs], float eps) {
-  float ss = 0.f;
+RTP_DEVICE void norm_row(uint64_t (&a)[kNrWords], uint64_t (&b)[kNrWords], float eps) {
+  uint64_t s2 = 0ull;
 #pragma unroll
-  for (int i = 0; i < kNrPairs; ++i) ss = __fmaf_rn(a[i], a[i], __fmaf_rn(b[i], b[i], ss));
-  ss = group_sum(ss);
+  for (int i = 0; i < kNrWords; ++i) s2 = fma2(a[i], a[i], fma2(b[i], b[i], s2));
+  float s0, s1;
+  unpack2(s2, s0, s1);
+  const float ss = group_sum(s0 + s1);
   const bool wide = !(ss < 1e30f) || ss + 128.f * eps < 1e-30f;
   if (!__any_sync(0xffffffffu, wide)) {
-    const float r = __frsqrt_rn(__fmaf_rn(ss, 1.f / kHeadDim, eps));
+    const float r = rsqrtf(__fmaf_rn(ss, 1.f / kHeadDim, eps));
+    const uint64_t r2 = pack2(r, r);
 #pragma unroll
-    for (int i = 0; i < kNrPairs; ++i) {
-      a[i] = a[i] * r * wa[i];
-      b[i] = b[i] * r * wb[i];
+    for (int i = 0; i < kNrWords; ++i) {
+      a[i] = mul2(a[i], r2);
+      b[i] = mul2(b[i], r2);
     }
     return;
   }
+  float x[4 * kNrWords];
+#pragma unroll
+  for (int i = 0; i < kNrWords; ++i) {
+    unpack2(a[i], x[4 * i], x[4 * i + 1]);
+    unpack2(b[i], x[4 * i + 2], x[4 * i + 3]);
+  }
   double sd = 0.0;
 #pragma unroll
-  for (int i = 0; i < kNrPairs; ++i) sd += (double)a[i] * a[i] + (double)b[i] * b[i];
+  for (int i = 0; i < 4 * kNrWords; ++i) sd += (double)x[i] * x[i];
+  const double r = 1.0 / sqrt(group_sum(sd) / kHeadDim + (double)eps);
 #pragma unroll
-  for (int o = 1; o < kNrLanes; o <<= 1) sd += __shfl_xor_sync(0xffffffffu, sd, o);
-  const double r = 1.0 / sqrt(sd / kHeadDim + (double)eps);
-#pragma unroll
-  for (int i = 0; i < kNrPairs; ++i) {
-    a[i] = (float)(a[i] * r) * wa[i];
-    b[i] = (float)(b[i] * r) * wb[i];
+  for (int i = 0; i < kNrWords; ++i) {
+    a[i] = pack2((float)(x[4 * i] * r), (float)(x[4 * i + 1] * r));
+    b[i] = pack2((float)(x[4 * i + 2] * r), (float)(x[4 * i + 3] * r));
   }
 }
 
-// Thread block: kNrThreads / 8 tokens x A.heads_per_group heads (of the Hq query then Hk key heads).
+// Thread block: blockDim / 16 tokens x A.heads_per_group heads, of the queries or of the keys.
 template <typename Tin, typename Tout, bool kHalf>
-__global__ void __launch_bounds__(kNrThreads) qk_norm_rope_kernel(NormRopeArgs A) {
+__global__ void __launch_bounds__(kNrThreads, 3) qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs A) {
+  using Row = LaneRow<Tin, kHalf>;
+  pdl_wait();
+  pdl_release();
   const int lane = threadIdx.x & (kNrLanes - 1);
   const int64_t tok = (int64_t)blockIdx.x * (blockDim.x / kNrLanes) + threadIdx.x / kNrLanes;
   const bool live = tok < (int64_t)A.B * A.T;  // (the shuffles below take whole warps)
-  const int b = live ? (int)(tok / A.T) : 0, t = live ? (int)(tok % A.T) : 0;
+  const int b = live ? (int)(tok / A.T) : 0, t = live ? (int)(tok - (int64_t)b * A.T) : 0;
+  const bool is_q = (int)blockIdx.y < A.q_parts;
+  const int h0 = ((int)blockIdx.y - (is_q ? 0 : A.q_parts)) * A.heads_per_group;
+  const int n = min(A.heads_per_group, (is_q ? A.Hq : A.Hk) - h0);  // heads of this block
+  const View4& in = is_q ? A.q : A.k;
+  const MutView4& out = is_q ? A.q_out : A.k_out;
 
-  float cs[kNrPairs], sn[kNrPairs];
-  {
-    const double p = live ? (double)((int64_t)A.pos[b] + (A.offs ? A.offs[(int64_t)b * A.T + t] : t)) : 0.0;
-    const double* f = A.inv_freq + kNrPairs * lane;
+  const Tin* src = static_cast<const Tin*>(in.data) + b * in.sb + t * in.sn + h0 * in.sh;
+  Row x[kNrAhead] = {};
 #pragma unroll
-    for (int i = 0; i < kNrPairs; ++i) {
-      const double turns = p * __ldg(f + i) * 0.15915494309189533577;  // 1 / (2 pi)
-      sincospif((float)(2.0 * (turns - rint(turns))), &sn[i], &cs[i]);
-    }
+  for (int u = 0; u < kNrAhead; ++u) {
+    if (live && u < n) x[u].load(src, lane);
+    src += in.sh;
   }
-  const int H = A.Hq + A.Hk;
-  const int h0 = blockIdx.y * A.heads_per_group, h1 = min(h0 + A.heads_per_group, H);
-  float wa[kNrPairs], wb[kNrPairs];
-  bool have_w = false;
-  for (int h = h0; h < h1; h += kNrUnroll) {
-    LaneRow<Tin, kHalf> x[kNrUnroll];
+  const int64_t pos = live ? (int64_t)A.pos[b] + (A.offs ? A.offs[tok] : t) : 0;
+  float cs[kNrPairs], sn[kNrPairs];
 #pragma unroll
-    for (int u = 0; u < kNrUnroll; ++u) {
-      const int hh = h + u;
-      if (hh >= h1 || !live) continue;
-      const View4& src = hh < A.Hq ? A.q : A.k;
-      x[u].load(static_cast<const Tin*>(src.data) + b * src.sb + (hh < A.Hq ? hh : hh - A.Hq) * src.sh + t * src.sn,
-                lane);
+  for (int i = 0; i < kNrPairs; ++i) {
+    const double turns = (double)pos * __ldg(A.inv_freq + kNrPairs * lane + i) * 0.15915494309189533577;  // 1 / (2 pi)
+    sincospif((float)(2.0 * (turns - rint(turns))), &sn[i], &cs[i]);
+  }
+
+  // The turn with the norm's weights in it: y_a = a ca + b cb, y_b = b da + a db.
+  uint64_t ca[kNrWords], cb[kNrWords], da[kNrWords], db[kNrWords];
+  const void* w = is_q ? A.qw : A.kw;
+  const bool w_bf16 = is_q ? A.qw_bf16 : A.kw_bf16;
+  const int64_t w_stride = is_q ? A.qw_stride : A.kw_stride;  // 0: one row for all heads
+  auto turn = [&](int h) {
+    float wa[kNrPairs], wb[kNrPairs];
+    if (!w) {
+#pragma unroll
+      for (int i = 0; i < kNrPairs; ++i) wa[i] = wb[i] = 1.f;
+    } else if (w_bf16) {
+      LaneRow<__nv_bfloat16, kHalf> r;
+      r.load(static_cast<const __nv_bfloat16*>(w) + w_stride * h, lane);
+      r.to_float(wa, wb);
+    } else {
+      LaneRow<float, kHalf> r;
+      r.load(static_cast<const float*>(w) + w_stride * h, lane);
+      r.to_float(wa, wb);
     }
 #pragma unroll
-    for (int u = 0; u < kNrUnroll; ++u) {
-      const int hh = h + u;
-      if (hh >= h1) continue;  // uniform over the block
-      const bool is_q = hh < A.Hq;
-      const int hk = is_q ? hh : hh - A.Hq;
-      const void* w = is_q ? A.qw : A.kw;
-      float a[kNrPairs], c[kNrPairs];
-      if (live) {
-        x[u].to_float(a, c);
-      } else {
+    for (int i = 0; i < kNrWords; ++i) {
+      const int j = 2 * i, k = 2 * i + 1;
+      ca[i] = pack2(wa[j] * cs[j], wa[k] * cs[k]);
+      cb[i] = pack2(-(wb[j] * sn[j]), -(wb[k] * sn[k]));
+      da[i] = pack2(wb[j] * cs[j], wb[k] * cs[k]);
+      db[i] = pack2(wa[j] * sn[j], wa[k] * sn[k]);
+    }
+  };
+  turn(h0);
+
+  Tout* dst = static_cast<Tout*>(out.data) + b * out.sb + t * out.sn + h0 * out.sh;
+#pragma unroll 1
+  for (int h = 0; h < n; h += kNrAhead) {
 #pragma unroll
-        for (int i = 0; i < kNrPairs; ++i) a[i] = c[i] = 0.f;
-      }
-      if (w) {
-        const int64_t ws = is_q ? A.qw_stride : A.kw_stride;  // 0: one weight row for all heads
-        if (!have_w || ws || hh == A.Hq) {
-          load_weight<kHalf>(w, ws * hk, is_q ? A.qw_bf16 : A.kw_bf16, lane, wa, wb);
-          have_w = true;
-        }
-        norm_row(a, c, wa, wb, A.eps);
-      }
-      if (!live) continue;
-      float ya[kNrPairs], yb[kNrPairs];
+    for (int u = 0; u < kNrAhead; ++u) {
+      if (h + u >= n) break;  // uniform over the block
+      float fa[kNrPairs], fb[kNrPairs];
+      x[u].to_float(fa, fb);
+      if (live && h + u + kNrAhead < n) x[u].load(src, lane);
+      src += in.sh;
+      uint64_t a[kNrWords], c[kNrWords];
 #pragma unroll
-      for (int i = 0; i < kNrPairs; ++i) {
-        ya[i] = __fmaf_rn(a[i], cs[i], -(c[i] * sn[i]));
-        yb[i] = __fmaf_rn(c[i], cs[i], a[i] * sn[i]);
+      for (int i = 0; i < kNrWords; ++i) {
+        a[i] = pack2(fa[2 * i], fa[2 * i + 1]);
+        c[i] = pack2(fb[2 * i], fb[2 * i + 1]);
       }
-      const MutView4& dst = is_q ? A.q_out : A.k_out;
-      store_row<Tout, kHalf>(static_cast<Tout*>(dst.data) + b * dst.sb + hk * dst.sh + t * dst.sn, lane, ya, yb);
+      if (w) norm_row(a, c, A.eps);
+#pragma unroll
+      for (int i = 0; i < kNrWords; ++i) {
+        unpack2(fma2(a[i], ca[i], mul2(c[i], cb[i])), fa[2 * i], fa[2 * i + 1]);
+        unpack2(fma2(c[i], da[i], mul2(a[i], db[i])), fb[2 * i], fb[2 * i + 1]);
+      }
+      if (live) store_row<Tout, kHalf>(dst, lane, fa, fb);
+      dst += out.sh;
+      if (w_stride && h + u + 1 < n) turn(h0 + h + u + 1);
     }
   }
 }
 
 template <typename Tin, typename Tout>
 cudaError_t launch(const NormRopeArgs& a, bool half, dim3 grid, int threads, cudaStream_t stream) {
-  if (half)
-    qk_norm_rope_kernel<Tin, Tout, true><<<grid, threads, 0, stream>>>(a);
-  else
-    qk_norm_rope_kernel<Tin, Tout, false><<<grid, threads, 0, stream>>>(a);
-  return cudaGetLastError();
+  if (half) return launch_pdl(qk_norm_rope_kernel<Tin, Tout, true>, grid, dim3(threads), 0, stream, 1, a);
+  return launch_pdl(qk_norm_rope_kernel<Tin, Tout, false>, grid, dim3(threads), 0, stream, 1, a);
 }
 
 }  // namespace
@@ -233,10 +268,16 @@ cudaError_t launch_qk_norm_rope(NormRopeArgs a, bool in_bf16, bool out_bf16, boo
   const int64_t toks = (int64_t)a.B * a.T;
   const int H = a.Hq + a.Hk;
   if (toks == 0 || H == 0) return cudaSuccess;
-  const int threads = kNrThreads;
-  const int64_t blocks = (toks * kNrLanes + threads - 1) / threads;
-  a.heads_per_group = 8;
-  const dim3 grid((unsigned)blocks, (unsigned)((H + a.heads_per_group - 1) / a.heads_per_group));
+  constexpr int kPer = kNrThreads / kNrLanes;  // tokens per full block
+  const int threads = toks < kPer ? (int)(toks * kNrLanes + 31) / 32 * 32 : kNrThreads;
+  const int64_t blocks = (toks + kPer - 1) / kPer;
+  // all heads of a token in one block (queries and keys apart) when there are tokens enough for 8 blocks per SM,
+  // else the heads are divided (each part computes the angles again)
+  const int64_t parts = blocks >= kNrBlocks ? 1 : (kNrBlocks + blocks - 1) / blocks;
+  const int64_t per = (H + parts - 1) / parts;
+  a.heads_per_group = (int)per;
+  a.q_parts = (int)((a.Hq + per - 1) / per);
+  const dim3 grid((unsigned)blocks, (unsigned)(a.q_parts + (a.Hk + per - 1) / per));
   if (in_bf16)
     return out_bf16 ? launch<__nv_bfloat16, __nv_bfloat16>(a, half, grid, threads, stream)
                     : launch<__nv_bfloat16, float>(a, half, grid, threads, stream);
