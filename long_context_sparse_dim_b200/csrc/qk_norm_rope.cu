@@ -30,38 +30,43 @@ namespace rtp {
 namespace {
 
 constexpr int kNrThreads = 256;
-constexpr int kNrLanes = 16;     // lanes per row
-constexpr int kNrPairs = 4;      // pairs per lane
 constexpr int kNrAhead = 4;      // rows on their way per lane group
 constexpr int kNrBlocks = 148 * 8;
 
-// A lane's 8 elements of a row as raw words: half pairing, dims 4l .. 4l + 3 and 64 + 4l ..; adjacent
-// pairing, dims 8l .. 8l + 7.
-template <typename T, bool kHalf>
+// A lane's share of a row of kLanes lanes as raw words, in two parts of kPairs elements.  Half pairing: the
+// first members of its pairs, then the second; adjacent pairing: neighbouring dims.
+template <typename T, bool kHalf, int kLanes>
 struct LaneRow {
-  static constexpr int kWords = sizeof(T) == 2 ? 2 : 4;  // 32-bit words per 4 elements
+  static constexpr int kPairs = 64 / kLanes;
+  static constexpr int kWords = kPairs * (int)sizeof(T) / 4;  // 32-bit words per part
   uint32_t w[2][kWords];
-  RTP_DEVICE static int offset(int part, int lane) { return kHalf ? part * 64 + 4 * lane : 8 * lane + 4 * part; }
+  RTP_DEVICE static int offset(int part, int lane) {
+    return kHalf ? part * 64 + kPairs * lane : 2 * kPairs * lane + kPairs * part;
+  }
   // (plain loads: the output may be the input)
   RTP_DEVICE void load(const T* row, int lane) {
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      if constexpr (sizeof(T) == 2) {
-        const uint2 x = *reinterpret_cast<const uint2*>(row + offset(p, lane));
+      const T* src = row + offset(p, lane);
+      if constexpr (kWords == 2) {
+        const uint2 x = *reinterpret_cast<const uint2*>(src);
         w[p][0] = x.x;
         w[p][1] = x.y;
       } else {
-        const uint4 x = *reinterpret_cast<const uint4*>(row + offset(p, lane));
-        w[p][0] = x.x;
-        w[p][1] = x.y;
-        w[p][2] = x.z;
-        w[p][3] = x.w;
+#pragma unroll
+        for (int i = 0; i < kWords; i += 4) {
+          const uint4 x = reinterpret_cast<const uint4*>(src)[i / 4];
+          w[p][i] = x.x;
+          w[p][i + 1] = x.y;
+          w[p][i + 2] = x.z;
+          w[p][i + 3] = x.w;
+        }
       }
     }
   }
   // first (a) and second (b) members of the lane's pairs
-  RTP_DEVICE void to_float(float (&a)[kNrPairs], float (&b)[kNrPairs]) const {
-    float x[2][4];
+  RTP_DEVICE void to_float(float (&a)[kPairs], float (&b)[kPairs]) const {
+    float x[2][kPairs];
 #pragma unroll
     for (int p = 0; p < 2; ++p)
 #pragma unroll
@@ -73,39 +78,43 @@ struct LaneRow {
           x[p][i] = __uint_as_float(w[p][i]);
         }
       }
-    split(x, a, b);
-  }
-  RTP_DEVICE static void split(const float (&x)[2][4], float (&a)[kNrPairs], float (&b)[kNrPairs]) {
 #pragma unroll
-    for (int i = 0; i < kNrPairs; ++i) {
-      a[i] = kHalf ? x[0][i] : x[i >> 1][2 * (i & 1)];
-      b[i] = kHalf ? x[1][i] : x[i >> 1][2 * (i & 1) + 1];
+    for (int i = 0; i < kPairs; ++i) {
+      constexpr int kHalfPairs = kPairs / 2;
+      a[i] = kHalf ? x[0][i] : x[i / kHalfPairs][2 * (i % kHalfPairs)];
+      b[i] = kHalf ? x[1][i] : x[i / kHalfPairs][2 * (i % kHalfPairs) + 1];
+    }
+  }
+  // a row from its members
+  RTP_DEVICE static void store(T* row, int lane, const float (&a)[kPairs], const float (&b)[kPairs]) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      float x[kPairs];
+#pragma unroll
+      for (int i = 0; i < kPairs / 2; ++i) {
+        x[2 * i] = kHalf ? (p ? b[2 * i] : a[2 * i]) : a[kPairs / 2 * p + i];
+        x[2 * i + 1] = kHalf ? (p ? b[2 * i + 1] : a[2 * i + 1]) : b[kPairs / 2 * p + i];
+      }
+      T* dst = row + offset(p, lane);
+#pragma unroll
+      for (int i = 0; i < kPairs; i += 16 / (int)sizeof(T)) {
+        if constexpr (sizeof(T) == 4)
+          *reinterpret_cast<float4*>(dst + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+        else if constexpr (kPairs == 4)
+          *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+        else
+          *reinterpret_cast<uint4*>(dst + i) =
+              make_uint4(pack_bf16x2(x[i], x[i + 1]), pack_bf16x2(x[i + 2], x[i + 3]),
+                         pack_bf16x2(x[i + 4], x[i + 5]), pack_bf16x2(x[i + 6], x[i + 7]));
+      }
     }
   }
 };
 
-template <typename T, bool kHalf>
-RTP_DEVICE void store_row(T* row, int lane, const float (&a)[kNrPairs], const float (&b)[kNrPairs]) {
-#pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    float x[4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      x[2 * i] = kHalf ? (p ? b[2 * i] : a[2 * i]) : a[2 * p + i];
-      x[2 * i + 1] = kHalf ? (p ? b[2 * i + 1] : a[2 * i + 1]) : b[2 * p + i];
-    }
-    T* dst = row + LaneRow<T, kHalf>::offset(p, lane);
-    if constexpr (sizeof(T) == 2)
-      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-    else
-      *reinterpret_cast<float4*>(dst) = make_float4(x[0], x[1], x[2], x[3]);
-  }
-}
-
-template <typename V>
+template <int kLanes, typename V>
 RTP_DEVICE V group_sum(V v) {
 #pragma unroll
-  for (int o = 1; o < kNrLanes; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = 1; o < kLanes; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
@@ -127,53 +136,54 @@ RTP_DEVICE uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
-constexpr int kNrWords = kNrPairs / 2;  // packed words of a lane's first (or second) members
-
 // x <- x * rsqrt(mean(x^2) + eps).  Rows whose sum of squares leaves the range of fp32 (elements past
 // about 1e15, or all tiny with an eps as tiny) are summed in fp64.
-RTP_DEVICE void norm_row(uint64_t (&a)[kNrWords], uint64_t (&b)[kNrWords], float eps) {
+template <int kLanes>
+RTP_DEVICE void norm_row(uint64_t (&a)[32 / kLanes], uint64_t (&b)[32 / kLanes], float eps) {
+  constexpr int kWords = 32 / kLanes;
   uint64_t s2 = 0ull;
 #pragma unroll
-  for (int i = 0; i < kNrWords; ++i) s2 = fma2(a[i], a[i], fma2(b[i], b[i], s2));
+  for (int i = 0; i < kWords; ++i) s2 = fma2(a[i], a[i], fma2(b[i], b[i], s2));
   float s0, s1;
   unpack2(s2, s0, s1);
-  const float ss = group_sum(s0 + s1);
+  const float ss = group_sum<kLanes>(s0 + s1);
   const bool wide = !(ss < 1e30f) || ss + 128.f * eps < 1e-30f;
   if (!__any_sync(0xffffffffu, wide)) {
     const float r = rsqrtf(__fmaf_rn(ss, 1.f / kHeadDim, eps));
     const uint64_t r2 = pack2(r, r);
 #pragma unroll
-    for (int i = 0; i < kNrWords; ++i) {
+    for (int i = 0; i < kWords; ++i) {
       a[i] = mul2(a[i], r2);
       b[i] = mul2(b[i], r2);
     }
     return;
   }
-  float x[4 * kNrWords];
+  float x[4 * kWords];
 #pragma unroll
-  for (int i = 0; i < kNrWords; ++i) {
+  for (int i = 0; i < kWords; ++i) {
     unpack2(a[i], x[4 * i], x[4 * i + 1]);
     unpack2(b[i], x[4 * i + 2], x[4 * i + 3]);
   }
   double sd = 0.0;
 #pragma unroll
-  for (int i = 0; i < 4 * kNrWords; ++i) sd += (double)x[i] * x[i];
-  const double r = 1.0 / sqrt(group_sum(sd) / kHeadDim + (double)eps);
+  for (int i = 0; i < 4 * kWords; ++i) sd += (double)x[i] * x[i];
+  const double r = 1.0 / sqrt(group_sum<kLanes>(sd) / kHeadDim + (double)eps);
 #pragma unroll
-  for (int i = 0; i < kNrWords; ++i) {
+  for (int i = 0; i < kWords; ++i) {
     a[i] = pack2((float)(x[4 * i] * r), (float)(x[4 * i + 1] * r));
     b[i] = pack2((float)(x[4 * i + 2] * r), (float)(x[4 * i + 3] * r));
   }
 }
 
-// Thread block: blockDim / 16 tokens x A.heads_per_group heads, of the queries or of the keys.
-template <typename Tin, typename Tout, bool kHalf>
-__global__ void __launch_bounds__(kNrThreads, 3) qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs A) {
-  using Row = LaneRow<Tin, kHalf>;
+// Thread block: blockDim / kLanes tokens x A.heads_per_group heads, of the queries or of the keys.
+template <typename Tin, typename Tout, bool kHalf, int kLanes>
+__global__ void __launch_bounds__(kNrThreads, kLanes == 8 ? 2 : 3) qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs A) {
+  using Row = LaneRow<Tin, kHalf, kLanes>;
+  constexpr int kPairs = Row::kPairs, kWords = kPairs / 2;  // pairs of a lane; packed words of their members
   pdl_wait();
   pdl_release();
-  const int lane = threadIdx.x & (kNrLanes - 1);
-  const int64_t tok = (int64_t)blockIdx.x * (blockDim.x / kNrLanes) + threadIdx.x / kNrLanes;
+  const int lane = threadIdx.x & (kLanes - 1);
+  const int64_t tok = (int64_t)blockIdx.x * (blockDim.x / kLanes) + threadIdx.x / kLanes;
   const bool live = tok < (int64_t)A.B * A.T;  // (the shuffles below take whole warps)
   const int b = live ? (int)(tok / A.T) : 0, t = live ? (int)(tok - (int64_t)b * A.T) : 0;
   const bool is_q = (int)blockIdx.y < A.q_parts;
@@ -190,34 +200,34 @@ __global__ void __launch_bounds__(kNrThreads, 3) qk_norm_rope_kernel(const __gri
     src += in.sh;
   }
   const int64_t pos = live ? (int64_t)A.pos[b] + (A.offs ? A.offs[tok] : t) : 0;
-  float cs[kNrPairs], sn[kNrPairs];
+  float cs[kPairs], sn[kPairs];
 #pragma unroll
-  for (int i = 0; i < kNrPairs; ++i) {
-    const double turns = (double)pos * __ldg(A.inv_freq + kNrPairs * lane + i) * 0.15915494309189533577;  // 1 / (2 pi)
+  for (int i = 0; i < kPairs; ++i) {
+    const double turns = (double)pos * __ldg(A.inv_freq + kPairs * lane + i) * 0.15915494309189533577;  // 1 / (2 pi)
     sincospif((float)(2.0 * (turns - rint(turns))), &sn[i], &cs[i]);
   }
 
   // The turn with the norm's weights in it: y_a = a ca + b cb, y_b = b da + a db.
-  uint64_t ca[kNrWords], cb[kNrWords], da[kNrWords], db[kNrWords];
+  uint64_t ca[kWords], cb[kWords], da[kWords], db[kWords];
   const void* w = is_q ? A.qw : A.kw;
   const bool w_bf16 = is_q ? A.qw_bf16 : A.kw_bf16;
   const int64_t w_stride = is_q ? A.qw_stride : A.kw_stride;  // 0: one row for all heads
   auto turn = [&](int h) {
-    float wa[kNrPairs], wb[kNrPairs];
+    float wa[kPairs], wb[kPairs];
     if (!w) {
 #pragma unroll
-      for (int i = 0; i < kNrPairs; ++i) wa[i] = wb[i] = 1.f;
+      for (int i = 0; i < kPairs; ++i) wa[i] = wb[i] = 1.f;
     } else if (w_bf16) {
-      LaneRow<__nv_bfloat16, kHalf> r;
+      LaneRow<__nv_bfloat16, kHalf, kLanes> r;
       r.load(static_cast<const __nv_bfloat16*>(w) + w_stride * h, lane);
       r.to_float(wa, wb);
     } else {
-      LaneRow<float, kHalf> r;
+      LaneRow<float, kHalf, kLanes> r;
       r.load(static_cast<const float*>(w) + w_stride * h, lane);
       r.to_float(wa, wb);
     }
 #pragma unroll
-    for (int i = 0; i < kNrWords; ++i) {
+    for (int i = 0; i < kWords; ++i) {
       const int j = 2 * i, k = 2 * i + 1;
       ca[i] = pack2(wa[j] * cs[j], wa[k] * cs[k]);
       cb[i] = pack2(-(wb[j] * sn[j]), -(wb[k] * sn[k]));
@@ -233,33 +243,33 @@ __global__ void __launch_bounds__(kNrThreads, 3) qk_norm_rope_kernel(const __gri
 #pragma unroll
     for (int u = 0; u < kNrAhead; ++u) {
       if (h + u >= n) break;  // uniform over the block
-      float fa[kNrPairs], fb[kNrPairs];
+      float fa[kPairs], fb[kPairs];
       x[u].to_float(fa, fb);
       if (live && h + u + kNrAhead < n) x[u].load(src, lane);
       src += in.sh;
-      uint64_t a[kNrWords], c[kNrWords];
+      uint64_t a[kWords], c[kWords];
 #pragma unroll
-      for (int i = 0; i < kNrWords; ++i) {
+      for (int i = 0; i < kWords; ++i) {
         a[i] = pack2(fa[2 * i], fa[2 * i + 1]);
         c[i] = pack2(fb[2 * i], fb[2 * i + 1]);
       }
-      if (w) norm_row(a, c, A.eps);
+      if (w) norm_row<kLanes>(a, c, A.eps);
 #pragma unroll
-      for (int i = 0; i < kNrWords; ++i) {
+      for (int i = 0; i < kWords; ++i) {
         unpack2(fma2(a[i], ca[i], mul2(c[i], cb[i])), fa[2 * i], fa[2 * i + 1]);
         unpack2(fma2(c[i], da[i], mul2(a[i], db[i])), fb[2 * i], fb[2 * i + 1]);
       }
-      if (live) store_row<Tout, kHalf>(dst, lane, fa, fb);
+      if (live) LaneRow<Tout, kHalf, kLanes>::store(dst, lane, fa, fb);
       dst += out.sh;
       if (w_stride && h + u + 1 < n) turn(h0 + h + u + 1);
     }
   }
 }
 
-template <typename Tin, typename Tout>
+template <typename Tin, typename Tout, int kLanes>
 cudaError_t launch(const NormRopeArgs& a, bool half, dim3 grid, int threads, cudaStream_t stream) {
-  if (half) return launch_pdl(qk_norm_rope_kernel<Tin, Tout, true>, grid, dim3(threads), 0, stream, 1, a);
-  return launch_pdl(qk_norm_rope_kernel<Tin, Tout, false>, grid, dim3(threads), 0, stream, 1, a);
+  if (half) return launch_pdl(qk_norm_rope_kernel<Tin, Tout, true, kLanes>, grid, dim3(threads), 0, stream, 1, a);
+  return launch_pdl(qk_norm_rope_kernel<Tin, Tout, false, kLanes>, grid, dim3(threads), 0, stream, 1, a);
 }
 
 }  // namespace
@@ -268,9 +278,12 @@ cudaError_t launch_qk_norm_rope(NormRopeArgs a, bool in_bf16, bool out_bf16, boo
   const int64_t toks = (int64_t)a.B * a.T;
   const int H = a.Hq + a.Hk;
   if (toks == 0 || H == 0) return cudaSuccess;
-  constexpr int kPer = kNrThreads / kNrLanes;  // tokens per full block
-  const int threads = toks < kPer ? (int)(toks * kNrLanes + 31) / 32 * 32 : kNrThreads;
-  const int64_t blocks = (toks + kPer - 1) / kPer;
+  // Eight lanes to a row once there are tokens enough to fill the SMs with them: fewer instructions per byte.
+  // fp32 rows keep 16 (8 would hold 64 registers of rows ahead).
+  const int lanes = in_bf16 && toks * 8 >= (int64_t)kNrThreads * kNrBlocks / 2 ? 8 : 16;
+  const int tokens = kNrThreads / lanes;  // of a full block
+  const int threads = toks < tokens ? (int)(toks * lanes + 31) / 32 * 32 : kNrThreads;
+  const int64_t blocks = (toks + tokens - 1) / tokens;
   // all heads of a token in one block (queries and keys apart) when there are tokens enough for 8 blocks per SM,
   // else the heads are divided (each part computes the angles again)
   const int64_t parts = blocks >= kNrBlocks ? 1 : (kNrBlocks + blocks - 1) / blocks;
@@ -278,11 +291,14 @@ cudaError_t launch_qk_norm_rope(NormRopeArgs a, bool in_bf16, bool out_bf16, boo
   a.heads_per_group = (int)per;
   a.q_parts = (int)((a.Hq + per - 1) / per);
   const dim3 grid((unsigned)blocks, (unsigned)(a.q_parts + (a.Hk + per - 1) / per));
-  if (in_bf16)
-    return out_bf16 ? launch<__nv_bfloat16, __nv_bfloat16>(a, half, grid, threads, stream)
-                    : launch<__nv_bfloat16, float>(a, half, grid, threads, stream);
-  return out_bf16 ? launch<float, __nv_bfloat16>(a, half, grid, threads, stream)
-                  : launch<float, float>(a, half, grid, threads, stream);
+  if (!in_bf16)
+    return out_bf16 ? launch<float, __nv_bfloat16, 16>(a, half, grid, threads, stream)
+                    : launch<float, float, 16>(a, half, grid, threads, stream);
+  if (lanes == 8)
+    return out_bf16 ? launch<__nv_bfloat16, __nv_bfloat16, 8>(a, half, grid, threads, stream)
+                    : launch<__nv_bfloat16, float, 8>(a, half, grid, threads, stream);
+  return out_bf16 ? launch<__nv_bfloat16, __nv_bfloat16, 16>(a, half, grid, threads, stream)
+                  : launch<__nv_bfloat16, float, 16>(a, half, grid, threads, stream);
 }
 
 }  // namespace rtp
