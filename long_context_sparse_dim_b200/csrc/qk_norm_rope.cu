@@ -30,8 +30,7 @@ namespace rtp {
 namespace {
 
 constexpr int kNrThreads = 256;
-constexpr int kNrAhead = 4;      // rows on their way per lane group
-constexpr int kNrBlocks = 148 * 8;
+constexpr int kNrBlocks = 148 * 4;
 
 // A lane's share of a row of kLanes lanes as raw words, in two parts of kPairs elements.  Half pairing: the
 // first members of its pairs, then the second; adjacent pairing: neighbouring dims.
@@ -180,6 +179,8 @@ template <typename Tin, typename Tout, bool kHalf, int kLanes>
 __global__ void __launch_bounds__(kNrThreads, kLanes == 8 ? 2 : 3) qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs A) {
   using Row = LaneRow<Tin, kHalf, kLanes>;
   constexpr int kPairs = Row::kPairs, kWords = kPairs / 2;  // pairs of a lane; packed words of their members
+  constexpr int kAhead = sizeof(Tin) == 2 ? 4 : 2;          // rows on their way per lane group
+  __shared__ float2 angle[kPairs][kNrThreads];              // cosine and sine, only the thread's own
   pdl_wait();
   pdl_release();
   const int lane = threadIdx.x & (kLanes - 1);
@@ -193,18 +194,19 @@ __global__ void __launch_bounds__(kNrThreads, kLanes == 8 ? 2 : 3) qk_norm_rope_
   const MutView4& out = is_q ? A.q_out : A.k_out;
 
   const Tin* src = static_cast<const Tin*>(in.data) + b * in.sb + t * in.sn + h0 * in.sh;
-  Row x[kNrAhead] = {};
+  Row x[kAhead] = {};
 #pragma unroll
-  for (int u = 0; u < kNrAhead; ++u) {
+  for (int u = 0; u < kAhead; ++u) {
     if (live && u < n) x[u].load(src, lane);
     src += in.sh;
   }
   const int64_t pos = live ? (int64_t)A.pos[b] + (A.offs ? A.offs[tok] : t) : 0;
-  float cs[kPairs], sn[kPairs];
 #pragma unroll
   for (int i = 0; i < kPairs; ++i) {
     const double turns = (double)pos * __ldg(A.inv_freq + kPairs * lane + i) * 0.15915494309189533577;  // 1 / (2 pi)
-    sincospif((float)(2.0 * (turns - rint(turns))), &sn[i], &cs[i]);
+    float2 cs;
+    sincospif((float)(2.0 * (turns - rint(turns))), &cs.y, &cs.x);
+    angle[i][threadIdx.x] = cs;
   }
 
   // The turn with the norm's weights in it: y_a = a ca + b cb, y_b = b da + a db.
@@ -229,23 +231,24 @@ __global__ void __launch_bounds__(kNrThreads, kLanes == 8 ? 2 : 3) qk_norm_rope_
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       const int j = 2 * i, k = 2 * i + 1;
-      ca[i] = pack2(wa[j] * cs[j], wa[k] * cs[k]);
-      cb[i] = pack2(-(wb[j] * sn[j]), -(wb[k] * sn[k]));
-      da[i] = pack2(wb[j] * cs[j], wb[k] * cs[k]);
-      db[i] = pack2(wa[j] * sn[j], wa[k] * sn[k]);
+      const float2 aj = angle[j][threadIdx.x], ak = angle[k][threadIdx.x];
+      ca[i] = pack2(wa[j] * aj.x, wa[k] * ak.x);
+      cb[i] = pack2(-(wb[j] * aj.y), -(wb[k] * ak.y));
+      da[i] = pack2(wb[j] * aj.x, wb[k] * ak.x);
+      db[i] = pack2(wa[j] * aj.y, wa[k] * ak.y);
     }
   };
   turn(h0);
 
   Tout* dst = static_cast<Tout*>(out.data) + b * out.sb + t * out.sn + h0 * out.sh;
 #pragma unroll 1
-  for (int h = 0; h < n; h += kNrAhead) {
+  for (int h = 0; h < n; h += kAhead) {
 #pragma unroll
-    for (int u = 0; u < kNrAhead; ++u) {
+    for (int u = 0; u < kAhead; ++u) {
       if (h + u >= n) break;  // uniform over the block
       float fa[kPairs], fb[kPairs];
       x[u].to_float(fa, fb);
-      if (live && h + u + kNrAhead < n) x[u].load(src, lane);
+      if (live && h + u + kAhead < n) x[u].load(src, lane);
       src += in.sh;
       uint64_t a[kWords], c[kWords];
 #pragma unroll
@@ -280,11 +283,11 @@ cudaError_t launch_qk_norm_rope(NormRopeArgs a, bool in_bf16, bool out_bf16, boo
   if (toks == 0 || H == 0) return cudaSuccess;
   // Eight lanes to a row once there are tokens enough to fill the SMs with them: fewer instructions per byte.
   // fp32 rows keep 16 (8 would hold 64 registers of rows ahead).
-  const int lanes = in_bf16 && toks * 8 >= (int64_t)kNrThreads * kNrBlocks / 2 ? 8 : 16;
+  const int lanes = in_bf16 && toks * 8 >= (int64_t)kNrThreads * kNrBlocks ? 8 : 16;
   const int tokens = kNrThreads / lanes;  // of a full block
   const int threads = toks < tokens ? (int)(toks * lanes + 31) / 32 * 32 : kNrThreads;
   const int64_t blocks = (toks + tokens - 1) / tokens;
-  // all heads of a token in one block (queries and keys apart) when there are tokens enough for 8 blocks per SM,
+  // all heads of a token in one block (queries and keys apart) when there are tokens enough for 4 blocks per SM,
   // else the heads are divided (each part computes the angles again)
   const int64_t parts = blocks >= kNrBlocks ? 1 : (kNrBlocks + blocks - 1) / blocks;
   const int64_t per = (H + parts - 1) / parts;
