@@ -18,9 +18,13 @@
 // min(n, W) stored ring rows; the kernel writes that length per sequence, and
 // the sequence length after the append (the next append's position).
 //
-// rtp_kv_accept is the same pass over some of the T rows: step i of sequence b
-// takes row path[b][i] (the accepted tokens of a drafted tree, root first), for
-// the first count[b] steps.
+// rtp_kv_accept does the same for some of the T rows: step i of sequence b takes
+// row path[b][i] (the accepted tokens of a drafted tree, root first), for the
+// first count[b] steps.  There a warp takes 8 neighbouring steps of one
+// (sequence, KV head): their row numbers are one load away and cover for each
+// other's latency, the steps past count cost nothing, and one read of P serves
+// all rows.  (Rows a grid apart, as the append takes them, had half of the slots
+// empty and twice the waits: 64 sequences of up to 256 accepted drafts, 48 us.)
 #include "common.cuh"
 #include "launch.h"
 #include "project.cuh"
@@ -59,11 +63,9 @@ struct Row4 {
 
 constexpr int kAppSmemHeads = 8;  // P of up to this many retrieval heads is staged in shared memory
 
-// kPath: step t of sequence b takes row path[b][t] of the new rows, for t < count[b]; else row t, t < T.
-template <typename T, bool kPath>
+template <typename T>
 __global__ void __launch_bounds__(kAppThreads, 3)
 kv_append_kernel(KvAppendArgs A) {
-  const int steps = kPath ? A.A : A.T;
   // P [R, 16, 128] f32 in shared memory (32 KB per 4 heads), read there by every projection
   extern __shared__ float4 p_smem[];
   const bool p_in_smem = A.R <= kAppSmemHeads;
@@ -75,7 +77,7 @@ kv_append_kernel(KvAppendArgs A) {
   const int lane = threadIdx.x & 31;
   const int64_t warp0 = ((int64_t)blockIdx.x * kAppThreads + threadIdx.x) >> 5;
   const int64_t nwarps = ((int64_t)gridDim.x * kAppThreads) >> 5;
-  const int64_t rows = (int64_t)A.B * A.H * steps;
+  const int64_t rows = (int64_t)A.B * A.H * A.T;
   for (int64_t r0 = warp0; r0 < rows; r0 += kAppUnroll * nwarps) {
     // up to kAppUnroll rows of this warp: every load first, then the writes
     Row4<T> kx[kAppUnroll], vx[kAppUnroll];
@@ -88,16 +90,9 @@ kv_append_kernel(KvAppendArgs A) {
       const int64_t r = r0 + u * nwarps;
       kdst[u] = nullptr;
       if (r >= rows) continue;
-      const int t = (int)(r % steps);
-      const int64_t bh = r / steps;
+      const int t = (int)(r % A.T);
+      const int64_t bh = r / A.T;
       const int h = (int)(bh % A.H), b = (int)(bh / A.H);
-      int n_new = steps, src = t;  // rows this sequence appends; the row of this step
-      if (kPath) {
-        n_new = min(max(A.count[b], 0), steps);
-        if (t >= n_new) continue;
-        src = A.path[(int64_t)b * steps + t];
-        if (src < 0 || src >= A.T) continue;  // no such row: nothing written
-      }
       const int p = A.pos[b] + t;  // position of this token in its sequence
       hrow[u] = h;
       idst[u] = nullptr;
@@ -108,15 +103,15 @@ kv_append_kernel(KvAppendArgs A) {
         idst[u] = static_cast<T*>(A.k_idx.data) + b * A.k_idx.sb + h * A.k_idx.sh + (int64_t)p * A.k_idx.sn;
       } else {
         // only the last W tokens of the append are kept (two tokens W apart share a slot)
-        if (p < 0 || t < n_new - A.W) continue;
+        if (p < 0 || t < A.T - A.W) continue;
         const int l = h - A.R;
         const int slot = p % A.W;
         kdst[u] = static_cast<T*>(A.k_ring.data) + b * A.k_ring.sb + l * A.k_ring.sh + (int64_t)slot * A.k_ring.sn;
         vdst[u] = static_cast<T*>(A.v_ring.data) + b * A.v_ring.sb + l * A.v_ring.sh + (int64_t)slot * A.v_ring.sn;
       }
-      kx[u].load(static_cast<const T*>(A.k_new.data) + b * A.k_new.sb + h * A.k_new.sh + (int64_t)src * A.k_new.sn,
+      kx[u].load(static_cast<const T*>(A.k_new.data) + b * A.k_new.sb + h * A.k_new.sh + (int64_t)t * A.k_new.sn,
                  lane);
-      vx[u].load(static_cast<const T*>(A.v_new.data) + b * A.v_new.sb + h * A.v_new.sh + (int64_t)src * A.v_new.sn,
+      vx[u].load(static_cast<const T*>(A.v_new.data) + b * A.v_new.sb + h * A.v_new.sh + (int64_t)t * A.v_new.sn,
                  lane);
     }
 #pragma unroll
@@ -135,35 +130,115 @@ kv_append_kernel(KvAppendArgs A) {
   }
   if (blockIdx.x == 0) {
     for (int b = threadIdx.x; b < A.B; b += kAppThreads) {
-      // one past the last appended position
-      const int end = A.pos[b] + (kPath ? min(max(A.count[b], 0), steps) : steps);
+      const int end = A.pos[b] + A.T;  // one past the last appended position
       if (A.lens_out) A.lens_out[b] = A.R > 0 ? max(min(end, A.N), 0) : max(end, 0);
       if (A.ring_lens) A.ring_lens[b] = max(min(end, A.W), 0);
     }
   }
 }
 
-template <typename T, bool kPath>
-cudaError_t launch(const KvAppendArgs& a, unsigned blocks, size_t smem, cudaStream_t stream) {
-  cudaFuncSetAttribute(kv_append_kernel<T, kPath>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  kv_append_kernel<T, kPath><<<blocks, kAppThreads, smem, stream>>>(a);
-  return cudaGetLastError();
+constexpr int kAccSteps = 8;  // steps per warp
+constexpr int kAccRows = 4;   // of them with their rows in flight together
+
+template <typename T>
+__global__ void __launch_bounds__(kAppThreads, 3)
+kv_accept_kernel(const __grid_constant__ KvAppendArgs A) {
+  pdl_wait();
+  pdl_release();
+  const int lane = threadIdx.x & 31;
+  const int chunks = (A.A + kAccSteps - 1) / kAccSteps;  // (0: only the lengths)
+  const int64_t item = ((int64_t)blockIdx.x * kAppThreads + threadIdx.x) >> 5;
+  if (item < (int64_t)A.B * A.H * chunks) {
+    const int64_t bh = item / chunks;
+    const int t0 = (int)(item - bh * chunks) * kAccSteps;
+    const int b = (int)(bh / A.H), h = (int)(bh - (int64_t)b * A.H);
+    const int n = min(max(A.count[b], 0), A.A), pos = A.pos[b];
+    // lane i < kAccSteps: the row that step t0 + i takes, or -1 (none, or nowhere to keep it)
+    int row = -1;
+    if (lane < kAccSteps && t0 + lane < n) {
+      const int t = t0 + lane, p = pos + t;
+      row = A.path[(int64_t)b * A.A + t];
+      if (row >= A.T || p < 0) row = -1;
+      // outside the cache; or pushed out of the ring by a later step (two tokens W apart share a slot)
+      if (h < A.R ? p >= A.N : t < n - A.W) row = -1;
+    }
+    if (__any_sync(0xffffffffu, row >= 0)) {
+      const bool ret = h < A.R;
+      const int l = h - A.R;
+      const T* kn = static_cast<const T*>(A.k_new.data) + b * A.k_new.sb + h * A.k_new.sh;
+      const T* vn = static_cast<const T*>(A.v_new.data) + b * A.v_new.sb + h * A.v_new.sh;
+      const MutView4& kd = ret ? A.k_cache : A.k_ring;
+      const MutView4& vd = ret ? A.v_cache : A.v_ring;
+      T* ko = static_cast<T*>(kd.data) + b * kd.sb + (ret ? h : l) * kd.sh;
+      T* vo = static_cast<T*>(vd.data) + b * vd.sb + (ret ? h : l) * vd.sh;
+#pragma unroll 1
+      for (int i0 = 0; i0 < kAccSteps; i0 += kAccRows) {
+        Row4<T> kx[kAccRows], vx[kAccRows];
+        int src[kAccRows];
+#pragma unroll
+        for (int i = 0; i < kAccRows; ++i) {
+          src[i] = __shfl_sync(0xffffffffu, row, i0 + i);
+          if (src[i] < 0) continue;  // warp-uniform
+          kx[i].load(kn + (int64_t)src[i] * A.k_new.sn, lane);
+          vx[i].load(vn + (int64_t)src[i] * A.v_new.sn, lane);
+        }
+#pragma unroll
+        for (int i = 0; i < kAccRows; ++i) {
+          if (src[i] < 0) continue;
+          const int p = pos + t0 + i0 + i, at = ret ? p : p % A.W;
+          kx[i].store(ko + (int64_t)at * kd.sn, lane);
+          vx[i].store(vo + (int64_t)at * vd.sn, lane);
+        }
+        if (!ret) continue;
+        const float4* P4 = reinterpret_cast<const float4*>(A.P) + (int64_t)h * kIdxDim * (kHeadDim / 4) + lane;
+        T* io = static_cast<T*>(A.k_idx.data) + b * A.k_idx.sb + h * A.k_idx.sh;
+#pragma unroll
+        for (int i = 0; i < kAccRows; ++i) {
+          if (src[i] < 0) continue;
+          float xv[4];
+          kx[i].to_float(xv);
+          project_row_with<T>([&](int j) { return __ldg(P4 + j * (kHeadDim / 4)); }, xv, lane,
+                              io + (int64_t)(pos + t0 + i0 + i) * A.k_idx.sn);
+        }
+      }
+    }
+  }
+  if (blockIdx.x == 0) {
+    for (int b = threadIdx.x; b < A.B; b += kAppThreads) {
+      const int end = A.pos[b] + min(max(A.count[b], 0), A.A);  // one past the last appended position
+      if (A.lens_out) A.lens_out[b] = A.R > 0 ? max(min(end, A.N), 0) : max(end, 0);
+      if (A.ring_lens) A.ring_lens[b] = max(min(end, A.W), 0);
+    }
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append(const KvAppendArgs& a, bool bf16, cudaStream_t stream) {
-  const int64_t rows = (int64_t)a.B * a.H * (a.path ? a.A : a.T);
+  const int64_t rows = (int64_t)a.B * a.H * a.T;
   if (a.B == 0 || (rows == 0 && !a.lens_out && !a.ring_lens)) return cudaSuccess;
   int64_t blocks = (rows + kAppUnroll * (kAppThreads / 32) - 1) / (kAppUnroll * (kAppThreads / 32));
   if (blocks < 1) blocks = 1;  // an empty append still writes the lengths
   if (blocks > 148 * 16) blocks = 148 * 16;
   const size_t smem = a.R <= kAppSmemHeads ? (size_t)a.R * kIdxDim * kHeadDim * sizeof(float) : 0;
-  if (a.path)
-    return bf16 ? launch<__nv_bfloat16, true>(a, (unsigned)blocks, smem, stream)
-                : launch<float, true>(a, (unsigned)blocks, smem, stream);
-  return bf16 ? launch<__nv_bfloat16, false>(a, (unsigned)blocks, smem, stream)
-              : launch<float, false>(a, (unsigned)blocks, smem, stream);
+  if (bf16) {
+    cudaFuncSetAttribute(kv_append_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    kv_append_kernel<__nv_bfloat16><<<(unsigned)blocks, kAppThreads, smem, stream>>>(a);
+  } else {
+    cudaFuncSetAttribute(kv_append_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    kv_append_kernel<float><<<(unsigned)blocks, kAppThreads, smem, stream>>>(a);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_accept(const KvAppendArgs& a, bool bf16, cudaStream_t stream) {
+  if (a.B == 0) return cudaSuccess;
+  const int64_t items = (int64_t)a.B * a.H * ((a.A + kAccSteps - 1) / kAccSteps);
+  const int64_t blocks = items ? (items + kAppThreads / 32 - 1) / (kAppThreads / 32) : 1;  // (1: the lengths)
+  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const dim3 grid((unsigned)blocks), block(kAppThreads);
+  return bf16 ? launch_pdl(kv_accept_kernel<__nv_bfloat16>, grid, block, 0, stream, 1, a)
+              : launch_pdl(kv_accept_kernel<float>, grid, block, 0, stream, 1, a);
 }
 
 }  // namespace rtp

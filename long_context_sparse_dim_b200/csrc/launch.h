@@ -182,6 +182,7 @@ struct KvAppendArgs {
   int A = 0;
 };
 cudaError_t launch_kv_append(const KvAppendArgs& a, bool bf16, cudaStream_t stream);
+cudaError_t launch_kv_accept(const KvAppendArgs& a, bool bf16, cudaStream_t stream);
 
 // Per-head norm and position rotation (rtp_qk_norm_rope).
 struct NormRopeArgs {

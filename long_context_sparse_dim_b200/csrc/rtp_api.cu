@@ -326,7 +326,7 @@ rtp_status rtp_kv_accept(const rtp_tensor* k_new, const rtp_tensor* v_new, const
   a.path = path;
   a.count = count;
   a.A = A;
-  return cuda_status(rtp::launch_kv_append(a, k_new->dtype == RTP_BF16, (cudaStream_t)stream));
+  return cuda_status(rtp::launch_kv_accept(a, k_new->dtype == RTP_BF16, (cudaStream_t)stream));
 }
 
 // ---- per-head norm and rotation --------------------------------------------------------
