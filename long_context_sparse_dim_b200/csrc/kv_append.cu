@@ -138,11 +138,11 @@ kv_append_kernel(KvAppendArgs A) {
 }
 
 constexpr int kAccSteps = 8;  // steps per warp
-constexpr int kAccRows = 4;   // of them with their rows in flight together
 
 template <typename T>
-__global__ void __launch_bounds__(kAppThreads, 3)
+__global__ void __launch_bounds__(kAppThreads, sizeof(T) == 2 ? 4 : 3)
 kv_accept_kernel(const __grid_constant__ KvAppendArgs A) {
+  constexpr int kAccRows = sizeof(T) == 2 ? 8 : 4;  // rows in flight together
   pdl_wait();
   pdl_release();
   const int lane = threadIdx.x & 31;
@@ -152,13 +152,13 @@ kv_accept_kernel(const __grid_constant__ KvAppendArgs A) {
     const int64_t bh = item / chunks;
     const int t0 = (int)(item - bh * chunks) * kAccSteps;
     const int b = (int)(bh / A.H), h = (int)(bh - (int64_t)b * A.H);
+    const int given = lane < kAccSteps && t0 + lane < A.A ? A.path[(int64_t)b * A.A + t0 + lane] : -1;
     const int n = min(max(A.count[b], 0), A.A), pos = A.pos[b];
     // lane i < kAccSteps: the row that step t0 + i takes, or -1 (none, or nowhere to keep it)
     int row = -1;
     if (lane < kAccSteps && t0 + lane < n) {
       const int t = t0 + lane, p = pos + t;
-      row = A.path[(int64_t)b * A.A + t];
-      if (row >= A.T || p < 0) row = -1;
+      row = given < A.T && p >= 0 ? given : -1;
       // outside the cache; or pushed out of the ring by a later step (two tokens W apart share a slot)
       if (h < A.R ? p >= A.N : t < n - A.W) row = -1;
     }
