@@ -20,10 +20,9 @@
 //
 // rtp_kv_accept does the same for some of the T rows: step i of sequence b takes
 // row path[b][i] (the accepted tokens of a drafted tree, root first), for the
-// first count[b] steps.  There a warp takes 8 neighbouring steps of one
+// first count[b] steps.  There a warp takes up to 8 neighbouring steps of one
 // (sequence, KV head): their row numbers are one load away and cover for each
-// other's latency, the steps past count cost nothing, and one read of P serves
-// all rows.  (Rows a grid apart, as the append takes them, had half of the slots
+// other's latency, and the steps past count cost nothing.  (Rows a grid apart, as the append takes them, had half of the slots
 // empty and twice the waits: 64 sequences of up to 256 accepted drafts, 48 us.)
 #include "common.cuh"
 #include "launch.h"
@@ -137,72 +136,81 @@ kv_append_kernel(KvAppendArgs A) {
   }
 }
 
-constexpr int kAccSteps = 8;  // steps per warp
+// Steps per warp: a projection is some 300 instructions of one warp, so that 8 of them in a row were the longest
+// wait of all (23 us, against 8 rows that are only copied).
+constexpr int kAccSteps = 8, kAccRetSteps = 2;
+
+// One warp: steps t0 .. t0 + kSteps - 1 of sequence b, KV head h (kRet: a retrieval head).
+template <typename T, int kSteps, bool kRet>
+RTP_DEVICE void accept_steps(const KvAppendArgs& A, int b, int h, int t0, int lane) {
+  constexpr int kRows = sizeof(T) == 2 || kSteps <= 4 ? kSteps : 4;  // rows in flight together
+  const int given = lane < kSteps && t0 + lane < A.A ? A.path[(int64_t)b * A.A + t0 + lane] : -1;
+  const int n = min(max(A.count[b], 0), A.A), pos = A.pos[b];
+  // lane i < kSteps: the row that step t0 + i takes, or -1 (none, or nowhere to keep it: outside the cache, or
+  // pushed out of the ring by a later step, since two tokens W apart share a slot)
+  int row = -1;
+  if (lane < kSteps && t0 + lane < n) {
+    const int t = t0 + lane, p = pos + t;
+    row = given < A.T && p >= 0 ? given : -1;
+    if (kRet ? p >= A.N : t < n - A.W) row = -1;
+  }
+  if (!__any_sync(0xffffffffu, row >= 0)) return;
+  const T* kn = static_cast<const T*>(A.k_new.data) + b * A.k_new.sb + h * A.k_new.sh;
+  const T* vn = static_cast<const T*>(A.v_new.data) + b * A.v_new.sb + h * A.v_new.sh;
+  const MutView4& kd = kRet ? A.k_cache : A.k_ring;
+  const MutView4& vd = kRet ? A.v_cache : A.v_ring;
+  const int l = kRet ? h : h - A.R;
+  T* ko = static_cast<T*>(kd.data) + b * kd.sb + l * kd.sh;
+  T* vo = static_cast<T*>(vd.data) + b * vd.sb + l * vd.sh;
+#pragma unroll 1
+  for (int i0 = 0; i0 < kSteps; i0 += kRows) {
+    Row4<T> kx[kRows], vx[kRows];
+    int src[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      src[i] = __shfl_sync(0xffffffffu, row, i0 + i);
+      if (src[i] < 0) continue;  // warp-uniform
+      kx[i].load(kn + (int64_t)src[i] * A.k_new.sn, lane);
+      vx[i].load(vn + (int64_t)src[i] * A.v_new.sn, lane);
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      if (src[i] < 0) continue;
+      const int p = pos + t0 + i0 + i, at = kRet ? p : p % A.W;
+      kx[i].store(ko + (int64_t)at * kd.sn, lane);
+      vx[i].store(vo + (int64_t)at * vd.sn, lane);
+    }
+    if constexpr (kRet) {
+      const float4* P4 = reinterpret_cast<const float4*>(A.P) + (int64_t)h * kIdxDim * (kHeadDim / 4) + lane;
+      T* io = static_cast<T*>(A.k_idx.data) + b * A.k_idx.sb + h * A.k_idx.sh;
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        if (src[i] < 0) continue;
+        float xv[4];
+        kx[i].to_float(xv);
+        project_row_with<T>([&](int j) { return __ldg(P4 + j * (kHeadDim / 4)); }, xv, lane,
+                            io + (int64_t)(pos + t0 + i0 + i) * A.k_idx.sn);
+      }
+    }
+  }
+}
 
 template <typename T>
 __global__ void __launch_bounds__(kAppThreads, sizeof(T) == 2 ? 4 : 3)
 kv_accept_kernel(const __grid_constant__ KvAppendArgs A) {
-  constexpr int kAccRows = sizeof(T) == 2 ? 8 : 4;  // rows in flight together
   pdl_wait();
   pdl_release();
-  const int lane = threadIdx.x & 31;
-  const int chunks = (A.A + kAccSteps - 1) / kAccSteps;  // (0: only the lengths)
+  const int lane = threadIdx.x & 31, L = A.H - A.R;
   const int64_t item = ((int64_t)blockIdx.x * kAppThreads + threadIdx.x) >> 5;
-  if (item < (int64_t)A.B * A.H * chunks) {
-    const int64_t bh = item / chunks;
-    const int t0 = (int)(item - bh * chunks) * kAccSteps;
-    const int b = (int)(bh / A.H), h = (int)(bh - (int64_t)b * A.H);
-    const int given = lane < kAccSteps && t0 + lane < A.A ? A.path[(int64_t)b * A.A + t0 + lane] : -1;
-    const int n = min(max(A.count[b], 0), A.A), pos = A.pos[b];
-    // lane i < kAccSteps: the row that step t0 + i takes, or -1 (none, or nowhere to keep it)
-    int row = -1;
-    if (lane < kAccSteps && t0 + lane < n) {
-      const int t = t0 + lane, p = pos + t;
-      row = given < A.T && p >= 0 ? given : -1;
-      // outside the cache; or pushed out of the ring by a later step (two tokens W apart share a slot)
-      if (h < A.R ? p >= A.N : t < n - A.W) row = -1;
-    }
-    if (__any_sync(0xffffffffu, row >= 0)) {
-      const bool ret = h < A.R;
-      const int l = h - A.R;
-      const T* kn = static_cast<const T*>(A.k_new.data) + b * A.k_new.sb + h * A.k_new.sh;
-      const T* vn = static_cast<const T*>(A.v_new.data) + b * A.v_new.sb + h * A.v_new.sh;
-      const MutView4& kd = ret ? A.k_cache : A.k_ring;
-      const MutView4& vd = ret ? A.v_cache : A.v_ring;
-      T* ko = static_cast<T*>(kd.data) + b * kd.sb + (ret ? h : l) * kd.sh;
-      T* vo = static_cast<T*>(vd.data) + b * vd.sb + (ret ? h : l) * vd.sh;
-#pragma unroll 1
-      for (int i0 = 0; i0 < kAccSteps; i0 += kAccRows) {
-        Row4<T> kx[kAccRows], vx[kAccRows];
-        int src[kAccRows];
-#pragma unroll
-        for (int i = 0; i < kAccRows; ++i) {
-          src[i] = __shfl_sync(0xffffffffu, row, i0 + i);
-          if (src[i] < 0) continue;  // warp-uniform
-          kx[i].load(kn + (int64_t)src[i] * A.k_new.sn, lane);
-          vx[i].load(vn + (int64_t)src[i] * A.v_new.sn, lane);
-        }
-#pragma unroll
-        for (int i = 0; i < kAccRows; ++i) {
-          if (src[i] < 0) continue;
-          const int p = pos + t0 + i0 + i, at = ret ? p : p % A.W;
-          kx[i].store(ko + (int64_t)at * kd.sn, lane);
-          vx[i].store(vo + (int64_t)at * vd.sn, lane);
-        }
-        if (!ret) continue;
-        const float4* P4 = reinterpret_cast<const float4*>(A.P) + (int64_t)h * kIdxDim * (kHeadDim / 4) + lane;
-        T* io = static_cast<T*>(A.k_idx.data) + b * A.k_idx.sb + h * A.k_idx.sh;
-#pragma unroll
-        for (int i = 0; i < kAccRows; ++i) {
-          if (src[i] < 0) continue;
-          float xv[4];
-          kx[i].to_float(xv);
-          project_row_with<T>([&](int j) { return __ldg(P4 + j * (kHeadDim / 4)); }, xv, lane,
-                              io + (int64_t)(pos + t0 + i0 + i) * A.k_idx.sn);
-        }
-      }
-    }
-  }
+  const int ret_chunks = (A.A + kAccRetSteps - 1) / kAccRetSteps, loc_chunks = (A.A + kAccSteps - 1) / kAccSteps;
+  const int64_t ret_items = (int64_t)A.B * A.R * ret_chunks;
+  if (item < ret_items)
+    accept_steps<T, kAccRetSteps, true>(A, (int)(item / ret_chunks / A.R), (int)(item / ret_chunks % A.R),
+                                        (int)(item % ret_chunks) * kAccRetSteps, lane);
+  else if (item - ret_items < (int64_t)A.B * L * loc_chunks)
+    accept_steps<T, kAccSteps, false>(A, (int)((item - ret_items) / loc_chunks / L),
+                                      A.R + (int)((item - ret_items) / loc_chunks % L),
+                                      (int)((item - ret_items) % loc_chunks) * kAccSteps, lane);
   if (blockIdx.x == 0) {
     for (int b = threadIdx.x; b < A.B; b += kAppThreads) {
       const int end = A.pos[b] + min(max(A.count[b], 0), A.A);  // one past the last appended position
@@ -233,7 +241,8 @@ cudaError_t launch_kv_append(const KvAppendArgs& a, bool bf16, cudaStream_t stre
 
 cudaError_t launch_kv_accept(const KvAppendArgs& a, bool bf16, cudaStream_t stream) {
   if (a.B == 0) return cudaSuccess;
-  const int64_t items = (int64_t)a.B * a.H * ((a.A + kAccSteps - 1) / kAccSteps);
+  const int64_t items = (int64_t)a.B * (a.R * (int64_t)((a.A + kAccRetSteps - 1) / kAccRetSteps) +
+                                        (a.H - a.R) * (int64_t)((a.A + kAccSteps - 1) / kAccSteps));
   const int64_t blocks = items ? (items + kAppThreads / 32 - 1) / (kAppThreads / 32) : 1;  // (1: the lengths)
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   const dim3 grid((unsigned)blocks), block(kAppThreads);
