@@ -136,34 +136,33 @@ kv_append_kernel(KvAppendArgs A) {
   }
 }
 
-// Steps per warp: a projection is some 300 instructions of one warp, so that 8 of them in a row were the longest
-// wait of all (23 us, against 8 rows that are only copied).
-constexpr int kAccSteps = 8, kAccRetSteps = 2;
+// Steps per warp: of a local head (copies), of a retrieval head (copies and projections, four rows at once).
+constexpr int kAccSteps = 8, kAccRetSteps = 4;
 
-// One warp: steps t0 .. t0 + kSteps - 1 of sequence b, KV head h (kRet: a retrieval head).
-template <typename T, int kSteps, bool kRet>
-RTP_DEVICE void accept_steps(const KvAppendArgs& A, int b, int h, int t0, int lane) {
-  constexpr int kRows = sizeof(T) == 2 || kSteps <= 4 ? kSteps : 4;  // rows in flight together
-  const int given = lane < kSteps && t0 + lane < A.A ? A.path[(int64_t)b * A.A + t0 + lane] : -1;
-  const int n = min(max(A.count[b], 0), A.A), pos = A.pos[b];
-  // lane i < kSteps: the row that step t0 + i takes, or -1 (none, or nowhere to keep it: outside the cache, or
-  // pushed out of the ring by a later step, since two tokens W apart share a slot)
-  int row = -1;
-  if (lane < kSteps && t0 + lane < n) {
-    const int t = t0 + lane, p = pos + t;
-    row = given < A.T && p >= 0 ? given : -1;
-    if (kRet ? p >= A.N : t < n - A.W) row = -1;
-  }
+// Lane i < kSteps: the row that step t0 + i of sequence b takes, or -1 (none, or nowhere to keep it: outside the
+// cache, or pushed out of the ring by a later step, since two tokens W apart share a slot).
+template <int kSteps, bool kRet>
+RTP_DEVICE int accepted_row(const KvAppendArgs& A, int b, int t0, int lane) {
+  const int t = t0 + lane;
+  const int given = lane < kSteps && t < A.A ? A.path[(int64_t)b * A.A + t] : -1;
+  const int n = min(max(A.count[b], 0), A.A), p = A.pos[b] + t;
+  if (lane >= kSteps || t >= n || given >= A.T || p < 0) return -1;
+  return (kRet ? p >= A.N : t < n - A.W) ? -1 : given;
+}
+
+// One warp: kAccSteps steps of a local head.
+template <typename T>
+RTP_DEVICE void accept_local(const KvAppendArgs& A, int b, int h, int t0, int lane) {
+  constexpr int kRows = sizeof(T) == 2 ? kAccSteps : kAccSteps / 2;  // rows in flight together
+  const int row = accepted_row<kAccSteps, false>(A, b, t0, lane);
   if (!__any_sync(0xffffffffu, row >= 0)) return;
+  const int p0 = A.pos[b] + t0, l = h - A.R;
   const T* kn = static_cast<const T*>(A.k_new.data) + b * A.k_new.sb + h * A.k_new.sh;
   const T* vn = static_cast<const T*>(A.v_new.data) + b * A.v_new.sb + h * A.v_new.sh;
-  const MutView4& kd = kRet ? A.k_cache : A.k_ring;
-  const MutView4& vd = kRet ? A.v_cache : A.v_ring;
-  const int l = kRet ? h : h - A.R;
-  T* ko = static_cast<T*>(kd.data) + b * kd.sb + l * kd.sh;
-  T* vo = static_cast<T*>(vd.data) + b * vd.sb + l * vd.sh;
+  T* ko = static_cast<T*>(A.k_ring.data) + b * A.k_ring.sb + l * A.k_ring.sh;
+  T* vo = static_cast<T*>(A.v_ring.data) + b * A.v_ring.sb + l * A.v_ring.sh;
 #pragma unroll 1
-  for (int i0 = 0; i0 < kSteps; i0 += kRows) {
+  for (int i0 = 0; i0 < kAccSteps; i0 += kRows) {
     Row4<T> kx[kRows], vx[kRows];
     int src[kRows];
 #pragma unroll
@@ -176,42 +175,90 @@ RTP_DEVICE void accept_steps(const KvAppendArgs& A, int b, int h, int t0, int la
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       if (src[i] < 0) continue;
-      const int p = pos + t0 + i0 + i, at = kRet ? p : p % A.W;
-      kx[i].store(ko + (int64_t)at * kd.sn, lane);
-      vx[i].store(vo + (int64_t)at * vd.sn, lane);
-    }
-    if constexpr (kRet) {
-      const float4* P4 = reinterpret_cast<const float4*>(A.P) + (int64_t)h * kIdxDim * (kHeadDim / 4) + lane;
-      T* io = static_cast<T*>(A.k_idx.data) + b * A.k_idx.sb + h * A.k_idx.sh;
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        if (src[i] < 0) continue;
-        float xv[4];
-        kx[i].to_float(xv);
-        project_row_with<T>([&](int j) { return __ldg(P4 + j * (kHeadDim / 4)); }, xv, lane,
-                            io + (int64_t)(pos + t0 + i0 + i) * A.k_idx.sn);
-      }
+      const int at = (p0 + i0 + i) % A.W;
+      kx[i].store(ko + (int64_t)at * A.k_ring.sn, lane);
+      vx[i].store(vo + (int64_t)at * A.v_ring.sn, lane);
     }
   }
 }
 
+// One warp: kAccRetSteps steps of a retrieval head, eight lanes to a row.  Lane s of a row holds its 4-element
+// chunks s, s + 8, s + 16 and s + 24, so that the first two levels of the projection's sum (chunks 16, then 8
+// apart, the order of project_row_with) stay in the lane, and a load of P serves four rows.
 template <typename T>
-__global__ void __launch_bounds__(kAppThreads, sizeof(T) == 2 ? 4 : 3)
+RTP_DEVICE void accept_retrieval(const KvAppendArgs& A, int b, int h, int t0, int lane) {
+  const int mine = accepted_row<kAccRetSteps, true>(A, b, t0, lane);
+  if (!__any_sync(0xffffffffu, mine >= 0)) return;
+  const int g = lane >> 3, s = lane & 7;
+  const int src = __shfl_sync(0xffffffffu, mine, g);
+  const bool live = src >= 0;
+  const int64_t p = A.pos[b] + t0 + g, r = live ? src : 0;
+  const T* kn = static_cast<const T*>(A.k_new.data) + b * A.k_new.sb + h * A.k_new.sh + r * A.k_new.sn;
+  const T* vn = static_cast<const T*>(A.v_new.data) + b * A.v_new.sb + h * A.v_new.sh + r * A.v_new.sn;
+  T* ko = static_cast<T*>(A.k_cache.data) + b * A.k_cache.sb + h * A.k_cache.sh + p * A.k_cache.sn;
+  T* vo = static_cast<T*>(A.v_cache.data) + b * A.v_cache.sb + h * A.v_cache.sh + p * A.v_cache.sn;
+  float x[4][4];
+  {
+    Row4<T> kx[4], vx[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      kx[c].x = {};
+      if (!live) continue;
+      kx[c].load(kn, s + 8 * c);
+      vx[c].load(vn, s + 8 * c);
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      kx[c].to_float(x[c]);
+      if (!live) continue;
+      kx[c].store(ko, s + 8 * c);
+      vx[c].store(vo, s + 8 * c);
+    }
+  }
+  const float4* P4 = reinterpret_cast<const float4*>(A.P) + (int64_t)h * kIdxDim * (kHeadDim / 4) + s;
+  float acc[kIdxDim];
+#pragma unroll
+  for (int j = 0; j < kIdxDim; ++j) {
+    float a[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float4 q = __ldg(P4 + j * (kHeadDim / 4) + 8 * c);
+      a[c] = __fmul_rn(q.x, x[c][0]);
+      a[c] = __fmaf_rn(q.y, x[c][1], a[c]);
+      a[c] = __fmaf_rn(q.z, x[c][2], a[c]);
+      a[c] = __fmaf_rn(q.w, x[c][3], a[c]);
+    }
+    acc[j] = (a[0] + a[2]) + (a[1] + a[3]);
+  }
+  halve<16>(acc, lane, 4);
+  halve<8>(acc, lane, 2);
+  halve<4>(acc, lane, 1);  // (lane s: outputs 2 s and 2 s + 1)
+  if (live) {
+    T* io = static_cast<T*>(A.k_idx.data) + b * A.k_idx.sb + h * A.k_idx.sh + p * A.k_idx.sn + 2 * s;
+    store1<T>(io, acc[0]);
+    store1<T>(io + 1, acc[1]);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kAppThreads, 3)
 kv_accept_kernel(const __grid_constant__ KvAppendArgs A) {
   pdl_wait();
   pdl_release();
-  const int lane = threadIdx.x & 31, L = A.H - A.R;
-  const int64_t item = ((int64_t)blockIdx.x * kAppThreads + threadIdx.x) >> 5;
-  const int ret_chunks = (A.A + kAccRetSteps - 1) / kAccRetSteps, loc_chunks = (A.A + kAccSteps - 1) / kAccSteps;
-  const int64_t ret_items = (int64_t)A.B * A.R * ret_chunks;
-  if (item < ret_items)
-    accept_steps<T, kAccRetSteps, true>(A, (int)(item / ret_chunks / A.R), (int)(item / ret_chunks % A.R),
-                                        (int)(item % ret_chunks) * kAccRetSteps, lane);
-  else if (item - ret_items < (int64_t)A.B * L * loc_chunks)
-    accept_steps<T, kAccSteps, false>(A, (int)((item - ret_items) / loc_chunks / L),
-                                      A.R + (int)((item - ret_items) / loc_chunks % L),
-                                      (int)((item - ret_items) % loc_chunks) * kAccSteps, lane);
-  if (blockIdx.x == 0) {
+  const int lane = threadIdx.x & 31;
+  const unsigned ret_chunks = (A.A + kAccRetSteps - 1) / kAccRetSteps, loc_chunks = (A.A + kAccSteps - 1) / kAccSteps;
+  const unsigned ret_items = A.R * ret_chunks;
+  const unsigned item = (blockIdx.x * kAppThreads + threadIdx.x) >> 5;  // of each sequence
+  const int64_t seq = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
+  if (seq < A.B) {
+    const int b = (int)seq;
+    if (item < ret_items)
+      accept_retrieval<T>(A, b, (int)(item / ret_chunks), (int)(item % ret_chunks) * kAccRetSteps, lane);
+    else if (item - ret_items < (A.H - A.R) * loc_chunks)
+      accept_local<T>(A, b, A.R + (int)((item - ret_items) / loc_chunks),
+                      (int)((item - ret_items) % loc_chunks) * kAccSteps, lane);
+  }
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
     for (int b = threadIdx.x; b < A.B; b += kAppThreads) {
       const int end = A.pos[b] + min(max(A.count[b], 0), A.A);  // one past the last appended position
       if (A.lens_out) A.lens_out[b] = A.R > 0 ? max(min(end, A.N), 0) : max(end, 0);
@@ -241,11 +288,12 @@ cudaError_t launch_kv_append(const KvAppendArgs& a, bool bf16, cudaStream_t stre
 
 cudaError_t launch_kv_accept(const KvAppendArgs& a, bool bf16, cudaStream_t stream) {
   if (a.B == 0) return cudaSuccess;
-  const int64_t items = (int64_t)a.B * (a.R * (int64_t)((a.A + kAccRetSteps - 1) / kAccRetSteps) +
-                                        (a.H - a.R) * (int64_t)((a.A + kAccSteps - 1) / kAccSteps));
+  const int64_t items = a.R * (int64_t)((a.A + kAccRetSteps - 1) / kAccRetSteps) +
+                        (a.H - a.R) * (int64_t)((a.A + kAccSteps - 1) / kAccSteps);  // of a sequence
+  if (items * 32 > INT32_MAX) return cudaErrorInvalidConfiguration;
   const int64_t blocks = items ? (items + kAppThreads / 32 - 1) / (kAppThreads / 32) : 1;  // (1: the lengths)
-  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-  const dim3 grid((unsigned)blocks), block(kAppThreads);
+  const dim3 grid((unsigned)blocks, (unsigned)(a.B < 65535 ? a.B : 65535), (unsigned)((a.B + 65534) / 65535));
+  const dim3 block(kAppThreads);
   return bf16 ? launch_pdl(kv_accept_kernel<__nv_bfloat16>, grid, block, 0, stream, 1, a)
               : launch_pdl(kv_accept_kernel<float>, grid, block, 0, stream, 1, a);
 }
