@@ -102,8 +102,10 @@ struct TrSmem {
   alignas(1024) uint8_t k[kTrStages][kTrTile];
   alignas(1024) uint8_t v[kTrStages][kTrTile];
   alignas(1024) uint8_t p[2][2][kTrKeys * kTrStream * 2];  // [stream][hi, lo]
+  int row_at[NR];                        // each row's draft times 8 plus its head in the group
   alignas(16) float nref[2][kTrStream];  // minus the reference of each row (log2 units)
-  alignas(16) float alpha[2][kTrStream];  // 2^(old - new reference) of the last raise; at a segment's end the row sums
+  alignas(16) float alpha[2][kTrStream];  // 2^(old - new reference) of the last raise; at a segment's end their scales or 1 / sum
+  float sum[NR == 64 ? 2 : 1][NR == 64 ? kTrStream : 1];
   float wt[NR == 64 ? 2 : 1][2][NR == 64 ? kTrStream : 1];  // [stream writing][stream summed]: factors of its O
   uint32_t colmax[2][kTrStream];         // the largest sum of a row in any thread (float bits)
   uint64_t k_full[kTrStages], k_empty[kTrStages], v_full[kTrStages], v_empty[kTrStages];
@@ -153,6 +155,10 @@ RTP_DEVICE bool wait_bar(uint64_t* bar, uint32_t parity, bool& alive, const Tree
       break;
     }
   return alive;
+}
+
+RTP_DEVICE void prefetch_map(const CUtensorMap* m) {
+  asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
 }
 
 // Barrier of n threads that also ORs a predicate.
@@ -357,8 +363,7 @@ __device__ __noinline__ void scalar_row(const TreeAttnArgs& A, int b, int h, int
   out = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
 }
 
-RTP_DEVICE void store_row4(const TreeAttnArgs& A, int b, int h, int t, int lane, const float4& y) {
-  const int64_t off = b * A.o.sb + h * A.o.sh + t * A.o.sn + 4 * lane;
+RTP_DEVICE void store4(const TreeAttnArgs& A, int64_t off, const float4& y) {
   if (A.o_bf16)
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(A.o.data) + off) =
         make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
@@ -373,8 +378,8 @@ RTP_DEVICE bool finite4(const float4& y) {
 // ---- layout of the workspace -------------------------------------------------------------
 struct TrLayout {
   int nr, rbs, ranges;  // rows per CTA, row blocks per KV head, ranges of the line of tiles
-  size_t table, o, lse;  // byte sizes
-  size_t bytes() const { return table + o + lse; }
+  size_t table, o, ml;  // byte sizes
+  size_t bytes() const { return table + o + ml; }
 };
 
 TrLayout tree_layout(int64_t B, int64_t Hq, int64_t T, int64_t Hk, bool sel) {
@@ -388,7 +393,7 @@ TrLayout tree_layout(int64_t B, int64_t Hq, int64_t T, int64_t Hk, bool sel) {
   L.table = up((size_t)(B * Hk) * sizeof(int2));
   const size_t slots = (size_t)L.rbs * L.ranges * 2 * L.nr;
   L.o = up(slots * kHeadDim * sizeof(float));
-  L.lse = up(slots * sizeof(float));
+  L.ml = up(slots * sizeof(float2));
   return L;
 }
 
@@ -396,7 +401,7 @@ TrLayout tree_layout(int64_t B, int64_t Hq, int64_t T, int64_t Hk, bool sel) {
 struct TrParts {
   int2* table;  // [B * Hk] first range and number of pieces
   float* o;     // [row block][2 * ranges][nr][128]
-  float* lse;   // [row block][2 * ranges][nr] log2 of the sum of 2^logit; o is normalised
+  float2* ml;   // [row block][2 * ranges][nr] m and l, the sum of 2^logit being 2^m l; o is normalised
   int nr, rbs, ranges;
 };
 
@@ -445,6 +450,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     mbar_fence_init();
   }
   if (tid < 2 * kTrStream) S.colmax[0][tid] = 0u;
+  if (tid < NR) {
+    const int r = min(row0 + tid, rows - 1), g = r / A.T;
+    S.row_at[tid] = (r - g * A.T) * 8 + g;
+  }
+  if (use_tma && tid == kTrThreads - 1) {
+    prefetch_map(&kmap);
+    prefetch_map(&vmap);
+  }
   if (warp == 0) tmem_alloc(&S.tmem_base, kTmemCols);
   // rows past the last one never get a P: zeros
   if (nrows < NR) {
@@ -567,20 +580,18 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
 #pragma unroll 1
     while (more && ok) {
       const TrSeg s = walk.s;
-      more = walk.next(A);
-      const int seg_flags = 4 * segs, last_flags = seg_flags + 1 + (more ? 0 : 2);
+      const int seg_flags = 4 * segs, last_flags = seg_flags + (s.base + s.u1 < hi ? 1 : 3);
       // ---- the query rows (the previous segment's products are done with the buffer) ----
       {
         const bool free = segs == 0 || wait_bar(&S.q_free, (segs - 1) & 1u, alive, A);
         if (bar_or(kBarLoad, kTrLoad, !free)) break;
         const __nv_bfloat16* qb =
             static_cast<const __nv_bfloat16*>(A.q.data) + s.b * A.q.sb + (int64_t)s.kvh * A.G * A.q.sh + chunk * 8;
-#pragma unroll 2
+#pragma unroll 4
         for (int i = 0; i < NR / 8; ++i) {
-          const int r = r_first + 8 * i, rr = min(row0 + r, rows - 1);
-          const int g = rr / A.T, t = rr - g * A.T;
-          cp16(smem_addr(S.q) + (uint32_t)(chunk >> 3) * (NR * 128u) + slot0 + 1024u * i, qb + g * A.q.sh + t * A.q.sn,
-               r < nrows);
+          const int r = r_first + 8 * i, at = S.row_at[r];
+          cp16(smem_addr(S.q) + (uint32_t)(chunk >> 3) * (NR * 128u) + slot0 + 1024u * i,
+               qb + (at & 7) * A.q.sh + (at >> 3) * A.q.sn, r < nrows);
         }
         cp_commit();
         q_due = true;
@@ -609,6 +620,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         ++segs;
       }
       const int drafts_end = min(s.u1, s.span.draft_tiles);
+      more = walk.next(A);
       for (int u = s.u0; u < drafts_end && ok; ++u)
         ok = gather(A.kn, A.vn, s, u, u + 1 == s.u1 ? last_flags : seg_flags, [&](int r, bool& live) {
           const int j = u * kTrKeys + r;
@@ -753,18 +765,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
           int at = wrap(head + count + before);  // (head, count <= 128 and before < 512: one wrap at most)
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            uint32_t left = uni[w];
-            while (left) {
-              const int bit = __ffs(left) - 1;
-              left &= left - 1;
-              const uint32_t b0 = __ballot_sync(0xffffffffu, (x[0][w] >> bit) & 1u);
-              const uint32_t b1 = __ballot_sync(0xffffffffu, (x[1][w] >> bit) & 1u);
-              if (lane == 0) {
-                S.qkey[at] = key0 + 32 * w + bit;
-                S.qbits[at] = make_uint2(b0, b1);
-              }
-              at = wrap(at + 1);
+            if (!uni[w]) continue;
+            const uint32_t b0 = transpose32(x[0][w], lane), b1 = transpose32(x[1][w], lane);
+            if ((uni[w] >> lane) & 1u) {  // this lane's key
+              const int to = wrap(at + __popc(uni[w] & ((1u << lane) - 1u)));
+              S.qkey[to] = key0 + 32 * w + lane;
+              S.qbits[to] = make_uint2(b0, b1);
             }
+            at = wrap(at + __popc(uni[w]));
           }
           count += all;
           named_sync(kBarLoad, kTrLoad);
@@ -957,20 +965,26 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         sync();
         const int row = sc >> 2;  // four threads a row, 32 keys each
         float sum = 0.f;
-#pragma unroll 4
+#pragma unroll 16
         for (int i = 0; i < 32; ++i)
           sum += scratch[((row >> 1) * kTrKeys + 32 * (sc & 3) + ((i + lane) & 31)) * 2 + (row & 1)];
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         const bool mine = (sc & 3) == 0, seen_row = (S.seen[x][row >> 5] >> (row & 31)) & 1u;
-        // log2 of a row's sum (infinite if that has left its range, or is a NaN: all that it meets becomes a NaN)
+        // the row's scale: its reference plus the exponent of its sum (infinite if the sum has left its range or is a
+        // NaN: all that it meets becomes a NaN)
         const bool fits = sum >= kTrLow && sum <= kTrTop;
-        const float lse = !seen_row ? kTrNone : fits ? log2f(sum) - S.nref[x][row] : INFINITY;
-        float whole_lse = lse;
+        const float ref = -S.nref[x][row];
+        const float lse = !seen_row ? kTrNone : fits ? ref + (float)((int)(__float_as_uint(sum) >> 23) - 127) : INFINITY;
+        float m = lse, all = sum;  // the piece: 2^m all
         if constexpr (kSplitRows) {
+          all = !seen_row ? 0.f : fits ? sum * ex2a(ref - m) : INFINITY;
           if (mine) alpha[row] = !seen_row ? 0.f : fits ? 1.f / sum : __int_as_float(0x7fffffff);
-        } else {  // the other stream's
-          if (mine) alpha[row] = lse;
+        } else {  // with the other stream's
+          if (mine) {
+            alpha[row] = lse;
+            S.sum[x][row] = sum;
+          }
           if (sc == 0) S.state[x] = (has ? 1 : 0) + (has_total ? 2 : 0);
           tc_fence_before();
           arrive_warp(&S.sum_full[x]);
@@ -978,42 +992,47 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
           wait_warp(&S.sum_full[x ^ 1], (uint32_t)seg);
           tc_fence_after();
           if (mine) {
-            const float a = S.alpha[0][row], b = S.alpha[1][row], m = fmaxf(a, b);
-            const float both = ex2a(a - m) + ex2a(b - m), inv = 1.f / both;
-            S.wt[x][0][row] = a <= kTrNone ? 0.f : ex2a(-S.nref[0][row] - m) * inv;
-            S.wt[x][1][row] = b <= kTrNone ? 0.f : ex2a(-S.nref[1][row] - m) * inv;
-            whole_lse = m <= kTrNone || m == INFINITY ? m : m + log2f(both);
+            const float a = S.alpha[0][row], b = S.alpha[1][row];
+            m = fmaxf(a, b);
+            const float fa = a <= kTrNone ? 0.f : ex2a(-S.nref[0][row] - m);
+            const float fb = b <= kTrNone ? 0.f : ex2a(-S.nref[1][row] - m);
+            all = S.sum[0][row] * fa + S.sum[1][row] * fb;
+            const float inv = m <= kTrNone ? 0.f : 1.f / all;
+            S.wt[x][0][row] = fa * inv;
+            S.wt[x][1][row] = fb * inv;
           }
         }
         if (!alive) break;
         if (info.slot >= 0 && mine && row < srows && (kSplitRows || x == 0))
-          W.lse[(int64_t)info.slot * NR + row_base - row0 + row] = whole_lse;
+          W.ml[(int64_t)info.slot * NR + row_base - row0 + row] = make_float2(m, all);
         sync();
         // eight rows at a time: all 32 of this thread's, or 16 when the streams share them
         const int c_first = kSplitRows ? col0 : col0 + 16 * x;
 #pragma unroll 1
         for (int c0 = c_first; c0 < c_first + (kSplitRows ? 32 : 16) && c0 < srows; c0 += 8) {
-          float y[8];
+          float y[8], e[kSplitRows ? 1 : 2][3][8];  // of each stream: the epoch's O (hi, lo), the total
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = 0.f;
-#pragma unroll 1
-          for (int src = kSplitRows ? x : 0; src < (kSplitRows ? x + 1 : 2); ++src) {
-            const int state = kSplitRows ? 1 + (has_total ? 2 : 0) : S.state[src];
-            if (!(state & 1)) continue;
+          for (int k = 0; k < (kSplitRows ? 1 : 2); ++k) {
+            const int src = kSplitRows ? x : k, state = kSplitRows ? 1 + (has_total ? 2 : 0) : S.state[src];
             const uint32_t at = lane_base + (uint32_t)src * kTmemStream + (uint32_t)c0;
-            const float* wt = kSplitRows ? alpha : S.wt[kSplitRows ? 0 : x][src];
-            float e[8], r[8], q[8];
-            tmem_ld8(at + kTmemOe, e);
-            tmem_ld8(at + kTmemOe + kTrStream, r);
-            if (state & 2) tmem_ld8(at + kTmemOt, q);
-            tmem_wait(e);
-            tmem_wait(r);
-            if (state & 2) tmem_wait(q);
+#pragma unroll
+            for (int i = 0; i < 24; ++i) e[k][i / 8][i % 8] = 0.f;
+            if (state & 1) {
+              tmem_ld8(at + kTmemOe, e[k][0]);
+              tmem_ld8(at + kTmemOe + kTrStream, e[k][1]);
+            }
+            if (state & 2) tmem_ld8(at + kTmemOt, e[k][2]);
+          }
+#pragma unroll
+          for (int k = 0; k < (kSplitRows ? 1 : 2); ++k) {
+            const float* wt = kSplitRows ? alpha : S.wt[kSplitRows ? 0 : x][k];
+            tmem_wait(e[k][0]);
+            tmem_wait(e[k][1]);
+            tmem_wait(e[k][2]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              e[i] += r[i];
-              if (state & 2) e[i] += q[i];
-              y[i] = __fmaf_rn(e[i], wt[c0 + i], y[i]);
+              const float sum_e = e[k][0][i] + e[k][1][i] + e[k][2][i];
+              y[i] = k == 0 ? sum_e * wt[c0 + i] : __fmaf_rn(sum_e, wt[c0 + i], y[i]);
             }
           }
 #pragma unroll
@@ -1027,17 +1046,19 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         if (has) arrive_warp(&S.o_free[x]);
         sync();
         // a warp per row: out, or to where the pieces of the group meet
-#pragma unroll 1
+        const int64_t o_seg = info.b * A.o.sb + (int64_t)info.kvh * A.G * A.o.sh;
+        float4* part = reinterpret_cast<float4*>(W.o) + ((int64_t)info.slot * NR + row_base - row0) * 32 + lane;
+#pragma unroll 4
         for (int i = warp & 7; i < (kSplitRows ? 64 : 32); i += 8) {
           const int c = kSplitRows ? i : (i & 15) + 32 * (i >> 4) + 16 * x;  // (the rows whose columns were this stream's)
           if (c >= srows) continue;
           float4 y = reinterpret_cast<const float4*>(scratch)[c * 32 + lane];
-          const int r = row_base + c, h = info.kvh * A.G + r / A.T, t = r % A.T;
           if (info.slot >= 0) {
-            reinterpret_cast<float4*>(W.o)[((int64_t)info.slot * NR + row_base - row0 + c) * 32 + lane] = y;
+            part[c * 32] = y;
           } else {
-            if (__any_sync(0xffffffffu, !finite4(y))) scalar_row(A, info.b, h, t, y);
-            store_row4(A, info.b, h, t, lane, y);
+            const int at = S.row_at[row_base - row0 + c];
+            if (__any_sync(0xffffffffu, !finite4(y))) scalar_row(A, info.b, info.kvh * A.G + (at & 7), at >> 3, y);
+            store4(A, o_seg + (at & 7) * A.o.sh + (at >> 3) * A.o.sn + 4 * lane, y);
           }
         }
         if (srows < kTrStream) {  // P's columns past the last row are zeros again
@@ -1104,7 +1125,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       bool raise = false;
       tc_fence_after();
       if (!has) {
-        // the references: each row's logit of the tile's first key
+        // the references: each row's logit of the tile's first key, as a whole number (so that no factor between
+        // references rounds)
         if (quad == 0) {
 #pragma unroll 1
           for (int hh = 0; hh < act; ++hh) {
@@ -1113,9 +1135,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
             tmem_wait(v);
             if (lane == 0) {
 #pragma unroll
-              for (int c = 0; c < 16; ++c) {
-                const float y = __uint_as_float(v[c]) * A.scale_log2;
-                S.nref[x][col0 + 16 * hh + c] = is_key && fabsf(y) < 1e30f ? -y : 0.f;
+              for (int c = 0; c < 16; c += 4) {
+                float y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  y[i] = -rintf(__uint_as_float(v[c + i]) * A.scale_log2);
+                  y[i] = (fabsf(y[i]) < 1e30f) & is_key ? y[i] : 0.f;
+                }
+                *reinterpret_cast<float4*>(&S.nref[x][col0 + 16 * hh + c]) = make_float4(y[0], y[1], y[2], y[3]);
               }
             }
           }
@@ -1284,12 +1311,13 @@ __global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const __grid_
   const bool join = pieces.y > 1;  // (one piece: its CTA has written the output)
   float m = kTrNone, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  // one more piece (or partial join) of weight 2^s l (an infinite s makes the sum a NaN)
-  auto take = [&](float s, float w, const float4& y, float mn) {
+  // one more piece (or partial join): 2^s w to the sum, 2^s v y to the output (an infinite s makes both NaNs)
+  auto take = [&](float s, float w, float v, const float4& y, float mn) {
     const float f = s <= kTrNone ? 0.f : ex2a(s - mn);
     if (f == 0.f && w == w) return;  // (what it holds may be anything)
     l += f * w;
-    o = make_float4(o.x + f * y.x, o.y + f * y.y, o.z + f * y.z, o.w + f * y.w);
+    const float g = f * v;
+    o = make_float4(o.x + g * y.x, o.y + g * y.y, o.z + g * y.z, o.w + g * y.w);
   };
   if (join) {
     const int c = r % W.nr;
@@ -1297,27 +1325,27 @@ __global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const __grid_
     auto at = [&](int i) { return (slot0 + 2 * (pieces.x + i) + (i == 0)) * W.nr + c; };
     constexpr int kUnroll = 4;
     for (int i = part; i < pieces.y; i += WPR * kUnroll) {
-      float s[kUnroll];
+      float2 s[kUnroll];
       float4 y[kUnroll];
 #pragma unroll
       for (int q = 0; q < kUnroll; ++q) {
         const int p = i + WPR * q;
-        s[q] = kTrNone;
+        s[q] = make_float2(kTrNone, 0.f);
         y[q] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (p < pieces.y) {
-          s[q] = W.lse[at(p)];
+          s[q] = W.ml[at(p)];
           y[q] = reinterpret_cast<const float4*>(W.o + at(p) * kHeadDim)[lane];
         }
       }
       float mn = m;
 #pragma unroll
-      for (int q = 0; q < kUnroll; ++q) mn = fmaxf(mn, s[q]);
+      for (int q = 0; q < kUnroll; ++q) mn = fmaxf(mn, s[q].x);
       const float al = ex2a(m - mn);
       m = mn;
       l *= al;
       o = make_float4(o.x * al, o.y * al, o.z * al, o.w * al);
 #pragma unroll
-      for (int q = 0; q < kUnroll; ++q) take(s[q], 1.f, y[q], mn);
+      for (int q = 0; q < kUnroll; ++q) take(s[q].x, s[q].y, s[q].y, y[q], mn);
     }
   }
   if (WPR > 1) {
@@ -1331,14 +1359,14 @@ __global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const __grid_
     l = 0.f;
     o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < WPR; ++w) take(sml[warp + w].x, sml[warp + w].y, so[warp + w][lane], M);
+    for (int w = 0; w < WPR; ++w) take(sml[warp + w].x, sml[warp + w].y, 1.f, so[warp + w][lane], M);
   }
   if (!join) return;
   const float inv = l != 0.f ? 1.f / l : 0.f;
   o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
   const int b = grp / A.Hk, h = grp % A.Hk * A.G + r / A.T, t = r % A.T;
   if (__any_sync(0xffffffffu, !finite4(o))) scalar_row(A, b, h, t, o);
-  store_row4(A, b, h, t, lane, o);
+  store4(A, b * A.o.sb + h * A.o.sh + t * A.o.sn + 4 * lane, o);
 }
 
 template <int NR, bool SEL>
@@ -1375,7 +1403,7 @@ cudaError_t launch_tree_attn(const TreeAttnArgs& a, cudaStream_t stream) {
   char* ws = static_cast<char*>(a.ws);
   w.table = reinterpret_cast<int2*>(ws);
   w.o = reinterpret_cast<float*>(ws + L.table);
-  w.lse = reinterpret_cast<float*>(ws + L.table + L.o);
+  w.ml = reinterpret_cast<float2*>(ws + L.table + L.o);
   w.nr = L.nr;
   w.rbs = L.rbs;
   w.ranges = L.ranges;
