@@ -1,0 +1,689 @@
+// Parts that the two forms of rtp_tree_attn's kernel share (tree_attn.cu: up to 64 query rows per KV head, and
+// selections; tree_attn_wide.cu: more rows): the work of a CTA, its loaders, the scalar pass.
+#pragma once
+
+#include <math.h>
+
+#include "launch.h"
+#include "tc05.cuh"
+
+namespace rtp {
+
+// Parts of the workspace that the kernels use.  A piece of a group lies in slot 2 range + (1 if it begins the group).
+struct TrParts {
+  int2* table;  // [B * Hk] first range and number of pieces
+  float* o;     // [row block][2 * ranges][nr][128]
+  float2* ml;   // [row block][2 * ranges][nr] m and l, the sum of 2^logit being 2^m l; o is normalised
+  float4* tot;  // [CTA][stream][32][128] totals of the wide form: four dims of a row each
+  int nr, rbs, ranges;
+};
+
+// The wide form (w.nr: 128 or 256 rows per CTA).
+cudaError_t launch_tree_attn_wide(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeAttnArgs& a,
+                                  const TrParts& w, int use_tma, cudaStream_t stream);
+
+// (every file has its own: the kernels are instantiated where they are launched)
+namespace {
+
+constexpr int kTrKeys = 128;                 // keys per tile
+constexpr int kTrStages = 2;                 // K/V ring
+constexpr int kTrHalf = kTrKeys * 128;       // 128 rows x 64 bf16, 128-byte swizzle
+constexpr int kTrTile = 2 * kTrHalf;         // one K or V tile: 32 KB
+constexpr int kTrLoadWarps = 4;
+constexpr float kTrHigh = 1.0995116e12f;     // 2^40: a sum above it raises the row's reference
+constexpr float kTrLow = 8.6736174e-19f;     // 2^-60: a sum below it has lost the row's largest terms
+constexpr float kTrTop = 1.2676506e30f;      // 2^100: a sum above it is past what a factor can scale down
+constexpr float kTrNone = -3.0e38f;          // log2 of an empty sum
+constexpr int kTrRound = 512;                // keys whose selection bits are read at a time
+constexpr int kTrQueue = 640;                // 128 left over + one round
+constexpr int kTrSms = 148;
+constexpr int kTrSoft = 256;                 // threads of a stream
+constexpr int kTrLoad = kTrLoadWarps * 32;
+constexpr int kTrThreads = 2 * kTrSoft + kTrLoad + 128;  // (whole warpgroups; one warp issues the MMAs)
+constexpr int kTrRing = 8;                   // tiles (and segments) described ahead
+// registers per thread of each role; the launch's threads x registers hold them all
+constexpr int kTrLaunchRegs = 80, kTrSoftRegs = 96, kTrLoadRegs = 56, kTrMmaRegs = 40;
+static_assert(2 * kTrSoft * kTrSoftRegs + kTrLoad * kTrLoadRegs + 128 * kTrMmaRegs <= kTrThreads * kTrLaunchRegs,
+              "register split");
+constexpr int kBarLoad = 1;                  // named barrier
+
+// What the softmax needs to know of a segment (a CTA's share of a group's tiles).
+struct TrSegInfo {
+  int b, kvh, n, lo, draft_tiles, max_depth;
+  int slot;   // where its partial result goes, or -1: the whole group
+  int pad;
+};
+
+// ---- small helpers --------------------------------------------------------------
+RTP_DEVICE void cp16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+RTP_DEVICE void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+RTP_DEVICE void cp_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory"); }
+RTP_DEVICE void fence_async() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
+
+template <int N>
+RTP_DEVICE void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
+template <int N>
+RTP_DEVICE void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
+
+// mbar_wait, kept small: the code of a CTA has to stay in the instruction cache, and most of it runs once or twice.
+RTP_DEVICE bool wait_bar(uint64_t* bar, uint32_t parity, bool& alive, const TreeAttnArgs& A) {
+  if (!alive) return false;
+  if (mbar_try(bar, parity)) return true;
+  const long long t0 = clock64();
+#pragma unroll 1
+  while (!mbar_try(bar, parity))
+    if (clock64() - t0 > A.budget) {
+      atomicExch(A.err, kDevErrTimeout);
+      alive = false;
+      break;
+    }
+  return alive;
+}
+
+RTP_DEVICE void prefetch_map(const CUtensorMap* m) {
+  asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+}
+
+// Barrier of n threads that also ORs a predicate.
+RTP_DEVICE bool bar_or(int id, int n, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(r)
+      : "r"((uint32_t)x), "r"(id), "r"(n)
+      : "memory");
+  return r != 0;
+}
+
+// Pairs of floats in one 64-bit word, and packed arithmetic on them.
+RTP_DEVICE uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+RTP_DEVICE void unpack2(uint64_t x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(x)); }
+RTP_DEVICE uint64_t add2u(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+RTP_DEVICE uint64_t sub2u(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("sub.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// (a * s + c.lo, b * s + c.hi), c a pair of floats in one 64-bit word.
+RTP_DEVICE void fma2c(uint32_t a, uint32_t b, uint64_t s, uint64_t c, float& ra, float& rb) {
+  uint64_t x, r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(x) : "r"(a), "r"(b));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(x), "l"(s), "l"(c));
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(ra), "=f"(rb) : "l"(r));
+}
+
+// Column c of every lane reduced over the 32 lanes, left in lane c (31 shuffles).
+template <int O, typename F>
+RTP_DEVICE float reduce_columns(float (&x)[2 * O], int lane, F op) {
+  const bool up = lane & O;
+  float y[O];
+#pragma unroll
+  for (int i = 0; i < O; ++i) {
+    const float keep = up ? x[i + O] : x[i], send = up ? x[i] : x[i + O];
+    y[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, O));
+  }
+  if constexpr (O == 1)
+    return y[0];
+  else
+    return reduce_columns<O / 2>(y, lane, op);
+}
+
+// Bit c of lane k becomes bit k of lane c.
+RTP_DEVICE uint32_t transpose32(uint32_t x, int lane) {
+  uint32_t m = 0x0000ffffu;
+#pragma unroll
+  for (int j = 16; j > 0; j >>= 1) {
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, x, j);
+    x = lane & j ? (x & ~m) | ((y >> j) & m) : (x & m) | ((y & m) << j);
+    m ^= m << (j >> 1);
+  }
+  return x;
+}
+
+// Waits for the loads that fill these registers (naming them keeps their uses behind it).
+RTP_DEVICE void tmem_wait(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
+RTP_DEVICE void tmem_wait(float (&r)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]));
+}
+
+// 32 lanes x 8 consecutive columns.
+RTP_DEVICE void tmem_ld8(uint32_t taddr, float (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+               : "r"(taddr));
+}
+
+// ---- what a sequence's rows attend -------------------------------------------------
+// Committed tokens of sequence b.
+RTP_DEVICE int committed(const TreeAttnArgs& A, int b) {
+  const int n = A.lens ? max(A.lens[b], 0) : A.N;
+  return A.ring ? n : min(n, A.N);
+}
+
+RTP_DEVICE int row_of(const TreeAttnArgs& A, uint32_t p) { return A.ring ? (int)(p % (uint32_t)A.N) : (int)p; }
+
+// Tokens between a draft and the oldest committed key it attends, less the draft's own depth (W > 0).
+RTP_DEVICE int draft_depth(const TreeAttnArgs& A, int b, int t) {
+  return A.W > 0 ? max(__ldg(A.depth + (int64_t)b * A.T + t), 0) : 0;
+}
+RTP_DEVICE int oldest_age(const TreeAttnArgs& A, int depth) { return A.W - 2 - depth; }
+
+RTP_DEVICE bool tree_bit(const TreeAttnArgs& A, int b, int t, int j) {
+  return (__ldg(A.tree + ((int64_t)b * A.T + t) * A.tree_words + (j >> 5)) >> (j & 31)) & 1u;
+}
+
+// Tiles of one KV head of a sequence: its drafts first, then the committed keys from position lo on (with a
+// selection: rounds of kTrRound keys, aligned).
+struct TrSpan {
+  int n, lo, draft_tiles, tiles;
+};
+template <bool SEL>
+RTP_DEVICE TrSpan span_of(const TreeAttnArgs& A, int b) {
+  constexpr uint32_t kStep = SEL ? kTrRound : kTrKeys;
+  TrSpan s;
+  s.n = committed(A, b);
+  s.lo = A.W > 0 ? max(0, s.n - (A.W - 1)) : 0;
+  if (SEL) s.lo = s.lo / kTrRound * kTrRound;
+  s.draft_tiles = (A.T + kTrKeys - 1) / kTrKeys;
+  s.tiles = s.draft_tiles + (int)(((uint32_t)(s.n - s.lo) + kStep - 1) / kStep);
+  return s;
+}
+
+// One segment: the tiles [u0, u1) of a group (b, kvh) that a CTA works on.
+struct TrSeg {
+  int b, kvh;
+  TrSpan span;
+  int u0, u1;
+  int base;  // the line's tile number of the group's tile 0
+};
+
+// Walks the segments of the range [lo, hi) of the line of tiles.
+template <bool SEL>
+struct TrWalk {
+  int pos, hi, base_b;
+  TrSeg s;
+  RTP_DEVICE void start(const TreeAttnArgs& A, int lo, int end, int b, int base) {
+    pos = lo;
+    hi = end;
+    base_b = base;
+    s.b = b;
+    s.span = span_of<SEL>(A, b);
+    s.kvh = (lo - base) / s.span.tiles;
+    fill();
+  }
+  RTP_DEVICE void fill() {
+    s.base = base_b + s.kvh * s.span.tiles;
+    s.u0 = pos - s.base;
+    s.u1 = min(s.span.tiles, hi - s.base);
+  }
+  RTP_DEVICE bool next(const TreeAttnArgs& A) {
+    pos = s.base + s.u1;
+    if (pos >= hi) return false;
+    if (++s.kvh == A.Hk) {
+      base_b += A.Hk * s.span.tiles;
+      s.kvh = 0;
+      s.span = span_of<SEL>(A, ++s.b);
+    }
+    fill();
+    return true;
+  }
+};
+
+// ---- the scalar pass ------------------------------------------------------------------
+// One warp computes one row from the definition.
+__device__ __noinline__ void scalar_row(const TreeAttnArgs& A, int b, int h, int t, float4& out) {
+  const int lane = threadIdx.x & 31, kvh = h / A.G;
+  auto row = [&](const View4& x, int head, int64_t r) {
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(x.data) + b * x.sb +
+                                                         head * x.sh + r * x.sn + 4 * lane));
+    return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+  };
+  const float4 q = row(A.q, h, t);
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto take = [&](const float4 k, const float4 v) {
+    const float s = warp_sum(q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w) * A.scale_log2;
+    const float mn = fmaxf(m, s);
+    const float al = mn == -INFINITY ? 1.f : ex2a(m - mn), p = mn == -INFINITY ? 0.f : ex2a(s - mn);
+    m = mn;
+    l = l * al + p;
+    o = make_float4(o.x * al + p * v.x, o.y * al + p * v.y, o.z * al + p * v.z, o.w * al + p * v.w);
+  };
+  const int n = committed(A, b), depth = draft_depth(A, b, t);
+  const int lo = A.W > 0 ? max(0, n - 1 - oldest_age(A, depth)) : 0;  // (past n when the window holds none)
+  const uint32_t* sel = A.sel ? A.sel + ((int64_t)(b * A.Hq + h) * A.T + t) * A.sel_words : nullptr;
+  if (A.W <= 0 || oldest_age(A, depth) >= 0)
+#pragma unroll 1
+    for (int p = lo; p < n; ++p) {
+      if (sel && !((__ldg(sel + (p >> 5)) >> (p & 31)) & 1u)) continue;
+      const int r = row_of(A, (uint32_t)p);
+      take(row(A.k, kvh, r), row(A.v, kvh, r));
+    }
+#pragma unroll 1
+  for (int j = 0; j < A.T; ++j) {
+    if (!tree_bit(A, b, t, j)) continue;
+    if (A.W > 0 && draft_depth(A, b, j) <= depth - A.W) continue;
+    take(row(A.kn, kvh, j), row(A.vn, kvh, j));
+  }
+  const float inv = l != 0.f ? 1.f / l : 0.f;  // (a NaN stays one)
+  out = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+}
+
+RTP_DEVICE void store4(const TreeAttnArgs& A, int64_t off, const float4& y) {
+  if (A.o_bf16)
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(A.o.data) + off) =
+        make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+  else
+    *reinterpret_cast<float4*>(static_cast<float*>(A.o.data) + off) = y;
+}
+
+RTP_DEVICE bool finite4(const float4& y) {
+  return isfinite(y.x) && isfinite(y.y) && isfinite(y.z) && isfinite(y.w);
+}
+
+// The part of a CTA's shared memory through which its loaders feed it: NR query rows, two stages of K and V,
+// and what the tiles on their way are.
+template <int NR, bool SEL>
+struct TrFeed {
+  static constexpr int kRows = NR;
+  static constexpr int kQueue = SEL ? kTrQueue : 1, kMasks = SEL ? 4 : 1;
+  alignas(1024) uint8_t q[NR * 256];  // blocks of up to 128 rows, each in two 64-column halves
+  alignas(1024) uint8_t k[kTrStages][kTrTile];
+  alignas(1024) uint8_t v[kTrStages][kTrTile];
+  uint64_t k_full[kTrStages], k_empty[kTrStages], v_full[kTrStages], v_empty[kTrStages], q_full, q_free;
+  int row_at[NR];                // each row's draft times 8 plus its head in the group
+  int2 meta[kTrRing];            // per tile: its number in the group; 4 * segment + 2 * (CTA's last) + (segment's last)
+  TrSegInfo seg[kTrRing];
+  int start_b, start_base;       // where this CTA's range begins: sequence, first tile of the sequence
+  int total, per;                // tiles of the whole line, and of a range
+  int cnt[2][kTrLoadWarps];
+  int qkey[kQueue];              // selected keys waiting for a tile (ring)
+  uint2 qbits[kQueue];           // and which rows selected them
+  uint32_t kmask[kMasks][2][SEL ? kTrKeys : 1];  // row bits of a tile's keys
+};
+
+// What a CTA works on: rows [row0, row0 + nrows) of every group, tiles [lo, hi) of the line.
+struct TrPlace {
+  int rb, range, row0, nrows;
+  int lo, hi, per;
+};
+
+template <typename Smem>
+RTP_DEVICE TrPlace tree_place(const Smem& S, const TreeAttnArgs& A, const TrParts& W) {
+  TrPlace p;
+  p.rb = blockIdx.x % W.rbs;
+  p.range = blockIdx.x / W.rbs;
+  p.row0 = p.rb * Smem::kRows;
+  p.nrows = min(Smem::kRows, A.G * A.T - p.row0);
+  return p;
+}
+
+// Before the inputs may be read: barriers and tables of the feed.
+template <typename Smem>
+RTP_DEVICE void tree_feed_init(Smem& S, const TreeAttnArgs& A, const TrPlace& p, const CUtensorMap& kmap,
+                               const CUtensorMap& vmap, int use_tma) {
+  const int tid = threadIdx.x;
+  if (tid == 0) {
+#pragma unroll 1
+    for (int i = 0; i < kTrStages; ++i) {
+      mbar_init(&S.k_full[i], 1);
+      mbar_init(&S.k_empty[i], 1);
+      mbar_init(&S.v_full[i], 1);
+      mbar_init(&S.v_empty[i], 1);
+    }
+    mbar_init(&S.q_full, 1);
+    mbar_init(&S.q_free, 1);
+    mbar_fence_init();
+  }
+  if (tid < Smem::kRows) {
+    const int r = min(p.row0 + tid, A.G * A.T - 1), g = r / A.T;
+    S.row_at[tid] = (r - g * A.T) * 8 + g;
+  }
+  if (use_tma && tid == kTrThreads - 1) {
+    prefetch_map(&kmap);
+    prefetch_map(&vmap);
+  }
+}
+
+// Warp 0: this CTA's range of the line of tiles.
+template <bool SEL, typename Smem>
+RTP_DEVICE void tree_find_range(Smem& S, const TreeAttnArgs& A, const TrParts& W, int range) {
+  const int lane = threadIdx.x & 31;
+  int sum = 0;
+  const int first = lane < A.B ? span_of<SEL>(A, lane).tiles : 0;
+#pragma unroll 1
+  for (int b = lane; b < A.B; b += 32) sum += b == lane ? first : span_of<SEL>(A, b).tiles;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const int total = sum * A.Hk, per = (total + W.ranges - 1) / W.ranges, lo = range * per;
+  if (lane == 0) {
+    S.total = total;
+    S.per = per;
+  }
+  int base = 0;
+#pragma unroll 1
+  for (int b0 = 0; b0 < A.B && lo < total; b0 += 32) {
+    const int b = b0 + lane;
+    const int mine = (b0 == 0 ? first : b < A.B ? span_of<SEL>(A, b).tiles : 0) * A.Hk;
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, base + incl > lo);
+    if (past) {
+      if (lane == __ffs(past) - 1) {
+        S.start_b = b;
+        S.start_base = base + incl - mine;
+      }
+      break;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+}
+
+// The loaders: kTrLoadWarps warps from thread 2 * kTrSoft on.
+template <bool SEL, typename Smem>
+RTP_DEVICE void tree_load(Smem& S, const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeAttnArgs& A,
+                          const TrParts& W, int use_tma, const TrPlace& place) {
+  constexpr int NR = Smem::kRows, kBlock = NR < 128 ? NR : 128;  // query rows; of one block
+  const int lane = threadIdx.x & 31, lt = threadIdx.x - 2 * kTrSoft, lw = lt >> 5;
+  const int row0 = place.row0, nrows = place.nrows, lo = place.lo, hi = place.hi;
+  bool alive = true;
+  const int chunk = lt & 15, r_first = lt >> 4;  // this thread's 16-byte column; rows r_first + 8 i
+  // (8 rows on, the swizzle is the same)
+  const uint32_t slot0 = (uint32_t)r_first * 128u + (uint32_t)(((chunk & 7) ^ r_first) << 4);
+  const uint32_t slot_kv = slot0 + (uint32_t)(chunk >> 3) * (uint32_t)kTrHalf;
+  uint32_t it = 0, k_loads = 0;  // tiles so far; tiles whose K has been sent for
+  int segs = 0;
+  bool q_due = false;
+  // Waits for a free K or V stage; false (for all loaders alike) once any wait gave up.
+  auto stage_free = [&](uint64_t* empty) {
+    const bool ok = wait_bar(&empty[it & 1], ((it >> 1) & 1u) ^ 1u, alive, A);
+    return !bar_or(kBarLoad, kTrLoad, !ok);
+  };
+  // 128 rows of K or V by cp.async: row_at(r, ok) gives the row of tile row r.
+  auto copy_rows = [&](const View4& x, uint8_t* tile, const TrSeg& s, auto&& row_at) {
+    const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(x.data) + s.b * x.sb + s.kvh * x.sh + chunk * 8;
+    const uint32_t dst = smem_addr(tile) + slot_kv;
+#pragma unroll 2
+    for (int i = 0; i < 16; ++i) {
+      bool ok;
+      const int row = row_at(r_first + 8 * i, ok);
+      cp16(dst + 1024u * i, ok ? (const void*)(base + row * x.sn) : A.q.data, ok);
+    }
+    cp_commit();
+  };
+  auto landed = [&](uint64_t* full) {  // (after a cp_wait) every loader's copies are there
+    fence_async();
+    named_sync(kBarLoad, kTrLoad);
+    if (lt == 0) {
+      if (q_due) mbar_arrive(&S.q_full);
+      if (full) mbar_arrive(full);
+    }
+    q_due = false;
+  };
+  auto gather = [&](const View4& xk, const View4& xv, const TrSeg& s, int u, int flags, auto&& row_at) -> bool {
+    const int st = it & 1;
+    bool k_there = false;
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+      // K is handed on before a wait for V's stage, else with V on its way
+      if (i == 1 && bar_or(kBarLoad, kTrLoad, !mbar_try(&S.v_empty[st], ((it >> 1) & 1u) ^ 1u))) {
+        cp_wait<0>();
+        landed(&S.k_full[st]);
+        k_there = true;
+      }
+      if (!stage_free(i ? S.v_empty : S.k_empty)) return false;
+      if (i == 0 && lt == 0) S.meta[it % kTrRing] = make_int2(u, flags);
+      copy_rows(i ? xv : xk, i ? S.v[st] : S.k[st], s, row_at);
+    }
+    if (!k_there) {
+      cp_wait<1>();
+      landed(&S.k_full[st]);
+    }
+    cp_wait<0>();
+    landed(&S.v_full[st]);
+    k_loads = ++it;
+    return true;
+  };
+  TrWalk<SEL> walk;
+  bool more = lo < hi, ok = true;
+  if (more) walk.start(A, lo, hi, S.start_b, S.start_base);
+#pragma unroll 1
+  while (more && ok) {
+    const TrSeg s = walk.s;
+    const int seg_flags = 4 * segs, last_flags = seg_flags + (s.base + s.u1 < hi ? 1 : 3);
+    // ---- the query rows (the previous segment's products are done with the buffer) ----
+    {
+      const bool free = segs == 0 || wait_bar(&S.q_free, (segs - 1) & 1u, alive, A);
+      if (bar_or(kBarLoad, kTrLoad, !free)) break;
+      const __nv_bfloat16* qb =
+          static_cast<const __nv_bfloat16*>(A.q.data) + s.b * A.q.sb + (int64_t)s.kvh * A.G * A.q.sh + chunk * 8;
+#pragma unroll 4
+      for (int i = 0; i < NR / 8; ++i) {
+        const int r = r_first + 8 * i, at = S.row_at[r];
+        cp16(smem_addr(S.q) + (uint32_t)(i / (kBlock / 8)) * (kBlock * 256u) + (uint32_t)(chunk >> 3) * (kBlock * 128u) +
+                 slot0 + 1024u * (i % (kBlock / 8)),
+             qb + (at & 7) * A.q.sh + (at >> 3) * A.q.sn, r < nrows);
+      }
+      cp_commit();
+      q_due = true;
+    }
+    {
+      TrSegInfo info;
+      info.b = s.b;
+      info.kvh = s.kvh;
+      info.n = s.span.n;
+      info.lo = s.span.lo;
+      info.draft_tiles = s.span.draft_tiles;
+      info.max_depth = 0;
+      if (A.W > 0) {
+#pragma unroll 1
+        for (int t = lane; t < A.T; t += 32) info.max_depth = max(info.max_depth, draft_depth(A, s.b, t));
+        info.max_depth = __reduce_max_sync(0xffffffffu, info.max_depth);
+      }
+      const bool whole = s.u0 == 0 && s.u1 == s.span.tiles;
+      info.slot = whole ? -1 : place.rb * 2 * W.ranges + 2 * place.range + (s.u0 == 0 ? 1 : 0);
+      info.pad = 0;
+      if (lt == 0) {
+        S.seg[segs % kTrRing] = info;
+        if (s.u0 == 0 && place.rb == 0)
+          W.table[s.b * A.Hk + s.kvh] = make_int2(place.range, (s.base + s.span.tiles - 1) / place.per - place.range + 1);
+      }
+      ++segs;
+    }
+    const int drafts_end = min(s.u1, s.span.draft_tiles);
+    more = walk.next(A);
+    for (int u = s.u0; u < drafts_end && ok; ++u)
+      ok = gather(A.kn, A.vn, s, u, u + 1 == s.u1 ? last_flags : seg_flags, [&](int r, bool& live) {
+        const int j = u * kTrKeys + r;
+        live = j < A.T;
+        return live ? j : 0;
+      });
+    if (!ok || s.u1 <= s.span.draft_tiles) continue;
+    if constexpr (!SEL) {
+      auto by_tma = [&](int u, uint32_t& p0, int& left, int& first) {  // a whole tile of neighbouring rows
+        p0 = (uint32_t)s.span.lo + (uint32_t)(u - s.span.draft_tiles) * kTrKeys;
+        left = s.span.n - (int)p0;  // committed rows from here on
+        first = row_of(A, p0);
+        return use_tma && left >= kTrKeys && A.N - first >= kTrKeys;
+      };
+      auto load = [&](const CUtensorMap* map, uint8_t* tile, uint64_t* full, int first) {
+        mbar_expect_tx(full, kTrTile);
+        tma_load_4d(tile, map, full, 0, first, s.kvh, s.b);
+        tma_load_4d(tile + kTrHalf, map, full, 64, first, s.kvh, s.b);
+      };
+      bool ahead = false;  // this tile's K is already on its way
+#pragma unroll 1
+      for (int u = max(s.u0, s.span.draft_tiles); u < s.u1 && ok; ++u) {
+        uint32_t p0;
+        int left, first;
+        const int st = it & 1;
+        if (by_tma(u, p0, left, first)) {
+          // the next tile's K before this one's V: scores are computed ahead of the products with V
+#pragma unroll 1
+          for (int i = ahead ? 1 : 0; i < 2 && ok; ++i) {
+            uint32_t q0;
+            int rest, at;
+            if (u + i == s.u1 || !by_tma(u + i, q0, rest, at)) {
+              ahead = false;
+              break;
+            }
+            it += i;
+            ok = stage_free(S.k_empty);
+            it -= i;
+            if (lt == 0 && ok) {
+              S.meta[(it + i) % kTrRing] = make_int2(u + i, u + i + 1 == s.u1 ? last_flags : seg_flags);
+              load(&kmap, S.k[st ^ i], &S.k_full[st ^ i], at);
+              k_loads = it + i + 1;
+            }
+            ahead = i;
+            if (q_due) {
+              cp_wait<0>();
+              landed(nullptr);
+            }
+          }
+          if (!ok || !(ok = stage_free(S.v_empty))) break;
+          if (lt == 0) load(&vmap, S.v[st], &S.v_full[st], first);
+          ++it;
+        } else {
+          ok = gather(A.k, A.v, s, u, u + 1 == s.u1 ? last_flags : seg_flags, [&](int r, bool& live) {
+            live = r < left;
+            return live ? row_of(A, p0 + (uint32_t)r) : 0;
+          });
+        }
+      }
+    } else {
+      const int rounds = s.span.tiles - s.span.draft_tiles;
+      int head = 0, count = 0, turn = 0;
+      auto wrap = [](int i) { return i >= kTrQueue ? i - kTrQueue : i; };
+      // this lane's rows: their mask rows, and the first key position their window admits
+      const uint32_t* words[2];
+      int from[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = lane + 32 * i;
+        words[i] = nullptr;
+        from[i] = 0;
+        if (r < nrows) {
+          words[i] = A.sel + ((int64_t)(s.b * A.Hq + s.kvh * A.G) * A.T + row0 + r) * A.sel_words;
+          if (A.W > 0) {
+            const int age = oldest_age(A, draft_depth(A, s.b, (row0 + r) % A.T));
+            from[i] = age < 0 ? s.span.n : s.span.n - 1 - age;
+          }
+        }
+      }
+      // a round's mask words, on their way while the round before is worked on; neighbouring ranges take rounds
+      // from all over the context (a prime larger than their number), since selected keys come in clusters
+      uint32_t ahead[2][4];
+      int next_key = 0;
+      auto fetch = [&](int u) {
+        const int i0 = u - s.span.draft_tiles;
+        const int round = (int)((uint64_t)i0 * 2654435761ull % (uint64_t)rounds);
+        next_key = s.span.lo + round * kTrRound + lw * 128;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const int wb = next_key + 32 * w, rem = s.span.n - wb;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) ahead[i][w] = words[i] && rem > 0 ? __ldg(words[i] + (wb >> 5)) : 0u;
+        }
+      };
+      fetch(max(s.u0, s.span.draft_tiles));
+      auto emit = [&](int take, int flags) {
+        // one key per loader thread: its row bits for the softmax
+        uint2 bits = make_uint2(0u, 0u);
+        if (lt < take) bits = S.qbits[wrap(head + lt)];
+        S.kmask[it & 3][0][lt] = bits.x;
+        S.kmask[it & 3][1][lt] = bits.y;
+        const int at = head;
+        ok = gather(A.k, A.v, s, s.span.draft_tiles, flags, [&](int r, bool& live) {
+          live = r < take;
+          return live ? S.qkey[wrap(at + r)] : 0;
+        });
+        head = wrap(head + take);
+        count -= take;
+      };
+      for (int u = max(s.u0, s.span.draft_tiles); u < s.u1 && ok; ++u) {
+        uint32_t x[2][4], uni[4];
+        const int key0 = next_key;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          x[0][w] = ahead[0][w];
+          x[1][w] = ahead[1][w];
+        }
+        if (u + 1 < s.u1) fetch(u + 1);
+        int mine = 0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const int wb = key0 + 32 * w, rem = s.span.n - wb;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (rem < 32) x[i][w] &= rem > 0 ? (1u << rem) - 1u : 0u;
+            const int cut = from[i] - wb;
+            if (cut > 0) x[i][w] &= cut < 32 ? ~0u << cut : 0u;
+          }
+          uni[w] = __reduce_or_sync(0xffffffffu, x[0][w] | x[1][w]);
+          mine += __popc(uni[w]);
+        }
+        if (lane == 0) S.cnt[turn & 1][lw] = mine;
+        named_sync(kBarLoad, kTrLoad);
+        int before = 0, all = 0;
+#pragma unroll
+        for (int w = 0; w < kTrLoadWarps; ++w) {
+          const int c = S.cnt[turn & 1][w];
+          before += w < lw ? c : 0;
+          all += c;
+        }
+        ++turn;
+        int at = wrap(head + count + before);  // (head, count <= 128 and before < 512: one wrap at most)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          if (!uni[w]) continue;
+          const uint32_t b0 = transpose32(x[0][w], lane), b1 = transpose32(x[1][w], lane);
+          if ((uni[w] >> lane) & 1u) {  // this lane's key
+            const int to = wrap(at + __popc(uni[w] & ((1u << lane) - 1u)));
+            S.qkey[to] = key0 + 32 * w + lane;
+            S.qbits[to] = make_uint2(b0, b1);
+          }
+          at = wrap(at + __popc(uni[w]));
+        }
+        count += all;
+        named_sync(kBarLoad, kTrLoad);
+        while (count > kTrKeys && ok) emit(kTrKeys, seg_flags);
+      }
+      if (ok) emit(count, last_flags);
+    }
+  }
+  cp_wait<0>();
+  if (lt == 0)  // copies still in flight land before the CTA ends
+    {
+    for (uint32_t i = k_loads > 2 ? k_loads - 2 : 0; i < k_loads; ++i) mbar_drain(&S.k_full[i & 1], (i >> 1) & 1u, A.err);
+    for (uint32_t i = it > 2 ? it - 2 : 0; i < it; ++i) mbar_drain(&S.v_full[i & 1], (i >> 1) & 1u, A.err);
+    }
+}
+
+}  // namespace
+
+}  // namespace rtp

@@ -1,0 +1,548 @@
+// rtp_tree_attn for more than 64 query rows (G heads x T drafts) per KV head.
+//
+// Here there are rows enough to fill the tensor core's 128 lanes, and they go
+// there: S = Q K^T and O = P V with the rows on M, P as a bf16 hi + lo pair read
+// from TMEM (over S, in place).  Against the form with the keys on M
+// (tree_attn.cu) this halves the traffic of the shared memory, which bound that
+// form at 128 rows (P never goes there), and a thread holds 64 logits of ONE row:
+// one reference, one sum, half the instructions per logit.
+//
+// Two streams of 8 softmax warps (two threads per row) alternate on the tensor
+// core: with more than 128 rows each has 128 rows of its own of every tile, so
+// that the keys of 256 rows are read once; else they take tiles in turn and meet
+// at a segment's end.  References are as in tree_attn.cu: not the running
+// maximum but the logit of the first tile's first key, raised where a sum has
+// grown past 2^40 (looked at every 8 tiles), the scalar pass for what falls
+// outside its range.
+//
+// O stays in TMEM for up to 32 tiles (512 products, each truncated: 2^-15 of a
+// value at the very worst), then joins an fp32 total in the workspace, which the
+// L2 cache keeps (there is no room left in TMEM or registers: 1.5% of the time).
+//
+// Bound: the tensor cores (P V counts twice) above about 100 rows; 128 drafted
+// rows and a tile of 128 keys are 512 + 1024 cycles of the tensor pipe.
+#include "tree_attn.cuh"
+
+namespace rtp {
+
+namespace {
+
+constexpr int kWideRows = 128;   // rows of a block: TMEM lanes
+constexpr int kWideEpoch = 32;   // tiles summed in TMEM before an fp32 add
+constexpr int kWideCheck = 8;    // tiles between looks at the sums
+constexpr int kWideQBlock = kWideRows * 256;
+constexpr uint32_t kTmemStreamW = 256, kTmemO = 128, kTmemColsW = 512;  // of a stream: S / P, then O
+
+template <int kBlocks>
+struct TrWideSmem : TrFeed<kWideRows * kBlocks, false> {
+  float part[2][2][kWideRows];   // [stream][half]: a row's sums over its two threads' keys (-1: attends none of them)
+  float ref[2][kWideRows];       // references, from a row's first thread to its second; at a segment's end all of them
+  float sum[2][kWideRows], scale[2][kWideRows];  // at a segment's end
+  uint64_t s_full[2], p_full[2], p_free[2], o_free[2], sum_full[2], sum_free[2], sync[2], fin;
+  int4 cur[2];                   // each stream's scores: tile (-1: no more), and its meta
+  int new_epoch[2];
+  int raise[2][2];               // some sum has grown too large (alternating looks)
+  uint32_t bad[2][kWideRows / 32];  // rows with a result that is not finite
+  int state[2];                  // at a segment's end: 1 the stream has an O, 2 and a total
+  uint32_t tmem_base;
+};
+
+template <int kBlocks>
+__global__ void __launch_bounds__(kTrThreads, 1)
+tree_attn_wide_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                      const __grid_constant__ TreeAttnArgs A, const __grid_constant__ TrParts W, int use_tma) {
+  using Smem = TrWideSmem<kBlocks>;
+  constexpr bool kShared = kBlocks == 1;  // the streams share the rows and take tiles in turn
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  Smem& S = *reinterpret_cast<Smem*>(smem_raw);
+  if (smem_addr(smem_raw) % 1024u) {  // (the swizzle and the descriptors rest on the alignment declared above)
+    if (threadIdx.x == 0) atomicExch(A.err, kDevErrTimeout);
+    return;
+  }
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  TrPlace place = tree_place(S, A, W);
+
+  if (tid == 0) {
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&S.s_full[i], 2);  // the products' commit, and the issuer (for S.cur)
+      mbar_init(&S.p_full[i], 8);
+      mbar_init(&S.p_free[i], 1);
+      mbar_init(&S.o_free[i], 8);
+      mbar_init(&S.sum_full[i], 8);
+      mbar_init(&S.sum_free[i], 8);
+      mbar_init(&S.sync[i], 8);
+      S.raise[i][0] = S.raise[i][1] = 0;
+    }
+    mbar_init(&S.fin, 1);
+  }
+  if (tid < 2 * kWideRows / 32) S.bad[0][tid] = 0u;
+  tree_feed_init(S, A, place, kmap, vmap, use_tma);
+  if (warp == 0) tmem_alloc(&S.tmem_base, kTmemColsW);
+  pdl_wait();
+  pdl_release();
+
+  if (warp == 0) tree_find_range<false>(S, A, W, place.range);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = S.tmem_base;
+  place.per = S.per;
+  place.lo = place.range * S.per;
+  place.hi = min(place.lo + S.per, S.total);
+  const bool work = place.lo < place.hi;
+
+  bool alive = true;
+
+  if (warp >= 2 * kTrSoft / 32 && warp < 2 * kTrSoft / 32 + kTrLoadWarps) {
+    // ---------------- loaders ----------------
+    regs_dec<kTrLoadRegs>();
+    tree_load<false>(S, kmap, vmap, A, W, use_tma, place);
+  } else if (warp >= 2 * kTrSoft / 32 + kTrLoadWarps) {
+    // ---------------- MMA issuer (one elected lane) ----------------
+    regs_dec<kTrMmaRegs>();
+    if (warp == 2 * kTrSoft / 32 + kTrLoadWarps && lane == 0 && work) {
+      constexpr uint32_t idesc_s = umma_idesc_bf16_f32(kWideRows, kTrKeys);
+      constexpr uint32_t idesc_o = umma_idesc_bf16_f32(kWideRows, kHeadDim) | (1u << 16);  // V is MN-major
+      auto ready = [&](uint64_t* bar, uint32_t parity) { return mbar_test(bar, parity & 1u); };
+      // Op o: the scores, later the product with V, of stream o % 2 and its tile.  Each of these returns false,
+      // having done nothing, while something it needs is missing.
+      auto tile_of = [](uint32_t o) { return kShared ? o : o >> 1; };
+      auto tile_done = [](uint32_t o) { return kShared || (o & 1u); };  // no later op of the other stream needs it
+      bool seg_start = true, end = false;
+      uint32_t segs = 0, epochs[2] = {0u, 0u};
+      int end_seg = 0;
+      auto issue_s = [&](uint32_t o) -> bool {
+        const uint32_t tile = tile_of(o), st = tile & 1, x = o & 1;
+        if (!ready(&S.p_free[x], (o >> 1) ^ 1u)) return false;  // the product before has read P, where S goes
+        if ((kShared || x == 0) && !ready(&S.k_full[st], tile >> 1)) return false;
+        if (seg_start) {
+          if (!ready(&S.q_full, segs)) return false;
+          ++segs;
+          seg_start = false;
+        }
+        tc_fence_after();
+        const uint32_t ka = smem_addr(S.k[st]), qa = smem_addr(S.q) + (kShared ? 0u : x * kWideQBlock);
+#pragma unroll
+        for (int kk = 0; kk < kHeadDim / 16; ++kk) {
+          const uint32_t off = (uint32_t)(kk >> 2) * kTrHalf + 32u * (uint32_t)(kk & 3);
+          umma_f16(tmem + x * kTmemStreamW, umma_desc_sw128(qa + off, 16), umma_desc_sw128(ka + off, 16), idesc_s,
+                   kk > 0 ? 1u : 0u);
+        }
+        umma_commit(&S.s_full[x]);
+        const int2 meta = S.meta[tile % kTrRing];
+        S.cur[x] = make_int4((int)tile, meta.x, meta.y, 0);
+        mbar_arrive(&S.s_full[x]);
+        if (tile_done(o)) {
+          umma_commit(&S.k_empty[st]);
+          if (meta.y & 1) {
+            umma_commit(&S.q_free);
+            seg_start = true;
+          }
+          if (meta.y & 2) {
+            end = true;
+            end_seg = (meta.y >> 2) + 1;
+          }
+        }
+        return true;
+      };
+      auto issue_pv = [&](uint32_t o) -> bool {
+        const uint32_t tile = tile_of(o), st = tile & 1, x = o & 1;
+        if (!ready(&S.p_full[x], o >> 1) || !ready(&S.v_full[st], tile >> 1)) return false;
+        const bool fresh = S.new_epoch[x] != 0;
+        uint32_t& ep = x ? epochs[1] : epochs[0];
+        if (fresh) {
+          if (ep > 0 && !ready(&S.o_free[x], ep - 1)) return false;
+          ++ep;
+        }
+        tc_fence_after();
+        const uint32_t va = smem_addr(S.v[st]), pa = tmem + x * kTmemStreamW;
+#pragma unroll
+        for (int kk = 0; kk < kTrKeys / 16; ++kk) {
+          const uint64_t b = umma_desc_sw128(va + (uint32_t)kk * 2048u, kTrHalf);
+          umma_f16_tmem_a(pa + kTmemO, pa + 16u * kk, b, idesc_o, fresh && kk == 0 ? 0u : 1u);
+          umma_f16_tmem_a(pa + kTmemO, pa + 16u * kk + 8u, b, idesc_o, 1u);
+        }
+        umma_commit(&S.p_free[x]);
+        if (tile_done(o)) umma_commit(&S.v_empty[st]);
+        return true;
+      };
+      // After the last op one more for each stream, that tells it so: the other may be waiting for its sums.
+      auto issue_end = [&](uint32_t o) {
+        const uint32_t x = o & 1;
+        umma_commit(&S.s_full[x]);  // (the stream's last product is done, too)
+        S.cur[x] = make_int4(-1, 0, 4 * end_seg, 0);
+        mbar_arrive(&S.s_full[x]);
+      };
+      // Whichever is ready, in each line's order: a stream's scores follow its product before.
+      uint32_t so = 0, po = 0, ops = 0;  // (two more score ops than ops: the ends)
+      long long since = clock64();
+#pragma unroll 1
+      while (!end || po < ops || so < ops + 2) {
+        bool moved = false;
+        if (so < po + 2) {
+          if (!end) {
+            if (issue_s(so)) {
+              moved = true;
+              if (end) ops = so + 1;
+              ++so;
+            }
+          } else if (so < ops + 2) {
+            issue_end(so++);
+            moved = true;
+          }
+        }
+        if (po < so && (!end || po < ops) && issue_pv(po)) {
+          moved = true;
+          ++po;
+        }
+        if (end && po == ops && so < ops + 2) {  // (the ends need no product after them)
+          issue_end(so++);
+          moved = true;
+        }
+        const long long now = clock64();
+        if (moved) {
+          since = now;
+        } else if (now - since > A.budget) {
+          atomicExch(A.err, kDevErrTimeout);
+          break;
+        }
+      }
+      umma_commit(&S.fin);  // every product issued is done before TMEM is freed
+      mbar_drain(&S.fin, 0, A.err);
+    }
+  } else {
+    // ---------------- softmax, output: two threads per row, 64 keys (then 64 dims) each ----------------
+    regs_inc<kTrSoftRegs>();
+    const int x = tid / kTrSoft, sc = tid % kTrSoft;              // stream, thread of it
+    const int quad = warp & 3, half = (warp >> 2) & 1, row = 32 * quad + lane;
+    const int base_row = kShared ? 0 : kWideRows * x;             // of the CTA's rows
+    const int nrows = max(0, min(kWideRows, place.nrows - base_row));
+    const bool act = 32 * quad < nrows, live = row < nrows;       // the warp, the thread has a row
+    const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
+    const uint32_t s_cols = lane_base + (uint32_t)x * kTmemStreamW + 64u * half;
+    const int at = S.row_at[base_row + row], t = at >> 3;
+    float4* const tot = W.tot + ((int64_t)blockIdx.x * 2 * 32 + 16 * half) * kWideRows + row;  // (stream 0's)
+    uint64_t scale2;
+    asm("mov.b64 %0, {%1, %1};\n" : "=l"(scale2) : "f"(A.scale_log2));
+    auto wait_warp = [&](uint64_t* b, uint32_t parity) {
+      if (!__all_sync(0xffffffffu, wait_bar(b, parity & 1u, alive, A))) alive = false;
+    };
+    auto arrive_warp = [&](uint64_t* b) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b);
+    };
+    // The stream's barrier (bounded, as every wait here).
+    uint32_t syncs = 0;
+    auto sync = [&]() {
+      arrive_warp(&S.sync[x]);
+      wait_warp(&S.sync[x], syncs++);
+    };
+
+    float ref = 0.f;        // the row's reference (log2 units, a whole number)
+    uint64_t l2 = 0ull;     // the row's sum over this thread's keys, in two parts
+    bool seen = false;      // the row attends some of them
+    int seg = 0;            // current segment
+    int seg_b = 0, seg_n = 0, seg_lo = 0, seg_drafts = 0, seg_depth = 0, oldest = 0;  // what its masks need
+    bool has = false, has_total = false;  // the stream has taken a tile of it; its epochs have a total
+    int in_epoch = 0;
+    uint32_t n = 0, looks = 0;            // ops of this stream so far; looks at the sums
+#pragma unroll 1
+    while (work) {
+      wait_warp(&S.s_full[x], n);  // (the scores, and the stream's product before)
+      if (!alive) break;
+      const int4 cur = S.cur[x];
+      const bool turn = n == 0 || seg < (cur.z >> 2);
+      tc_fence_after();
+
+      // ---- segments that ended before this tile: the row sums of both threads, then O ----
+#pragma unroll 1
+      for (; seg < (cur.z >> 2); ++seg) {
+        const TrSegInfo& info = S.seg[seg % kTrRing];
+        {
+          float a, b;
+          unpack2(l2, a, b);
+          S.part[x][half][row] = seen ? a + b : -1.f;
+        }
+        sync();
+        const float p0 = S.part[x][0][row], p1 = S.part[x][1][row];
+        const bool seen_row = p0 != -1.f || p1 != -1.f;
+        float sum = (p0 == -1.f ? 0.f : p0) + (p1 == -1.f ? 0.f : p1);
+        // the row's scale: its reference plus the exponent of its sum (infinite if the sum has left its range or is a
+        // NaN: all that it meets becomes a NaN)
+        const bool fits = sum >= kTrLow && sum <= kTrTop;
+        float m = !seen_row ? kTrNone : fits ? ref + (float)((int)(__float_as_uint(sum) >> 23) - 127) : INFINITY;
+        float w[2], all;  // factors of the streams' O (here w[0]: this one's); the piece's sum is 2^m all
+        if constexpr (!kShared) {
+          all = !seen_row ? 0.f : fits ? sum * ex2a(ref - m) : INFINITY;
+          w[0] = !seen_row ? 0.f : fits ? 1.f / sum : __int_as_float(0x7fffffff);
+          w[1] = 0.f;
+        } else {
+          if (half == 0) {
+            S.ref[x][row] = ref;
+            S.sum[x][row] = sum;
+            S.scale[x][row] = m;
+          }
+          if (sc == 0) S.state[x] = (has ? 1 : 0) + (has_total ? 2 : 0);
+          tc_fence_before();
+          arrive_warp(&S.sum_full[x]);
+          wait_warp(&S.sum_full[x], (uint32_t)seg);
+          wait_warp(&S.sum_full[x ^ 1], (uint32_t)seg);
+          tc_fence_after();
+          const float a = S.scale[0][row], b = S.scale[1][row];
+          m = fmaxf(a, b);
+          const float fa = a <= kTrNone ? 0.f : ex2a(S.ref[0][row] - m);
+          const float fb = b <= kTrNone ? 0.f : ex2a(S.ref[1][row] - m);
+          all = S.sum[0][row] * fa + S.sum[1][row] * fb;
+          const float inv = m <= kTrNone ? 0.f : 1.f / all;
+          w[0] = fa * inv;
+          w[1] = fb * inv;
+        }
+        if (!alive) break;
+        const int64_t slot_row = (int64_t)info.slot * Smem::kRows + base_row + row;
+        if (info.slot >= 0 && live && half == 0 && (!kShared || x == 0)) W.ml[slot_row] = make_float2(m, all);
+        // 16 dims at a time: the thread's 64, or 32 of them when the streams share the rows
+        const int64_t off = info.b * A.o.sb + (int64_t)(info.kvh * A.G + (at & 7)) * A.o.sh + t * A.o.sn;
+        bool bad = false;
+#pragma unroll 1
+        for (int i = 0; i < (kShared ? 2 : 4) && act; ++i) {
+          const int d0 = kShared ? 32 * x + 16 * i : 16 * i;  // past 64 * half
+          float y[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) y[c] = 0.f;
+#pragma unroll 1
+          for (int k = 0; k < (kShared ? 2 : 1); ++k) {
+            const int src = kShared ? k : x, state = kShared ? S.state[k] : 1 + (has_total ? 2 : 0);
+            if (!(state & 1)) continue;
+            const float f = kShared && k == 1 ? w[1] : w[0];
+            uint32_t e[16];
+            tmem_ld16(lane_base + (uint32_t)src * kTmemStreamW + kTmemO + 64u * half + (uint32_t)d0, e);
+            float4 q[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              q[c] = state & 2 ? __ldcg(tot + (32 * src + d0 / 4 + c) * kWideRows) : make_float4(0.f, 0.f, 0.f, 0.f);
+            tmem_wait(e);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              y[4 * c] = __fmaf_rn(__uint_as_float(e[4 * c]) + q[c].x, f, y[4 * c]);
+              y[4 * c + 1] = __fmaf_rn(__uint_as_float(e[4 * c + 1]) + q[c].y, f, y[4 * c + 1]);
+              y[4 * c + 2] = __fmaf_rn(__uint_as_float(e[4 * c + 2]) + q[c].z, f, y[4 * c + 2]);
+              y[4 * c + 3] = __fmaf_rn(__uint_as_float(e[4 * c + 3]) + q[c].w, f, y[4 * c + 3]);
+            }
+          }
+          if (!live) continue;
+          const int d = 64 * half + d0;
+          if (info.slot >= 0) {
+            float4* dst = reinterpret_cast<float4*>(W.o + slot_row * kHeadDim + d);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) dst[c] = make_float4(y[4 * c], y[4 * c + 1], y[4 * c + 2], y[4 * c + 3]);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) bad = bad | !isfinite(y[c]);
+            if (A.o_bf16) {
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(A.o.data) + off + d);
+#pragma unroll
+              for (int c = 0; c < 16; c += 8)
+                dst[c / 8] = make_uint4(pack_bf16x2(y[c], y[c + 1]), pack_bf16x2(y[c + 2], y[c + 3]),
+                                        pack_bf16x2(y[c + 4], y[c + 5]), pack_bf16x2(y[c + 6], y[c + 7]));
+            } else {
+              float4* dst = reinterpret_cast<float4*>(static_cast<float*>(A.o.data) + off + d);
+#pragma unroll
+              for (int c = 0; c < 4; ++c) dst[c] = make_float4(y[4 * c], y[4 * c + 1], y[4 * c + 2], y[4 * c + 3]);
+            }
+          }
+        }
+        tc_fence_before();
+        if constexpr (kShared) {  // both streams are done with each other's sums and O
+          arrive_warp(&S.sum_free[x ^ 1]);
+          wait_warp(&S.sum_free[x], (uint32_t)seg);
+        }
+        if (has) arrive_warp(&S.o_free[x]);
+        {
+          const uint32_t rows_bad = __ballot_sync(0xffffffffu, bad);
+          if (lane == 0 && rows_bad) atomicOr(&S.bad[x][quad], rows_bad);
+        }
+        sync();
+        if (S.bad[x][0] | S.bad[x][1] | S.bad[x][2] | S.bad[x][3]) {
+#pragma unroll 1
+          for (int r = warp & 7; r < nrows; r += 8)
+            if ((S.bad[x][r >> 5] >> (r & 31)) & 1u) {
+              const int ra = S.row_at[base_row + r], h = info.kvh * A.G + (ra & 7);
+              float4 y;
+              scalar_row(A, info.b, h, ra >> 3, y);
+              store4(A, info.b * A.o.sb + h * A.o.sh + (ra >> 3) * A.o.sn + 4 * lane, y);
+            }
+          sync();
+          if (sc < kWideRows / 32) S.bad[x][sc] = 0u;
+          sync();
+        }
+        l2 = 0ull;
+        seen = has = has_total = false;
+      }
+      if (cur.x < 0 || !alive) break;
+      if (turn) {
+        const TrSegInfo& info = S.seg[seg % kTrRing];
+        seg_b = info.b;
+        seg_n = info.n;
+        seg_lo = info.lo;
+        seg_drafts = info.draft_tiles;
+        seg_depth = info.max_depth;
+        oldest = oldest_age(A, draft_depth(A, seg_b, t));
+      }
+
+      // ---- which of this thread's keys the row attends ----
+      uint64_t mw = ~0ull;
+      if (cur.y < seg_drafts) {
+        const int j0 = cur.y * kTrKeys + 64 * half, w0 = 4 * cur.y + 2 * half;
+        const uint32_t* words = A.tree + ((int64_t)seg_b * A.T + t) * A.tree_words + w0;
+        const uint32_t lo = j0 < A.T ? __ldg(words) : 0u, hi = j0 + 32 < A.T ? __ldg(words + 1) : 0u;
+        mw = (uint64_t)hi << 32 | lo;
+        const int left = A.T - j0;
+        if (left < 64) mw &= left > 0 ? (1ull << left) - 1ull : 0ull;
+        if (A.W > 0 && seg_depth >= A.W) {
+          const int depth = draft_depth(A, seg_b, t);
+#pragma unroll 1
+          for (int j = 0; j < 64 && j < left; ++j)
+            if (draft_depth(A, seg_b, j0 + j) <= depth - A.W) mw &= ~(1ull << j);
+        }
+      } else {
+        const uint32_t p0 = (uint32_t)seg_lo + (uint32_t)(cur.y - seg_drafts) * kTrKeys + 64u * half;
+        const int left = seg_n - (int)p0;
+        if (left < 64) mw = left > 0 ? (1ull << left) - 1ull : 0ull;
+        if (A.W > 0) {  // key i of the half is left - 1 - i tokens older than the newest
+          const int cut = oldest < 0 ? 64 : max(left - 1 - oldest, 0);
+          mw &= cut < 64 ? ~0ull << cut : 0ull;
+        }
+      }
+      if (!live) mw = 0ull;
+      seen = seen | (mw != 0ull);
+
+      bool raise = false;
+      float alpha = 1.f;
+      if (!has) {
+        // the reference: the row's logit of the tile's first key, as a whole number (so that no factor between
+        // references rounds)
+        if (half == 0 && act) {
+          uint32_t v[16];
+          tmem_ld16(s_cols, v);
+          tmem_wait(v);
+          const float y = rintf(__uint_as_float(v[0]) * A.scale_log2);
+          S.ref[x][row] = fabsf(y) < 1e30f ? y : 0.f;
+        }
+        sync();
+        ref = act ? S.ref[x][row] : 0.f;
+      } else if (in_epoch % kWideCheck == 0) {
+        // raise the references of rows whose sums have grown large, by a power of two
+        float a, b;
+        unpack2(l2, a, b);
+        const uint32_t e = looks++ & 1u;
+        S.part[x][half][row] = a + b;
+        if (__any_sync(0xffffffffu, a + b > kTrHigh) && lane == 0) S.raise[x][e] = 1;
+        sync();
+        raise = S.raise[x][e] != 0;
+        if (sc == 0) S.raise[x][e ^ 1u] = 0;
+        if (raise) {
+          const float up = fmaxf(S.part[x][0][row], S.part[x][1][row]);
+          const float by = up > kTrHigh ? (float)ilogbf(up) : 0.f;
+          ref += by;
+          alpha = up <= kTrTop || !(up > kTrHigh) ? ex2a(-by) : __int_as_float(0x7fffffff);  // (out of range: a NaN)
+          l2 = pack2(a * alpha, b * alpha);
+          sync();  // (the parts are read)
+        }
+      }
+      const bool fresh = !has || raise || in_epoch == kWideEpoch;
+
+      // ---- P = 2^(logit - reference) as bf16 hi + lo, over S: the 16 keys of a slice keep their hi words in its
+      // first eight columns, lo in the other eight ----
+      if (act) {
+        const uint64_t nref2 = pack2(-ref, -ref);
+        uint32_t v[2][16];
+        tmem_ld16(s_cols, v[0]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t(&s)[16] = v[q & 1];
+          tmem_wait(s);
+          if (q < 3) tmem_ld16(s_cols + 16u * (q + 1), v[(q + 1) & 1]);
+          uint32_t hi_w[8], lo_w[8];
+          float d[16];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) fma2c(s[2 * i], s[2 * i + 1], scale2, nref2, d[2 * i], d[2 * i + 1]);
+          if (mw != ~0ull) {
+            const uint32_t bits = (uint32_t)(mw >> (16 * q));
+#pragma unroll
+            for (int c = 0; c < 16; ++c) d[c] = (bits >> c) & 1u ? d[c] : -INFINITY;
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint64_t p = pack2(ex2a(d[2 * i]), ex2a(d[2 * i + 1]));
+            l2 = add2u(l2, p);
+            float p0, p1;
+            unpack2(p, p0, p1);
+            hi_w[i] = pack_bf16x2(p0, p1);
+            unpack2(sub2u(p, pack2(bf16_lo(hi_w[i]), bf16_hi(hi_w[i]))), p0, p1);
+            lo_w[i] = pack_bf16x2(p0, p1);
+          }
+          tmem_st8(s_cols + 16u * q, hi_w);
+          tmem_st8(s_cols + 16u * q + 8u, lo_w);
+        }
+        tmem_st_wait();
+      }
+      tc_fence_before();
+      if (sc == 0) S.new_epoch[x] = fresh;
+      arrive_warp(&S.p_full[x]);
+
+      // ---- the epoch before this tile joins the total ----
+      if (fresh && has) {
+#pragma unroll 1
+        for (int i = 0; i < 4 && act; ++i) {
+          uint32_t e[16];
+          tmem_ld16(lane_base + (uint32_t)x * kTmemStreamW + kTmemO + 64u * half + 16u * i, e);
+          float4* p = tot + (32 * x + 4 * i) * kWideRows;
+          float4 q[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) q[c] = has_total ? __ldcg(p + c * kWideRows) : make_float4(0.f, 0.f, 0.f, 0.f);
+          tmem_wait(e);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            __stcg(p + c * kWideRows, make_float4((__uint_as_float(e[4 * c]) + q[c].x) * alpha,
+                                                  (__uint_as_float(e[4 * c + 1]) + q[c].y) * alpha,
+                                                  (__uint_as_float(e[4 * c + 2]) + q[c].z) * alpha,
+                                                  (__uint_as_float(e[4 * c + 3]) + q[c].w) * alpha));
+        }
+        tc_fence_before();
+        arrive_warp(&S.o_free[x]);
+        has_total = true;
+      }
+      in_epoch = fresh ? 1 : in_epoch + 1;
+      has = true;
+      ++n;
+      if (!alive) break;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_free(tmem, kTmemColsW);
+}
+
+template <int kBlocks>
+cudaError_t launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeAttnArgs& a, const TrParts& w,
+                   int use_tma, cudaStream_t stream) {
+  const size_t smem = sizeof(TrWideSmem<kBlocks>);
+  static_assert(sizeof(TrWideSmem<kBlocks>) <= 232448, "shared memory of one CTA");
+  cudaError_t e = cudaFuncSetAttribute(tree_attn_wide_kernel<kBlocks>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(tree_attn_wide_kernel<kBlocks>, dim3((unsigned)(w.rbs * w.ranges)), dim3(kTrThreads), smem, stream,
+                    1, kmap, vmap, a, w, use_tma);
+}
+
+}  // namespace
+
+cudaError_t launch_tree_attn_wide(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeAttnArgs& a,
+                                  const TrParts& w, int use_tma, cudaStream_t stream) {
+  return w.nr == kWideRows ? launch<1>(kmap, vmap, a, w, use_tma, stream)
+                           : launch<2>(kmap, vmap, a, w, use_tma, stream);
+}
+
+}  // namespace rtp
