@@ -131,8 +131,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   tc_fence_after();
   const uint32_t tmem = S.tmem_base;
   place.per = S.per;
-  place.lo = place.range * S.per;
-  place.hi = min(place.lo + S.per, S.total);
+  place.lo = S.start;
+  place.hi = S.end;
   const bool work = place.lo < place.hi;
 
   bool alive = true;
@@ -279,7 +279,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     for (int i = 0; i < 16; ++i) l2[i] = 0ull;
     uint32_t seen = 0u;                   // rows that attend any of them
     int seg = 0;                          // current segment
-    int seg_b = 0, seg_n = 0, seg_lo = 0, seg_drafts = 0, seg_depth = 0;  // what its masks need
+    int free_lo = 0, free_hi = 0;         // its tiles without masks
     int row_depth = 0;                    // (lane c: of row col0 + c)
     bool has = false, has_total = false;  // the stream has taken a tile of it; its epochs have a total
     int in_epoch = 0;
@@ -416,48 +416,48 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       if (cur.x < 0 || !alive) break;
       if (turn) {
         const TrSegInfo& info = S.seg[seg % kTrRing];
-        seg_b = info.b;
-        seg_n = info.n;
-        seg_lo = info.lo;
-        seg_drafts = info.draft_tiles;
-        seg_depth = info.max_depth;
-        row_depth = draft_depth(A, seg_b, (t_first + lane) % A.T);
+        free_lo = info.free_lo;
+        free_hi = info.free_hi;
+        row_depth = draft_depth(A, info.b, (t_first + lane) % A.T);
       }
 
       // ---- which of this thread's rows attend its key, and whether it is one at all ----
       uint32_t mw = ~0u;
-      bool is_key;
-      if (cur.y < seg_drafts) {
-        const int j = cur.y * kTrKeys + key;
-        is_key = j < A.T;
-        // lane c reads the tree word of row c; transposed, a lane has its key's bits over the rows
-        const bool words = cur.y * kTrKeys + 32 * quad < A.T && col0 + lane < nrows;
-        mw = transpose32(words ? __ldg(A.tree + ((int64_t)seg_b * A.T + (t_first + lane) % A.T) * A.tree_words +
-                                       4 * cur.y + quad)
-                               : 0u,
-                         lane);
-        if (!is_key) mw = 0u;
-        if (A.W > 0 && seg_depth >= A.W) {
-          const int dj = is_key ? draft_depth(A, seg_b, j) : 0;
-          uint32_t in = 0u;
-#pragma unroll 4
-          for (int c = 0; c < 32; ++c) in |= (uint32_t)(dj > __shfl_sync(0xffffffffu, row_depth, c) - A.W) << c;
-          mw &= in;
-        }
-      } else if constexpr (SEL) {
-        mw = S.kmask[cur.x & 3][col0 >> 5][key];
-        is_key = mw != 0u;
-      } else {
-        const uint32_t p0 = (uint32_t)seg_lo + (uint32_t)(cur.y - seg_drafts) * kTrKeys;
-        const int age = seg_n - 1 - (int)(p0 + (uint32_t)key);  // (below 0: past the end)
-        is_key = age >= 0;
-        if (!is_key) mw = 0u;
-        if (A.W > 0 && seg_n - 1 - (int)p0 > oldest_age(A, seg_depth)) {
-          uint32_t in = 0u;
-#pragma unroll 4
-          for (int c = 0; c < 32; ++c)
-            in |= (uint32_t)(age <= oldest_age(A, __shfl_sync(0xffffffffu, row_depth, c))) << c;
-          mw &= in;
+      bool is_key = true;
+      if (SEL || cur.y < free_lo || cur.y >= free_hi) {
+        const TrSegInfo& info = S.seg[seg % kTrRing];
+        if (cur.y < info.draft_tiles) {
+          const int j = cur.y * kTrKeys + key;
+          is_key = j < A.T;
+          // lane c reads the tree word of row c; transposed, a lane has its key's bits over the rows
+          const bool words = cur.y * kTrKeys + 32 * quad < A.T && col0 + lane < nrows;
+          mw = transpose32(words ? __ldg(A.tree + ((int64_t)info.b * A.T + (t_first + lane) % A.T) * A.tree_words +
+                                         4 * cur.y + quad)
+                                 : 0u,
+                           lane);
+          if (!is_key) mw = 0u;
+          if (A.W > 0 && info.max_depth >= A.W) {
+            const int dj = is_key ? draft_depth(A, info.b, j) : 0;
+            uint32_t in = 0u;
+  #pragma unroll 4
+            for (int c = 0; c < 32; ++c) in |= (uint32_t)(dj > __shfl_sync(0xffffffffu, row_depth, c) - A.W) << c;
+            mw &= in;
+          }
+        } else if constexpr (SEL) {
+          mw = S.kmask[cur.x & 3][col0 >> 5][key];
+          is_key = mw != 0u;
+        } else {
+          const uint32_t p0 = (uint32_t)info.lo + (uint32_t)(cur.y - info.draft_tiles) * kTrKeys;
+          const int age = info.n - 1 - (int)(p0 + (uint32_t)key);  // (below 0: past the end)
+          is_key = age >= 0;
+          if (!is_key) mw = 0u;
+          if (A.W > 0 && info.n - 1 - (int)p0 > oldest_age(A, info.max_depth)) {
+            uint32_t in = 0u;
+  #pragma unroll 4
+            for (int c = 0; c < 32; ++c)
+              in |= (uint32_t)(age <= oldest_age(A, __shfl_sync(0xffffffffu, row_depth, c))) << c;
+            mw &= in;
+          }
         }
       }
       seen |= mw;

@@ -50,8 +50,8 @@ constexpr int kBarLoad = 1;                  // named barrier
 // What the softmax needs to know of a segment (a CTA's share of a group's tiles).
 struct TrSegInfo {
   int b, kvh, n, lo, draft_tiles, max_depth;
-  int slot;   // where its partial result goes, or -1: the whole group
-  int pad;
+  int slot;              // where its partial result goes, or -1: the whole group
+  int free_lo, free_hi;  // tiles of the group whose keys every row attends
 };
 
 // ---- small helpers --------------------------------------------------------------
@@ -193,12 +193,17 @@ RTP_DEVICE bool tree_bit(const TreeAttnArgs& A, int b, int t, int j) {
 }
 
 // Tiles of one KV head of a sequence: its drafts first, then the committed keys from position lo on (with a
-// selection: rounds of kTrRound keys, aligned).
+// selection: rounds of kTrRound keys, aligned).  On the line a group takes more room (units) than its tiles: with
+// `align` the next multiple of it, so that every group begins a range; else up to three tiles more, the time that
+// a CTA spends on ending one group and beginning another.
 struct TrSpan {
-  int n, lo, draft_tiles, tiles;
+  int n, lo, draft_tiles, tiles, units;
 };
+RTP_DEVICE int units_of(int tiles, int align) {
+  return align ? (tiles + align - 1) / align * align : tiles + min(3, tiles / 16);
+}
 template <bool SEL>
-RTP_DEVICE TrSpan span_of(const TreeAttnArgs& A, int b) {
+RTP_DEVICE TrSpan span_of(const TreeAttnArgs& A, int b, int align) {
   constexpr uint32_t kStep = SEL ? kTrRound : kTrKeys;
   TrSpan s;
   s.n = committed(A, b);
@@ -206,6 +211,7 @@ RTP_DEVICE TrSpan span_of(const TreeAttnArgs& A, int b) {
   if (SEL) s.lo = s.lo / kTrRound * kTrRound;
   s.draft_tiles = (A.T + kTrKeys - 1) / kTrKeys;
   s.tiles = s.draft_tiles + (int)(((uint32_t)(s.n - s.lo) + kStep - 1) / kStep);
+  s.units = units_of(s.tiles, align);
   return s;
 }
 
@@ -214,38 +220,36 @@ struct TrSeg {
   int b, kvh;
   TrSpan span;
   int u0, u1;
-  int base;  // the line's tile number of the group's tile 0
+  int base;  // where the group's tile 0 is on the line
 };
 
-// Walks the segments of the range [lo, hi) of the line of tiles.
+// Walks the segments of the range [lo, hi) of the line; lo is a tile (not the room behind a group).
 template <bool SEL>
 struct TrWalk {
-  int pos, hi, base_b;
+  int hi, base_b, align;
   TrSeg s;
-  RTP_DEVICE void start(const TreeAttnArgs& A, int lo, int end, int b, int base) {
-    pos = lo;
+  RTP_DEVICE void start(const TreeAttnArgs& A, int lo, int end, int b, int base, int al) {
     hi = end;
+    align = al;
     base_b = base;
     s.b = b;
-    s.span = span_of<SEL>(A, b);
-    s.kvh = (lo - base) / s.span.tiles;
-    fill();
-  }
-  RTP_DEVICE void fill() {
-    s.base = base_b + s.kvh * s.span.tiles;
-    s.u0 = pos - s.base;
+    s.span = span_of<SEL>(A, b, align);
+    s.kvh = (lo - base) / s.span.units;
+    s.base = base_b + s.kvh * s.span.units;
+    s.u0 = lo - s.base;
     s.u1 = min(s.span.tiles, hi - s.base);
   }
-  RTP_DEVICE bool next(const TreeAttnArgs& A) {
-    pos = s.base + s.u1;
-    if (pos >= hi) return false;
+  // Whether the range goes on behind this segment.
+  RTP_DEVICE bool more() const { return s.base + s.span.units < hi; }
+  RTP_DEVICE void next(const TreeAttnArgs& A) {
     if (++s.kvh == A.Hk) {
-      base_b += A.Hk * s.span.tiles;
+      base_b += A.Hk * s.span.units;
       s.kvh = 0;
-      s.span = span_of<SEL>(A, ++s.b);
+      s.span = span_of<SEL>(A, ++s.b, align);
     }
-    fill();
-    return true;
+    s.base = base_b + s.kvh * s.span.units;
+    s.u0 = 0;
+    s.u1 = min(s.span.tiles, hi - s.base);
   }
 };
 
@@ -314,8 +318,9 @@ struct TrFeed {
   int row_at[NR];                // each row's draft times 8 plus its head in the group
   int2 meta[kTrRing];            // per tile: its number in the group; 4 * segment + 2 * (CTA's last) + (segment's last)
   TrSegInfo seg[kTrRing];
-  int start_b, start_base;       // where this CTA's range begins: sequence, first tile of the sequence
-  int total, per;                // tiles of the whole line, and of a range
+  int start_b, start_base, start;  // where this CTA's range begins: sequence, the sequence's place on the line, tile
+  int end;                       // and where it ends (start >= end: nothing to do)
+  int per, align;                // length of a range; see units_of
   int cnt[2][kTrLoadWarps];
   int qkey[kQueue];              // selected keys waiting for a tile (ring)
   uint2 qbits[kQueue];           // and which rows selected them
@@ -365,26 +370,50 @@ RTP_DEVICE void tree_feed_init(Smem& S, const TreeAttnArgs& A, const TrPlace& p,
   }
 }
 
-// Warp 0: this CTA's range of the line of tiles.
+// Warp 0: this CTA's range of the line.
 template <bool SEL, typename Smem>
 RTP_DEVICE void tree_find_range(Smem& S, const TreeAttnArgs& A, const TrParts& W, int range) {
   const int lane = threadIdx.x & 31;
-  int sum = 0;
-  const int first = lane < A.B ? span_of<SEL>(A, lane).tiles : 0;
+  int sum = 0, tiles = 0;
+  TrSpan first = span_of<SEL>(A, min(lane, A.B - 1), 0);
 #pragma unroll 1
-  for (int b = lane; b < A.B; b += 32) sum += b == lane ? first : span_of<SEL>(A, b).tiles;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  const int total = sum * A.Hk, per = (total + W.ranges - 1) / W.ranges, lo = range * per;
-  if (lane == 0) {
-    S.total = total;
-    S.per = per;
+  for (int b = lane; b < A.B; b += 32) {
+    const TrSpan span = b == lane ? first : span_of<SEL>(A, b, 0);
+    sum += span.units;
+    tiles += span.tiles;
   }
+  sum = __reduce_add_sync(0xffffffffu, sum);
+  tiles = __reduce_add_sync(0xffffffffu, tiles);
+  int total = sum * A.Hk, per = (total + W.ranges - 1) / W.ranges, align = 0;
+  if (A.B <= 32) {
+    // Ranges that never cross a group's end, if they can be no longer: lane l tries that many tiles more than the
+    // least.  (48 rings of 33 tiles: 3 ranges of 11 each, not 4 of 12 pieces: 53 -> 44 us.)
+    const int range_l = (tiles * A.Hk + W.ranges - 1) / W.ranges + lane;
+    int used = 0;
+#pragma unroll 1
+    for (int b = 0; b < A.B; ++b)
+      used += (int)((unsigned)(__shfl_sync(0xffffffffu, first.tiles, b) + range_l - 1) / (unsigned)range_l);
+    const uint32_t fits = __ballot_sync(0xffffffffu, used * A.Hk <= W.ranges && range_l <= per);
+    if (fits) {
+      per = align = __shfl_sync(0xffffffffu, range_l, __ffs(fits) - 1);
+      total = __shfl_sync(0xffffffffu, used, __ffs(fits) - 1) * A.Hk * per;
+      first.units = units_of(first.tiles, align);
+    }
+  }
+  const int lo = range * per;
+  if (lane == 0) {
+    S.per = per;
+    S.align = align;
+    S.end = min(lo + per, total);
+    S.start = total;
+  }
+  __syncwarp();
   int base = 0;
 #pragma unroll 1
   for (int b0 = 0; b0 < A.B && lo < total; b0 += 32) {
     const int b = b0 + lane;
-    const int mine = (b0 == 0 ? first : b < A.B ? span_of<SEL>(A, b).tiles : 0) * A.Hk;
+    const TrSpan span = b0 == 0 ? first : span_of<SEL>(A, min(b, A.B - 1), align);
+    const int mine = b < A.B ? span.units * A.Hk : 0;
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -394,8 +423,12 @@ RTP_DEVICE void tree_find_range(Smem& S, const TreeAttnArgs& A, const TrParts& W
     const uint32_t past = __ballot_sync(0xffffffffu, base + incl > lo);
     if (past) {
       if (lane == __ffs(past) - 1) {
-        S.start_b = b;
-        S.start_base = base + incl - mine;
+        const int base_b = base + incl - mine, kvh = (lo - base_b) / span.units, u = lo - base_b - kvh * span.units;
+        // in the room behind a group: from the next one on
+        const bool skip = u >= span.tiles, last = kvh + 1 == A.Hk;
+        S.start = skip ? base_b + (kvh + 1) * span.units : lo;
+        S.start_b = skip && last ? b + 1 : b;
+        S.start_base = skip && last ? base_b + mine : base_b;
       }
       break;
     }
@@ -415,7 +448,7 @@ RTP_DEVICE void tree_load(Smem& S, const CUtensorMap& kmap, const CUtensorMap& v
   // (8 rows on, the swizzle is the same)
   const uint32_t slot0 = (uint32_t)r_first * 128u + (uint32_t)(((chunk & 7) ^ r_first) << 4);
   const uint32_t slot_kv = slot0 + (uint32_t)(chunk >> 3) * (uint32_t)kTrHalf;
-  uint32_t it = 0, k_loads = 0;  // tiles so far; tiles whose K has been sent for
+  uint32_t it = 0, k_loads = 0, v_loads = 0;  // tiles so far; tiles whose K, whose V has been sent for
   int segs = 0;
   bool q_due = false;
   // Waits for a free K or V stage; false (for all loaders alike) once any wait gave up.
@@ -465,16 +498,17 @@ RTP_DEVICE void tree_load(Smem& S, const CUtensorMap& kmap, const CUtensorMap& v
     }
     cp_wait<0>();
     landed(&S.v_full[st]);
-    k_loads = ++it;
+    k_loads = v_loads = ++it;
     return true;
   };
   TrWalk<SEL> walk;
   bool more = lo < hi, ok = true;
-  if (more) walk.start(A, lo, hi, S.start_b, S.start_base);
+  if (more) walk.start(A, lo, hi, S.start_b, S.start_base, S.align);
 #pragma unroll 1
   while (more && ok) {
     const TrSeg s = walk.s;
-    const int seg_flags = 4 * segs, last_flags = seg_flags + (s.base + s.u1 < hi ? 1 : 3);
+    more = walk.more();
+    const int seg_flags = 4 * segs, last_flags = seg_flags + (more ? 1 : 3);
     // ---- the query rows (the previous segment's products are done with the buffer) ----
     {
       const bool free = segs == 0 || wait_bar(&S.q_free, (segs - 1) & 1u, alive, A);
@@ -506,7 +540,10 @@ RTP_DEVICE void tree_load(Smem& S, const CUtensorMap& kmap, const CUtensorMap& v
       }
       const bool whole = s.u0 == 0 && s.u1 == s.span.tiles;
       info.slot = whole ? -1 : place.rb * 2 * W.ranges + 2 * place.range + (s.u0 == 0 ? 1 : 0);
-      info.pad = 0;
+      // every row attends the keys of a whole tile that is young enough for the deepest draft
+      const int oldest = oldest_age(A, info.max_depth), young = A.W > 0 ? max(info.n - 1 - oldest - info.lo, 0) : 0;
+      info.free_lo = info.draft_tiles + (A.W > 0 && oldest < 0 ? s.span.tiles : (young + kTrKeys - 1) / kTrKeys);
+      info.free_hi = info.draft_tiles + (info.n - info.lo) / kTrKeys;
       if (lt == 0) {
         S.seg[segs % kTrRing] = info;
         if (s.u0 == 0 && place.rb == 0)
@@ -515,7 +552,7 @@ RTP_DEVICE void tree_load(Smem& S, const CUtensorMap& kmap, const CUtensorMap& v
       ++segs;
     }
     const int drafts_end = min(s.u1, s.span.draft_tiles);
-    more = walk.next(A);
+    if (more) walk.next(A);
     for (int u = s.u0; u < drafts_end && ok; ++u)
       ok = gather(A.kn, A.vn, s, u, u + 1 == s.u1 ? last_flags : seg_flags, [&](int r, bool& live) {
         const int j = u * kTrKeys + r;
@@ -524,55 +561,50 @@ RTP_DEVICE void tree_load(Smem& S, const CUtensorMap& kmap, const CUtensorMap& v
       });
     if (!ok || s.u1 <= s.span.draft_tiles) continue;
     if constexpr (!SEL) {
-      auto by_tma = [&](int u, uint32_t& p0, int& left, int& first) {  // a whole tile of neighbouring rows
-        p0 = (uint32_t)s.span.lo + (uint32_t)(u - s.span.draft_tiles) * kTrKeys;
-        left = s.span.n - (int)p0;  // committed rows from here on
-        first = row_of(A, p0);
-        return use_tma && left >= kTrKeys && A.N - first >= kTrKeys;
-      };
       auto load = [&](const CUtensorMap* map, uint8_t* tile, uint64_t* full, int first) {
         mbar_expect_tx(full, kTrTile);
         tma_load_4d(tile, map, full, 0, first, s.kvh, s.b);
         tma_load_4d(tile + kTrHalf, map, full, 64, first, s.kvh, s.b);
       };
-      bool ahead = false;  // this tile's K is already on its way
 #pragma unroll 1
-      for (int u = max(s.u0, s.span.draft_tiles); u < s.u1 && ok; ++u) {
-        uint32_t p0;
-        int left, first;
-        const int st = it & 1;
-        if (by_tma(u, p0, left, first)) {
-          // the next tile's K before this one's V: scores are computed ahead of the products with V
+      for (int u = max(s.u0, s.span.draft_tiles); u < s.u1 && ok;) {
+        const uint32_t p0 = (uint32_t)s.span.lo + (uint32_t)(u - s.span.draft_tiles) * kTrKeys;
+        const int left = s.span.n - (int)p0;  // committed rows from here on
+        const int first = row_of(A, p0);
+        // whole tiles of neighbouring rows come by TMA, by one thread
+        const int run = use_tma ? min(s.u1 - u, min(left, A.N - first) / kTrKeys) : 0;
+        if (run > 0) {
+          // the next tile's K goes before this one's V: scores are computed ahead of the products with V
+          auto send_k = [&](int i) {
+            const uint32_t tile = it + i, st = tile & 1;
+            if (!wait_bar(&S.k_empty[st], ((tile >> 1) & 1u) ^ 1u, alive, A)) return;
+            S.meta[tile % kTrRing] = make_int2(u + i, u + i + 1 == s.u1 ? last_flags : seg_flags);
+            load(&kmap, S.k[st], &S.k_full[st], first + i * kTrKeys);
+            k_loads = tile + 1;
+          };
+          if (lt == 0) send_k(0);
+          if (q_due) {
+            cp_wait<0>();
+            landed(nullptr);
+          }
+          if (lt == 0) {
 #pragma unroll 1
-          for (int i = ahead ? 1 : 0; i < 2 && ok; ++i) {
-            uint32_t q0;
-            int rest, at;
-            if (u + i == s.u1 || !by_tma(u + i, q0, rest, at)) {
-              ahead = false;
-              break;
-            }
-            it += i;
-            ok = stage_free(S.k_empty);
-            it -= i;
-            if (lt == 0 && ok) {
-              S.meta[(it + i) % kTrRing] = make_int2(u + i, u + i + 1 == s.u1 ? last_flags : seg_flags);
-              load(&kmap, S.k[st ^ i], &S.k_full[st ^ i], at);
-              k_loads = it + i + 1;
-            }
-            ahead = i;
-            if (q_due) {
-              cp_wait<0>();
-              landed(nullptr);
+            for (int i = 0; i < run && alive; ++i) {
+              if (i + 1 < run) send_k(i + 1);
+              const uint32_t tile = it + i, st = tile & 1;
+              if (!wait_bar(&S.v_empty[st], ((tile >> 1) & 1u) ^ 1u, alive, A)) break;
+              load(&vmap, S.v[st], &S.v_full[st], first + i * kTrKeys);
+              v_loads = tile + 1;
             }
           }
-          if (!ok || !(ok = stage_free(S.v_empty))) break;
-          if (lt == 0) load(&vmap, S.v[st], &S.v_full[st], first);
-          ++it;
+          it += run;
+          u += run;
         } else {
           ok = gather(A.k, A.v, s, u, u + 1 == s.u1 ? last_flags : seg_flags, [&](int r, bool& live) {
             live = r < left;
             return live ? row_of(A, p0 + (uint32_t)r) : 0;
           });
+          ++u;
         }
       }
     } else {
@@ -680,7 +712,7 @@ RTP_DEVICE void tree_load(Smem& S, const CUtensorMap& kmap, const CUtensorMap& v
   if (lt == 0)  // copies still in flight land before the CTA ends
     {
     for (uint32_t i = k_loads > 2 ? k_loads - 2 : 0; i < k_loads; ++i) mbar_drain(&S.k_full[i & 1], (i >> 1) & 1u, A.err);
-    for (uint32_t i = it > 2 ? it - 2 : 0; i < it; ++i) mbar_drain(&S.v_full[i & 1], (i >> 1) & 1u, A.err);
+    for (uint32_t i = v_loads > 2 ? v_loads - 2 : 0; i < v_loads; ++i) mbar_drain(&S.v_full[i & 1], (i >> 1) & 1u, A.err);
     }
 }
 

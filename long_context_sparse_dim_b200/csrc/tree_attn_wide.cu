@@ -88,8 +88,8 @@ tree_attn_wide_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
   tc_fence_after();
   const uint32_t tmem = S.tmem_base;
   place.per = S.per;
-  place.lo = place.range * S.per;
-  place.hi = min(place.lo + S.per, S.total);
+  place.lo = S.start;
+  place.hi = S.end;
   const bool work = place.lo < place.hi;
 
   bool alive = true;
@@ -243,7 +243,7 @@ tree_attn_wide_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
     uint64_t l2 = 0ull;     // the row's sum over this thread's keys, in two parts
     bool seen = false;      // the row attends some of them
     int seg = 0;            // current segment
-    int seg_b = 0, seg_n = 0, seg_lo = 0, seg_drafts = 0, seg_depth = 0, oldest = 0;  // what its masks need
+    int free_lo = 0, free_hi = 0;  // its tiles without masks
     bool has = false, has_total = false;  // the stream has taken a tile of it; its epochs have a total
     int in_epoch = 0;
     uint32_t n = 0, looks = 0;            // ops of this stream so far; looks at the sums
@@ -382,39 +382,39 @@ tree_attn_wide_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
       if (cur.x < 0 || !alive) break;
       if (turn) {
         const TrSegInfo& info = S.seg[seg % kTrRing];
-        seg_b = info.b;
-        seg_n = info.n;
-        seg_lo = info.lo;
-        seg_drafts = info.draft_tiles;
-        seg_depth = info.max_depth;
-        oldest = oldest_age(A, draft_depth(A, seg_b, t));
+        free_lo = info.free_lo;
+        free_hi = info.free_hi;
       }
 
       // ---- which of this thread's keys the row attends ----
       uint64_t mw = ~0ull;
-      if (cur.y < seg_drafts) {
-        const int j0 = cur.y * kTrKeys + 64 * half, w0 = 4 * cur.y + 2 * half;
-        const uint32_t* words = A.tree + ((int64_t)seg_b * A.T + t) * A.tree_words + w0;
-        const uint32_t lo = j0 < A.T ? __ldg(words) : 0u, hi = j0 + 32 < A.T ? __ldg(words + 1) : 0u;
-        mw = (uint64_t)hi << 32 | lo;
-        const int left = A.T - j0;
-        if (left < 64) mw &= left > 0 ? (1ull << left) - 1ull : 0ull;
-        if (A.W > 0 && seg_depth >= A.W) {
-          const int depth = draft_depth(A, seg_b, t);
-#pragma unroll 1
-          for (int j = 0; j < 64 && j < left; ++j)
-            if (draft_depth(A, seg_b, j0 + j) <= depth - A.W) mw &= ~(1ull << j);
+      if (cur.y < free_lo || cur.y >= free_hi) {
+        const TrSegInfo& info = S.seg[seg % kTrRing];
+        if (cur.y < info.draft_tiles) {
+          const int j0 = cur.y * kTrKeys + 64 * half, w0 = 4 * cur.y + 2 * half;
+          const uint32_t* words = A.tree + ((int64_t)info.b * A.T + t) * A.tree_words + w0;
+          const uint32_t lo = j0 < A.T ? __ldg(words) : 0u, hi = j0 + 32 < A.T ? __ldg(words + 1) : 0u;
+          mw = (uint64_t)hi << 32 | lo;
+          const int left = A.T - j0;
+          if (left < 64) mw &= left > 0 ? (1ull << left) - 1ull : 0ull;
+          if (A.W > 0 && info.max_depth >= A.W) {
+            const int depth = draft_depth(A, info.b, t);
+  #pragma unroll 1
+            for (int j = 0; j < 64 && j < left; ++j)
+              if (draft_depth(A, info.b, j0 + j) <= depth - A.W) mw &= ~(1ull << j);
+          }
+        } else {
+          const uint32_t p0 = (uint32_t)info.lo + (uint32_t)(cur.y - info.draft_tiles) * kTrKeys + 64u * half;
+          const int left = info.n - (int)p0;
+          if (left < 64) mw = left > 0 ? (1ull << left) - 1ull : 0ull;
+          if (A.W > 0) {  // key i of the half is left - 1 - i tokens older than the newest
+            const int oldest = oldest_age(A, draft_depth(A, info.b, t));
+            const int cut = oldest < 0 ? 64 : max(left - 1 - oldest, 0);
+            mw &= cut < 64 ? ~0ull << cut : 0ull;
+          }
         }
-      } else {
-        const uint32_t p0 = (uint32_t)seg_lo + (uint32_t)(cur.y - seg_drafts) * kTrKeys + 64u * half;
-        const int left = seg_n - (int)p0;
-        if (left < 64) mw = left > 0 ? (1ull << left) - 1ull : 0ull;
-        if (A.W > 0) {  // key i of the half is left - 1 - i tokens older than the newest
-          const int cut = oldest < 0 ? 64 : max(left - 1 - oldest, 0);
-          mw &= cut < 64 ? ~0ull << cut : 0ull;
-        }
+        if (!live) mw = 0ull;
       }
-      if (!live) mw = 0ull;
       seen = seen | (mw != 0ull);
 
       bool raise = false;
