@@ -42,8 +42,10 @@
 // the rows that hold no token.
 //
 // Work: the tiles of all (sequence, KV head) groups form one line, cut into
-// equal ranges, one CTA each; a CTA's range may begin or end inside a group, and
-// such pieces are joined by a second kernel (one warp or more per query row).
+// equal ranges, one CTA each; a CTA's range may begin or end inside a group.
+// Such pieces are joined by a second kernel, one warp or more per query row (by
+// the CTA that is the last to be done with a group it took 3 to 15 us longer:
+// that is 8 warps, one row after the other).
 //
 // With a selection a CTA reads the mask words of its rows, 512 keys at a time,
 // queues the keys that any row selected (a ballot per key transposes the bits:
@@ -633,6 +635,57 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   if (warp == 0) tmem_free(tmem, kTmemCols);
 }
 
+// The pieces of one row (part, part + step, ..) of a group: m, l with the sum of 2^logit being 2^m l, and o
+// unnormalised to match; four head dims per lane.
+struct TrSum {
+  float m = kTrNone, l = 0.f;
+  float4 o = {0.f, 0.f, 0.f, 0.f};
+  // one more piece: 2^s w to the sum, 2^s v y to the output (an infinite s makes both NaNs)
+  RTP_DEVICE void take(float s, float w, float v, const float4& y) {
+    const float f = s <= kTrNone ? 0.f : ex2a(s - m);
+    if (f == 0.f && w == w) return;  // (what it holds may be anything)
+    l += f * w;
+    const float g = f * v;
+    o = make_float4(o.x + g * y.x, o.y + g * y.y, o.z + g * y.z, o.w + g * y.w);
+  }
+  RTP_DEVICE void rebase(float mn) {
+    const float al = ex2a(m - mn);
+    m = mn;
+    l *= al;
+    o = make_float4(o.x * al, o.y * al, o.z * al, o.w * al);
+  }
+  RTP_DEVICE void finish() {
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  }
+};
+RTP_DEVICE TrSum join_pieces(const TrParts& W, int2 pieces, int rb, int c, int part, int step) {
+  TrSum sum;
+  const int lane = threadIdx.x & 31;
+  const int64_t slot0 = (int64_t)rb * 2 * W.ranges;
+  auto at = [&](int i) { return (slot0 + 2 * (pieces.x + i) + (i == 0)) * W.nr + c; };
+  constexpr int kUnroll = 4;
+#pragma unroll 1
+  for (int i = part; i < pieces.y; i += step * kUnroll) {
+    float2 s[kUnroll];
+    float4 y[kUnroll];
+#pragma unroll
+    for (int q = 0; q < kUnroll; ++q) {
+      const int p = i + step * q;
+      s[q] = make_float2(kTrNone, 0.f);
+      y[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (p < pieces.y) {
+        s[q] = __ldcg(W.ml + at(p));
+        y[q] = __ldcg(reinterpret_cast<const float4*>(W.o + at(p) * kHeadDim) + lane);
+      }
+    }
+    sum.rebase(fmaxf(fmaxf(fmaxf(sum.m, s[0].x), fmaxf(s[1].x, s[2].x)), s[3].x));
+#pragma unroll
+    for (int q = 0; q < kUnroll; ++q) sum.take(s[q].x, s[q].y, s[q].y, y[q]);
+  }
+  return sum;
+}
+
 // Joins the pieces of groups that several CTAs worked on: WPR warps per query row, pieces in turn, four
 // head dims per lane.
 constexpr int kTrJoinThreads = 256;
@@ -650,64 +703,24 @@ __global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const __grid_
   const int grp = have ? (int)(x / rows) : 0, r = have ? (int)(x % rows) : 0;
   const int2 pieces = have ? W.table[grp] : make_int2(0, 1);
   const bool join = pieces.y > 1;  // (one piece: its CTA has written the output)
-  float m = kTrNone, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  // one more piece (or partial join): 2^s w to the sum, 2^s v y to the output (an infinite s makes both NaNs)
-  auto take = [&](float s, float w, float v, const float4& y, float mn) {
-    const float f = s <= kTrNone ? 0.f : ex2a(s - mn);
-    if (f == 0.f && w == w) return;  // (what it holds may be anything)
-    l += f * w;
-    const float g = f * v;
-    o = make_float4(o.x + g * y.x, o.y + g * y.y, o.z + g * y.z, o.w + g * y.w);
-  };
-  if (join) {
-    const int c = r % W.nr;
-    const int64_t slot0 = (int64_t)(r / W.nr) * 2 * W.ranges;
-    auto at = [&](int i) { return (slot0 + 2 * (pieces.x + i) + (i == 0)) * W.nr + c; };
-    constexpr int kUnroll = 4;
-    for (int i = part; i < pieces.y; i += WPR * kUnroll) {
-      float2 s[kUnroll];
-      float4 y[kUnroll];
-#pragma unroll
-      for (int q = 0; q < kUnroll; ++q) {
-        const int p = i + WPR * q;
-        s[q] = make_float2(kTrNone, 0.f);
-        y[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (p < pieces.y) {
-          s[q] = W.ml[at(p)];
-          y[q] = reinterpret_cast<const float4*>(W.o + at(p) * kHeadDim)[lane];
-        }
-      }
-      float mn = m;
-#pragma unroll
-      for (int q = 0; q < kUnroll; ++q) mn = fmaxf(mn, s[q].x);
-      const float al = ex2a(m - mn);
-      m = mn;
-      l *= al;
-      o = make_float4(o.x * al, o.y * al, o.z * al, o.w * al);
-#pragma unroll
-      for (int q = 0; q < kUnroll; ++q) take(s[q].x, s[q].y, s[q].y, y[q], mn);
-    }
-  }
+  TrSum sum;
+  if (join) sum = join_pieces(W, pieces, r / W.nr, r % W.nr, part, WPR);
   if (WPR > 1) {
-    so[warp][lane] = o;
-    if (lane == 0) sml[warp] = make_float2(m, l);
+    so[warp][lane] = sum.o;
+    if (lane == 0) sml[warp] = make_float2(sum.m, sum.l);
     __syncthreads();
     if (part != 0) return;
-    float M = kTrNone;
+    sum = TrSum();
 #pragma unroll
-    for (int w = 0; w < WPR; ++w) M = fmaxf(M, sml[warp + w].x);
-    l = 0.f;
-    o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int w = 0; w < WPR; ++w) sum.m = fmaxf(sum.m, sml[warp + w].x);
 #pragma unroll
-    for (int w = 0; w < WPR; ++w) take(sml[warp + w].x, sml[warp + w].y, 1.f, so[warp + w][lane], M);
+    for (int w = 0; w < WPR; ++w) sum.take(sml[warp + w].x, sml[warp + w].y, 1.f, so[warp + w][lane]);
   }
   if (!join) return;
-  const float inv = l != 0.f ? 1.f / l : 0.f;
-  o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  sum.finish();
   const int b = grp / A.Hk, h = grp % A.Hk * A.G + r / A.T, t = r % A.T;
-  if (__any_sync(0xffffffffu, !finite4(o))) scalar_row(A, b, h, t, o);
-  store4(A, b * A.o.sb + h * A.o.sh + t * A.o.sn + 4 * lane, o);
+  if (__any_sync(0xffffffffu, !finite4(sum.o))) scalar_row(A, b, h, t, sum.o);
+  store4(A, b * A.o.sb + h * A.o.sh + t * A.o.sn + 4 * lane, sum.o);
 }
 
 // ---- layout of the workspace -------------------------------------------------------------
@@ -781,8 +794,9 @@ cudaError_t launch_tree_attn(const TreeAttnArgs& a, cudaStream_t stream) {
                         : L.nr == 64 ? launch_tiles<false>(kmap, vmap, a, w, use_tma, stream)
                                      : launch_tree_attn_wide(kmap, vmap, a, w, use_tma, stream);
   if (e != cudaSuccess) return e;
-  // about this many pieces in a group: one warp per row takes four at a time
-  const int64_t pieces = L.ranges / ((int64_t)a.B * a.Hk) + 1;
+  // about this many pieces in a group; one warp per row takes four at a time
+  const int64_t tiles = (a.T + kTrKeys - 1) / kTrKeys + a.N / kTrKeys + 1;
+  const int64_t most = L.ranges / ((int64_t)a.B * a.Hk) + 1, pieces = most < tiles ? most : tiles;
   if (pieces <= 4) return launch_join<1>(a, w, stream);
   if (pieces <= 16) return launch_join<4>(a, w, stream);
   return launch_join<8>(a, w, stream);

@@ -386,18 +386,17 @@ RTP_DEVICE void tree_find_range(Smem& S, const TreeAttnArgs& A, const TrParts& W
   tiles = __reduce_add_sync(0xffffffffu, tiles);
   int total = sum * A.Hk, per = (total + W.ranges - 1) / W.ranges, align = 0;
   if (A.B <= 32) {
-    // Ranges that never cross a group's end, if they can be no longer: lane l tries that many tiles more than the
-    // least.  (48 rings of 33 tiles: 3 ranges of 11 each, not 4 of 12 pieces: 53 -> 44 us.)
-    const int range_l = (tiles * A.Hk + W.ranges - 1) / W.ranges + lane;
-    int used = 0;
+    // Ranges that never cross a group's end, if they can be no longer.  (48 rings of 33 tiles: 3 ranges of 11 each,
+    // not 4 of 12 pieces: 53 -> 44 us.)
 #pragma unroll 1
-    for (int b = 0; b < A.B; ++b)
-      used += (int)((unsigned)(__shfl_sync(0xffffffffu, first.tiles, b) + range_l - 1) / (unsigned)range_l);
-    const uint32_t fits = __ballot_sync(0xffffffffu, used * A.Hk <= W.ranges && range_l <= per);
-    if (fits) {
-      per = align = __shfl_sync(0xffffffffu, range_l, __ffs(fits) - 1);
-      total = __shfl_sync(0xffffffffu, used, __ffs(fits) - 1) * A.Hk * per;
-      first.units = units_of(first.tiles, align);
+    for (int c = (tiles * A.Hk + W.ranges - 1) / W.ranges; c <= per; ++c) {
+      const int used = A.Hk * __reduce_add_sync(0xffffffffu, lane < A.B ? (first.tiles + c - 1) / c : 0);
+      if (used <= W.ranges) {
+        per = align = c;
+        total = used * c;
+        first.units = units_of(first.tiles, align);
+        break;
+      }
     }
   }
   const int lo = range * per;
@@ -509,6 +508,30 @@ RTP_DEVICE void tree_load(Smem& S, const CUtensorMap& kmap, const CUtensorMap& v
     const TrSeg s = walk.s;
     more = walk.more();
     const int seg_flags = 4 * segs, last_flags = seg_flags + (more ? 1 : 3);
+    // whole tiles of neighbouring rows come by TMA: how many from tile u on
+    auto tma_run = [&](int u, int& first) {
+      const uint32_t p0 = (uint32_t)s.span.lo + (uint32_t)(u - s.span.draft_tiles) * kTrKeys;
+      first = row_of(A, p0);
+      return SEL || !use_tma ? 0 : min(s.u1 - u, min(s.span.n - (int)p0, A.N - first) / kTrKeys);
+    };
+    auto load = [&](const CUtensorMap* map, uint8_t* tile, uint64_t* full, int first) {
+      mbar_expect_tx(full, kTrTile);
+      tma_load_4d(tile, map, full, 0, first, s.kvh, s.b);
+      tma_load_4d(tile + kTrHalf, map, full, 64, first, s.kvh, s.b);
+    };
+    auto send_k = [&](int u, uint32_t tile, int first) {
+      const uint32_t st = tile & 1;
+      if (!wait_bar(&S.k_empty[st], ((tile >> 1) & 1u) ^ 1u, alive, A)) return;
+      S.meta[tile % kTrRing] = make_int2(u, u + 1 == s.u1 ? last_flags : seg_flags);
+      load(&kmap, S.k[st], &S.k_full[st], first);
+      k_loads = tile + 1;
+    };
+    bool k_sent = false;  // the first tile's K is on its way
+    if (!SEL && s.u0 >= s.span.draft_tiles) {
+      int first;
+      k_sent = tma_run(s.u0, first) > 0;
+      if (k_sent && lt == 0) send_k(s.u0, it, first);
+    }
     // ---- the query rows (the previous segment's products are done with the buffer) ----
     {
       const bool free = segs == 0 || wait_bar(&S.q_free, (segs - 1) & 1u, alive, A);
@@ -547,7 +570,8 @@ RTP_DEVICE void tree_load(Smem& S, const CUtensorMap& kmap, const CUtensorMap& v
       if (lt == 0) {
         S.seg[segs % kTrRing] = info;
         if (s.u0 == 0 && place.rb == 0)
-          W.table[s.b * A.Hk + s.kvh] = make_int2(place.range, (s.base + s.span.tiles - 1) / place.per - place.range + 1);
+          W.table[s.b * A.Hk + s.kvh] =
+              make_int2(place.range, (s.base + s.span.tiles - 1) / place.per - place.range + 1);
       }
       ++segs;
     }
@@ -561,28 +585,15 @@ RTP_DEVICE void tree_load(Smem& S, const CUtensorMap& kmap, const CUtensorMap& v
       });
     if (!ok || s.u1 <= s.span.draft_tiles) continue;
     if constexpr (!SEL) {
-      auto load = [&](const CUtensorMap* map, uint8_t* tile, uint64_t* full, int first) {
-        mbar_expect_tx(full, kTrTile);
-        tma_load_4d(tile, map, full, 0, first, s.kvh, s.b);
-        tma_load_4d(tile + kTrHalf, map, full, 64, first, s.kvh, s.b);
-      };
 #pragma unroll 1
       for (int u = max(s.u0, s.span.draft_tiles); u < s.u1 && ok;) {
         const uint32_t p0 = (uint32_t)s.span.lo + (uint32_t)(u - s.span.draft_tiles) * kTrKeys;
         const int left = s.span.n - (int)p0;  // committed rows from here on
-        const int first = row_of(A, p0);
-        // whole tiles of neighbouring rows come by TMA, by one thread
-        const int run = use_tma ? min(s.u1 - u, min(left, A.N - first) / kTrKeys) : 0;
-        if (run > 0) {
-          // the next tile's K goes before this one's V: scores are computed ahead of the products with V
-          auto send_k = [&](int i) {
-            const uint32_t tile = it + i, st = tile & 1;
-            if (!wait_bar(&S.k_empty[st], ((tile >> 1) & 1u) ^ 1u, alive, A)) return;
-            S.meta[tile % kTrRing] = make_int2(u + i, u + i + 1 == s.u1 ? last_flags : seg_flags);
-            load(&kmap, S.k[st], &S.k_full[st], first + i * kTrKeys);
-            k_loads = tile + 1;
-          };
-          if (lt == 0) send_k(0);
+        int first;
+        const int run = tma_run(u, first);
+        if (run > 0) {  // by one thread
+          if (lt == 0 && !k_sent) send_k(u, it, first);
+          k_sent = false;
           if (q_due) {
             cp_wait<0>();
             landed(nullptr);
@@ -590,7 +601,8 @@ RTP_DEVICE void tree_load(Smem& S, const CUtensorMap& kmap, const CUtensorMap& v
           if (lt == 0) {
 #pragma unroll 1
             for (int i = 0; i < run && alive; ++i) {
-              if (i + 1 < run) send_k(i + 1);
+              // the next tile's K goes before this one's V: scores are computed ahead of the products with V
+              if (i + 1 < run) send_k(u + i + 1, it + i + 1, first + (i + 1) * kTrKeys);
               const uint32_t tile = it + i, st = tile & 1;
               if (!wait_bar(&S.v_empty[st], ((tile >> 1) & 1u) ^ 1u, alive, A)) break;
               load(&vmap, S.v[st], &S.v_full[st], first + i * kTrKeys);
