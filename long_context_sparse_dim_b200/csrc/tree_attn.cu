@@ -659,11 +659,11 @@ struct TrSum {
     o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
   }
 };
-RTP_DEVICE TrSum join_pieces(const TrParts& W, int2 pieces, int rb, int c, int part, int step) {
+RTP_DEVICE TrSum join_pieces(const TrParts& W, int grp, int2 pieces, int rb, int c, int part, int step) {
   TrSum sum;
   const int lane = threadIdx.x & 31;
-  const int64_t slot0 = (int64_t)rb * 2 * W.ranges;
-  auto at = [&](int i) { return (slot0 + 2 * (pieces.x + i) + (i == 0)) * W.nr + c; };
+  const int64_t slot0 = W.chunks ? ((int64_t)grp * W.rbs + rb) * W.chunks : ((int64_t)rb * W.ranges + pieces.x) * 2;
+  auto at = [&](int i) { return (slot0 + (W.chunks ? i : 2 * i + (i == 0))) * W.nr + c; };
   constexpr int kUnroll = 4;
 #pragma unroll 1
   for (int i = part; i < pieces.y; i += step * kUnroll) {
@@ -695,16 +695,16 @@ __global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const __grid_
   constexpr int kWarps = kTrJoinThreads / 32;
   __shared__ float4 so[kWarps][32];
   __shared__ float2 sml[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % WPR;
+  const uint32_t rows = A.G * A.T, x = blockIdx.x * (kWarps / WPR) + warp / WPR;
+  const bool have = x < rows * A.B * A.Hk;
+  const int grp = have ? x / rows : 0, r = have ? x % rows : 0;
   pdl_wait();
   pdl_release();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % WPR;
-  const int64_t rows = (int64_t)A.G * A.T, x = (int64_t)blockIdx.x * (kWarps / WPR) + warp / WPR;
-  const bool have = x < rows * A.B * A.Hk;
-  const int grp = have ? (int)(x / rows) : 0, r = have ? (int)(x % rows) : 0;
   const int2 pieces = have ? W.table[grp] : make_int2(0, 1);
   const bool join = pieces.y > 1;  // (one piece: its CTA has written the output)
   TrSum sum;
-  if (join) sum = join_pieces(W, pieces, r / W.nr, r % W.nr, part, WPR);
+  if (join) sum = join_pieces(W, grp, pieces, r / W.nr, r % W.nr, part, WPR);
   if (WPR > 1) {
     so[warp][lane] = sum.o;
     if (lane == 0) sml[warp] = make_float2(sum.m, sum.l);
@@ -724,26 +724,45 @@ __global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const __grid_
 }
 
 // ---- layout of the workspace -------------------------------------------------------------
+// CTAs (row blocks x tiles of 64 keys) up to which the small form is taken: three to an SM, fewer than can be there at
+// once.  It against the persistent forms, launches back to back: 8 groups x 18 tiles x 32 rows 11.4 us and 19.0, 8 x 34
+// x 64 rows 16.5 and 19.7, 64 x 6 x 64 rows 16.7 and 20.0, 24 x 18 x 64 rows 17.5 and 22.7; beyond, 8 x 65 x 64 rows
+// 23.1 and 19.5.
+constexpr int kSmallCtas = 148 * 3;
+
 struct TrLayout {
-  int nr, rbs, ranges;  // rows per CTA, row blocks per KV head, ranges of the line of tiles
+  int nr, rbs, ranges;       // rows per CTA, row blocks per KV head, ranges of the line of tiles
+  int chunks;                // small form: tiles of 64 keys; else 0
   size_t table, o, ml, tot;  // byte sizes
   size_t bytes() const { return table + o + ml + tot; }
 };
 
-TrLayout tree_layout(int64_t B, int64_t Hq, int64_t T, int64_t Hk, bool sel) {
+// keys: committed keys that a sequence can have in reach
+TrLayout tree_layout(int64_t B, int64_t Hq, int64_t T, int64_t Hk, int64_t keys, bool sel) {
   TrLayout L;
-  const int64_t rows = Hq / Hk * T;
-  // 64 rows go with the keys on the tensor core's lanes; more rows fill the lanes themselves, 256 to a CTA so that
-  // the keys are read once for them.  (A selection gathers its keys for 64 rows at a time: their union is smaller.)
-  L.nr = sel || rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
-  L.rbs = (int)((rows + L.nr - 1) / L.nr);
-  L.ranges = L.rbs >= kTrSms ? 1 : kTrSms / L.rbs;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  L.table = up((size_t)(B * Hk) * sizeof(int2));
-  const size_t slots = (size_t)L.rbs * L.ranges * 2 * L.nr;
+  const int64_t rows = Hq / Hk * T, groups = B * Hk;
+  L.table = up((size_t)groups * sizeof(int2));
+  L.tot = 0;
+  L.chunks = L.ranges = 0;
+  size_t slots;
+  const int64_t small_rbs = (rows + 63) / 64, small_tiles = (T + 63) / 64 + keys / 64 + 2;
+  if (groups * small_rbs <= kSmallCtas && groups * small_rbs * small_tiles <= kSmallCtas) {
+    L.nr = 64;
+    L.rbs = (int)small_rbs;
+    L.chunks = (int)small_tiles;
+    slots = (size_t)(groups * small_rbs) * L.chunks * 64;
+  } else {
+    // 64 rows go with the keys on the tensor core's lanes; more rows fill the lanes themselves, 256 to a CTA so that
+    // the keys are read once for them.  (A selection gathers its keys for 64 rows at a time: their union is smaller.)
+    L.nr = sel || rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
+    L.rbs = (int)((rows + L.nr - 1) / L.nr);
+    L.ranges = L.rbs >= kTrSms ? 1 : kTrSms / L.rbs;
+    slots = (size_t)L.rbs * L.ranges * 2 * L.nr;
+    if (L.nr > 64) L.tot = (size_t)L.rbs * L.ranges * 2 * 128 * kHeadDim * sizeof(float);
+  }
   L.o = up(slots * kHeadDim * sizeof(float));
   L.ml = up(slots * sizeof(float2));
-  L.tot = L.nr > 64 ? (size_t)L.rbs * L.ranges * 2 * 128 * kHeadDim * sizeof(float) : 0;
   return L;
 }
 
@@ -768,15 +787,24 @@ cudaError_t launch_join(const TreeAttnArgs& a, const TrParts& w, cudaStream_t st
 
 }  // namespace
 
+// The most that a call of these sizes takes, whatever its window or selection.
 size_t tree_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t T, int64_t Hk, int64_t N) {
-  (void)N;
-  const size_t plain = tree_layout(B, Hq, T, Hk, false).bytes(), sel = tree_layout(B, Hq, T, Hk, true).bytes();
-  return plain > sel ? plain : sel;
+  const size_t plain = tree_layout(B, Hq, T, Hk, N, false).bytes(), sel = tree_layout(B, Hq, T, Hk, N, true).bytes();
+  size_t most = plain > sel ? plain : sel;
+  // (a window may bring a call into the small form)
+  const int64_t rbs = (Hq / Hk * T + 63) / 64;
+  if (B * Hk * rbs <= kSmallCtas) {
+    const size_t slots = (size_t)kSmallCtas * 64;
+    const size_t small = (size_t)(B * Hk) * sizeof(int2) + slots * (kHeadDim * sizeof(float) + sizeof(float2)) + 1024;
+    if (small > most) most = small;
+  }
+  return most;
 }
 
 cudaError_t launch_tree_attn(const TreeAttnArgs& a, cudaStream_t stream) {
   if ((int64_t)a.B * a.Hq * a.T == 0) return cudaSuccess;
-  const TrLayout L = tree_layout(a.B, a.Hq, a.T, a.Hk, a.sel != nullptr);
+  const int64_t keys = a.W > 0 && a.W < a.N ? a.W : a.N;
+  const TrLayout L = tree_layout(a.B, a.Hq, a.T, a.Hk, keys, a.sel != nullptr);
   TrParts w;
   char* ws = static_cast<char*>(a.ws);
   w.table = reinterpret_cast<int2*>(ws);
@@ -786,19 +814,25 @@ cudaError_t launch_tree_attn(const TreeAttnArgs& a, cudaStream_t stream) {
   w.nr = L.nr;
   w.rbs = L.rbs;
   w.ranges = L.ranges;
+  w.chunks = L.chunks;
   // strides that the tensor map's encoder refuses (0 in a dim of several rows): every tile by cp.async
   CUtensorMap kmap{}, vmap{};
-  const int use_tma = !a.sel && a.N >= kTrKeys && make_row_map(&kmap, a.k, a.B, a.Hk, a.N, kTrKeys) &&
+  const int use_tma = !L.chunks && !a.sel && a.N >= kTrKeys && make_row_map(&kmap, a.k, a.B, a.Hk, a.N, kTrKeys) &&
                       make_row_map(&vmap, a.v, a.B, a.Hk, a.N, kTrKeys);
-  const cudaError_t e = a.sel          ? launch_tiles<true>(kmap, vmap, a, w, 0, stream)
+  const cudaError_t e = L.chunks       ? launch_tree_attn_small(a, w, L.chunks, stream)
+                        : a.sel      ? launch_tiles<true>(kmap, vmap, a, w, 0, stream)
                         : L.nr == 64 ? launch_tiles<false>(kmap, vmap, a, w, use_tma, stream)
                                      : launch_tree_attn_wide(kmap, vmap, a, w, use_tma, stream);
   if (e != cudaSuccess) return e;
-  // about this many pieces in a group; one warp per row takes four at a time
+  // About this many pieces in a group.  A warp takes four at a time, and every further warp per row costs, too: 18
+  // pieces of 256 rows in the small form take 11.4 us with two warps per row, 12.4 with four; 6 pieces 8.5 with one
+  // warp, 11.6 with four.
   const int64_t tiles = (a.T + kTrKeys - 1) / kTrKeys + a.N / kTrKeys + 1;
-  const int64_t most = L.ranges / ((int64_t)a.B * a.Hk) + 1, pieces = most < tiles ? most : tiles;
-  if (pieces <= 4) return launch_join<1>(a, w, stream);
-  if (pieces <= 16) return launch_join<4>(a, w, stream);
+  const int64_t most = (int64_t)L.ranges / ((int64_t)a.B * a.Hk) + 1;
+  const int64_t pieces = L.chunks ? L.chunks : most < tiles ? most : tiles;
+  if (pieces <= 8) return launch_join<1>(a, w, stream);
+  if (L.chunks && pieces <= 24) return launch_join<2>(a, w, stream);
+  if (pieces <= 40) return launch_join<4>(a, w, stream);
   return launch_join<8>(a, w, stream);
 }
 

@@ -9,16 +9,19 @@
 
 namespace rtp {
 
-// Parts of the workspace that the kernels use.  A piece of a group lies in slot 2 range + (1 if it begins the group).
+// Parts of the workspace that the kernels use.  A piece of a group lies in slot 2 range + (1 if it begins the group);
+// in the small form (chunks > 0) tile c of a group's row block in slot (group * rbs + row block) * chunks + c.
 struct TrParts {
   int2* table;  // [B * Hk] first range and number of pieces
   float* o;     // [row block][2 * ranges][nr][128]
   float2* ml;   // [row block][2 * ranges][nr] m and l, the sum of 2^logit being 2^m l; o is normalised
   float4* tot;  // [CTA][stream][32][128] totals of the wide form: four dims of a row each
   int nr, rbs, ranges;
+  int chunks;         // small form: tiles of 64 keys per group at most; 0 in the other forms
 };
 
-// The wide form (w.nr: 128 or 256 rows per CTA).
+// The small form, and the wide form (w.nr: 128 or 256 rows per CTA).
+cudaError_t launch_tree_attn_small(const TreeAttnArgs& a, const TrParts& w, int tiles, cudaStream_t stream);
 cudaError_t launch_tree_attn_wide(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeAttnArgs& a,
                                   const TrParts& w, int use_tma, cudaStream_t stream);
 
