@@ -196,7 +196,7 @@ RTP_API rtp_status rtp_kv_append(const rtp_tensor* k_new, const rtp_tensor* v_ne
  *   path    int32[B, A] device: accepted rows in order, each in [0, T); a step
  *           whose row is outside [0, T) writes nothing (its position keeps what
  *           it held)
- *   A       columns of path, >= 0
+ *   A       columns of path, >= 0 (0: path may be NULL)
  *   count   int32[B] device, clamped to [0, A]; 0 leaves the caches as they are
  *           and still writes the lengths
  * Errors as rtp_kv_append, plus INVALID_ARG for a NULL path or count, A < 0, or

@@ -319,7 +319,7 @@ rtp_status rtp_kv_accept(const rtp_tensor* k_new, const rtp_tensor* v_new, const
   if ((s = check_kv_append(k_new, v_new, pos, R, P, k_cache, v_cache, k_idx, k_ring, v_ring, lens_out, ring_lens,
                            &a)) != RTP_OK)
     return s;
-  if (!path || !count || A < 0) return RTP_ERR_INVALID_ARG;
+  if ((!path && A > 0) || !count || A < 0) return RTP_ERR_INVALID_ARG;
   const void* written[2] = {lens_out, ring_lens};
   for (const void* w : written)
     if (w && (w == path || w == count)) return RTP_ERR_INVALID_ARG;
@@ -637,9 +637,9 @@ rtp_status rtp_tree_attn(const rtp_tensor* q, const rtp_tensor* k, const rtp_ten
   if (q->dtype != RTP_BF16 || k_new->dtype != RTP_BF16) return RTP_ERR_DTYPE;  // tensor-core tiles
   const int64_t B = q->shape[0], Hq = q->shape[1], T = q->shape[2], Hk = k->shape[1], N = k->shape[2];
   if (k_new->shape[0] != B || k_new->shape[1] != Hk || k_new->shape[2] != T) return RTP_ERR_SHAPE;
-  if (!tree || !tree->mask) return RTP_ERR_INVALID_ARG;
+  if (!tree || (!tree->mask && B * T > 0)) return RTP_ERR_INVALID_ARG;
   if (tree->mask_words < (T + 31) / 32) return RTP_ERR_SHAPE;
-  if (W < 0 || (W > 0 && !tree->depth)) return RTP_ERR_INVALID_ARG;
+  if (W < 0 || (W > 0 && !tree->depth && B * T > 0)) return RTP_ERR_INVALID_ARG;
   if (ring != 0 && ring != 1) return RTP_ERR_INVALID_ARG;
   // a ring holds the last N tokens: the window must lie inside it, and selections name positions, not its rows
   if (ring && (W < 1 || W > N || sel)) return RTP_ERR_INVALID_ARG;
