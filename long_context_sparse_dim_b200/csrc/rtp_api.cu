@@ -646,6 +646,7 @@ rtp_status rtp_tree_attn(const rtp_tensor* q, const rtp_tensor* k, const rtp_ten
   if (sel && !sel->mask) return RTP_ERR_INVALID_ARG;
   if (sel && sel->mask_words < (N + 31) / 32) return RTP_ERR_SHAPE;
   if (B * Hk > INT32_MAX / 8 || Hq * T > INT32_MAX / 8) return RTP_ERR_UNSUPPORTED;
+  if (B * Hq * T > INT32_MAX) return RTP_ERR_UNSUPPORTED;  // (rows are numbered with 32 bits)
   // the kernel numbers its tiles of 128 keys (and of drafts) with 32 bits, with a range's length to spare
   if (B * Hk * (T / 128 + N / 128 + 3) > INT32_MAX / 2) return RTP_ERR_UNSUPPORTED;
   const size_t need = rtp_tree_attn_workspace_size(B, Hq, T, Hk, N);

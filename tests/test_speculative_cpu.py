@@ -96,6 +96,14 @@ def test_tree_attn_refusals():
     assert _tree_attn(k=d([2, 2, 64, 128], data=0x10004)) == 4
 
 
+def test_tree_attn_refuses_more_rows_than_it_numbers():
+    rtp = _lib()
+    d = lambda *a, **kw: _desc(rtp, *a, **kw)  # noqa: E731
+    B, T = 1 << 16, 1 << 13
+    assert _tree_attn(q=d([B, 4, T, 128]), o=d([B, 4, T, 128]), k=d([B, 1, 64, 128]), kn=d([B, 1, T, 128]),
+                      words=T // 32) == 7
+
+
 def test_tree_attn_workspace_is_checked():
     rtp = _lib()
     need = rtp.tree_attn_workspace_size(2, 8, 5, 2, 64)
