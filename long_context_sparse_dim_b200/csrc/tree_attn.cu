@@ -395,12 +395,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         for (int i = warp & 7; i < 32; i += 8) {
           const int c = (i & 15) + 32 * (i >> 4) + 16 * x;  // (the rows whose columns were this stream's)
           if (c >= nrows) continue;
-          float4 y = reinterpret_cast<const float4*>(scratch)[c * 32 + lane];
+          const float4 y = reinterpret_cast<const float4*>(scratch)[c * 32 + lane];
           if (info.slot >= 0) {
             part[c * 32] = y;
           } else {
             const int at = S.row_at[c];
-            if (__any_sync(0xffffffffu, !finite4(y))) scalar_row(A, info.b, info.kvh * A.G + (at & 7), at >> 3, y);
             store4(A, o_seg + (at & 7) * A.o.sh + (at >> 3) * A.o.sn + 4 * lane, y);
           }
         }
@@ -686,6 +685,56 @@ RTP_DEVICE TrSum join_pieces(const TrParts& W, int grp, int2 pieces, int rb, int
   return sum;
 }
 
+RTP_DEVICE bool finite4(const float4& y) {
+  return isfinite(y.x) && isfinite(y.y) && isfinite(y.z) && isfinite(y.w);
+}
+
+// ---- the scalar pass ------------------------------------------------------------------
+// One warp computes one row from the definition.
+__device__ __noinline__ void scalar_row(const TreeAttnArgs& A, int b, int h, int t, float4& out) {
+  const int lane = threadIdx.x & 31, kvh = h / A.G;
+  auto row = [&](const View4& x, int head, int64_t r) {
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(x.data) + b * x.sb +
+                                                         head * x.sh + r * x.sn + 4 * lane));
+    return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+  };
+  const float4 q = row(A.q, h, t);
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto take = [&](const float4 k, const float4 v) {
+    const float s = warp_sum(q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w) * A.scale_log2;
+    const float mn = fmaxf(m, s);
+    const float al = mn == -INFINITY ? 1.f : ex2a(m - mn), p = mn == -INFINITY ? 0.f : ex2a(s - mn);
+    m = mn;
+    l = l * al + p;
+    o = make_float4(o.x * al + p * v.x, o.y * al + p * v.y, o.z * al + p * v.z, o.w * al + p * v.w);
+  };
+  const int n = committed(A, b), depth = draft_depth(A, b, t);
+  const int lo = A.W > 0 ? max(0, n - 1 - oldest_age(A, depth)) : 0;  // (past n when the window holds none)
+  const uint32_t* sel = A.sel ? A.sel + ((int64_t)(b * A.Hq + h) * A.T + t) * A.sel_words : nullptr;
+  if (A.W <= 0 || oldest_age(A, depth) >= 0)
+#pragma unroll 1
+    for (int p = lo; p < n; ++p) {
+      if (sel && !((__ldg(sel + (p >> 5)) >> (p & 31)) & 1u)) continue;
+      const int r = row_of(A, (uint32_t)p);
+      take(row(A.k, kvh, r), row(A.v, kvh, r));
+    }
+#pragma unroll 1
+  for (int j = 0; j < A.T; ++j) {
+    if (!tree_bit(A, b, t, j)) continue;
+    if (A.W > 0 && draft_depth(A, b, j) <= depth - A.W) continue;
+    take(row(A.kn, kvh, j), row(A.vn, kvh, j));
+  }
+  const float inv = l != 0.f ? 1.f / l : 0.f;  // (a NaN stays one)
+  out = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+}
+
+RTP_DEVICE float4 load4(const TreeAttnArgs& A, int64_t off) {
+  if (!A.o_bf16) return __ldcg(reinterpret_cast<const float4*>(static_cast<const float*>(A.o.data) + off));
+  const uint2 w = __ldcg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(A.o.data) + off));
+  return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+}
+
 // Joins the pieces of groups that several CTAs worked on: WPR warps per query row, pieces in turn, four
 // head dims per lane.
 constexpr int kTrJoinThreads = 256;
@@ -702,7 +751,7 @@ __global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const __grid_
   pdl_wait();
   pdl_release();
   const int2 pieces = have ? W.table[grp] : make_int2(0, 1);
-  const bool join = pieces.y > 1;  // (one piece: its CTA has written the output)
+  const bool join = pieces.y > 1;  // (one piece: its CTA has written the output, not finite where it could not)
   TrSum sum;
   if (join) sum = join_pieces(W, grp, pieces, r / W.nr, r % W.nr, part, WPR);
   if (WPR > 1) {
@@ -716,11 +765,14 @@ __global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const __grid_
 #pragma unroll
     for (int w = 0; w < WPR; ++w) sum.take(sml[warp + w].x, sml[warp + w].y, 1.f, so[warp + w][lane]);
   }
-  if (!join) return;
-  sum.finish();
+  if (!have) return;
   const int b = grp / A.Hk, h = grp % A.Hk * A.G + r / A.T, t = r % A.T;
-  if (__any_sync(0xffffffffu, !finite4(sum.o))) scalar_row(A, b, h, t, sum.o);
-  store4(A, b * A.o.sb + h * A.o.sh + t * A.o.sn + 4 * lane, sum.o);
+  const int64_t at = b * A.o.sb + h * A.o.sh + t * A.o.sn + 4 * lane;
+  if (join) sum.finish();
+  else sum.o = load4(A, at);
+  const bool anew = __any_sync(0xffffffffu, !finite4(sum.o));
+  if (anew) scalar_row(A, b, h, t, sum.o);
+  if (anew | join) store4(A, at, sum.o);
 }
 
 // ---- layout of the workspace -------------------------------------------------------------

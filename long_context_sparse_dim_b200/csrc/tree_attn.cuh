@@ -256,56 +256,12 @@ struct TrWalk {
   }
 };
 
-// ---- the scalar pass ------------------------------------------------------------------
-// One warp computes one row from the definition.
-__device__ __noinline__ void scalar_row(const TreeAttnArgs& A, int b, int h, int t, float4& out) {
-  const int lane = threadIdx.x & 31, kvh = h / A.G;
-  auto row = [&](const View4& x, int head, int64_t r) {
-    const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(x.data) + b * x.sb +
-                                                         head * x.sh + r * x.sn + 4 * lane));
-    return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
-  };
-  const float4 q = row(A.q, h, t);
-  float m = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto take = [&](const float4 k, const float4 v) {
-    const float s = warp_sum(q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w) * A.scale_log2;
-    const float mn = fmaxf(m, s);
-    const float al = mn == -INFINITY ? 1.f : ex2a(m - mn), p = mn == -INFINITY ? 0.f : ex2a(s - mn);
-    m = mn;
-    l = l * al + p;
-    o = make_float4(o.x * al + p * v.x, o.y * al + p * v.y, o.z * al + p * v.z, o.w * al + p * v.w);
-  };
-  const int n = committed(A, b), depth = draft_depth(A, b, t);
-  const int lo = A.W > 0 ? max(0, n - 1 - oldest_age(A, depth)) : 0;  // (past n when the window holds none)
-  const uint32_t* sel = A.sel ? A.sel + ((int64_t)(b * A.Hq + h) * A.T + t) * A.sel_words : nullptr;
-  if (A.W <= 0 || oldest_age(A, depth) >= 0)
-#pragma unroll 1
-    for (int p = lo; p < n; ++p) {
-      if (sel && !((__ldg(sel + (p >> 5)) >> (p & 31)) & 1u)) continue;
-      const int r = row_of(A, (uint32_t)p);
-      take(row(A.k, kvh, r), row(A.v, kvh, r));
-    }
-#pragma unroll 1
-  for (int j = 0; j < A.T; ++j) {
-    if (!tree_bit(A, b, t, j)) continue;
-    if (A.W > 0 && draft_depth(A, b, j) <= depth - A.W) continue;
-    take(row(A.kn, kvh, j), row(A.vn, kvh, j));
-  }
-  const float inv = l != 0.f ? 1.f / l : 0.f;  // (a NaN stays one)
-  out = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-}
-
 RTP_DEVICE void store4(const TreeAttnArgs& A, int64_t off, const float4& y) {
   if (A.o_bf16)
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(A.o.data) + off) =
         make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
   else
     *reinterpret_cast<float4*>(static_cast<float*>(A.o.data) + off) = y;
-}
-
-RTP_DEVICE bool finite4(const float4& y) {
-  return isfinite(y.x) && isfinite(y.y) && isfinite(y.z) && isfinite(y.w);
 }
 
 // The part of a CTA's shared memory through which its loaders feed it: NR query rows, two stages of K and V,

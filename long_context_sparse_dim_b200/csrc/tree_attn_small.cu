@@ -164,8 +164,8 @@ tree_attn_small_kernel(const __grid_constant__ TreeAttnArgs A, const __grid_cons
       uint64_t bits = j0 < A.T ? __ldg(words + (j0 >> 5)) : 0u;
       if (KW == 64 && j0 + 32 < A.T) bits |= (uint64_t)__ldg(words + (j0 >> 5) + 1) << 32;
       in &= bits >> sh;
-      if (A.W > 0) {
-        const int depth = draft_depth(A, b, t_row[h]);
+      const int depth = A.W > 0 ? draft_depth(A, b, t_row[h]) : 0;
+      if (A.W > 0 && depth >= A.W) {  // (below it the window holds every draft)
 #pragma unroll 1
         for (int j = 0; j < KW && j < left; ++j)
           if (draft_depth(A, b, p0 + j) <= depth - A.W) in &= ~(1ull << j);
@@ -274,13 +274,12 @@ tree_attn_small_kernel(const __grid_constant__ TreeAttnArgs A, const __grid_cons
   const int64_t slot = ((int64_t)blockIdx.y * gridDim.x + u) * kSmRows;
 #pragma unroll 2
   for (int r = warp; r < nrows; r += 4) {
-    float4 y = reinterpret_cast<const float4*>(acc)[r * 32 + lane];
+    const float4 y = reinterpret_cast<const float4*>(acc)[r * 32 + lane];
     if (tiles > 1) {
       reinterpret_cast<float4*>(W.o)[(slot + r) * 32 + lane] = y;
       if (lane == 0) W.ml[slot + r] = S.row_ml[r];
     } else {
       const int g = (row0 + r) / A.T, t = row0 + r - g * A.T, h = kvh * A.G + g;
-      if (__any_sync(0xffffffffu, !finite4(y))) scalar_row(A, b, h, t, y);
       store4(A, b * A.o.sb + h * A.o.sh + t * A.o.sn + 4 * lane, y);
     }
   }

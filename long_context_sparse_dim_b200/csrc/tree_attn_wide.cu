@@ -42,7 +42,6 @@ struct TrWideSmem : TrFeed<kWideRows * kBlocks, false> {
   int4 cur[2];                   // each stream's scores: tile (-1: no more), and its meta
   int new_epoch[2];
   int raise[2][2];               // some sum has grown too large (alternating looks)
-  uint32_t bad[2][kWideRows / 32];  // rows with a result that is not finite
   int state[2];                  // at a segment's end: 1 the stream has an O, 2 and a total
   uint32_t tmem_base;
 };
@@ -76,7 +75,6 @@ tree_attn_wide_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
     }
     mbar_init(&S.fin, 1);
   }
-  if (tid < 2 * kWideRows / 32) S.bad[0][tid] = 0u;
   tree_feed_init(S, A, place, kmap, vmap, use_tma);
   if (warp == 0) tmem_alloc(&S.tmem_base, kTmemColsW);
   pdl_wait();
@@ -303,7 +301,6 @@ tree_attn_wide_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
         if (info.slot >= 0 && live && half == 0 && (!kShared || x == 0)) W.ml[slot_row] = make_float2(m, all);
         // 16 dims at a time: the thread's 64, or 32 of them when the streams share the rows
         const int64_t off = info.b * A.o.sb + (int64_t)(info.kvh * A.G + (at & 7)) * A.o.sh + t * A.o.sn;
-        bool bad = false;
 #pragma unroll 1
         for (int i = 0; i < (kShared ? 2 : 4) && act; ++i) {
           const int d0 = kShared ? 32 * x + 16 * i : 16 * i;  // past 64 * half
@@ -337,8 +334,6 @@ tree_attn_wide_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
 #pragma unroll
             for (int c = 0; c < 4; ++c) dst[c] = make_float4(y[4 * c], y[4 * c + 1], y[4 * c + 2], y[4 * c + 3]);
           } else {
-#pragma unroll
-            for (int c = 0; c < 16; ++c) bad = bad | !isfinite(y[c]);
             if (A.o_bf16) {
               uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(A.o.data) + off + d);
 #pragma unroll
@@ -358,24 +353,7 @@ tree_attn_wide_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
           wait_warp(&S.sum_free[x], (uint32_t)seg);
         }
         if (has) arrive_warp(&S.o_free[x]);
-        {
-          const uint32_t rows_bad = __ballot_sync(0xffffffffu, bad);
-          if (lane == 0 && rows_bad) atomicOr(&S.bad[x][quad], rows_bad);
-        }
         sync();
-        if (S.bad[x][0] | S.bad[x][1] | S.bad[x][2] | S.bad[x][3]) {
-#pragma unroll 1
-          for (int r = warp & 7; r < nrows; r += 8)
-            if ((S.bad[x][r >> 5] >> (r & 31)) & 1u) {
-              const int ra = S.row_at[base_row + r], h = info.kvh * A.G + (ra & 7);
-              float4 y;
-              scalar_row(A, info.b, h, ra >> 3, y);
-              store4(A, info.b * A.o.sb + h * A.o.sh + (ra >> 3) * A.o.sn + 4 * lane, y);
-            }
-          sync();
-          if (sc < kWideRows / 32) S.bad[x][sc] = 0u;
-          sync();
-        }
         l2 = 0ull;
         seen = has = has_total = false;
       }

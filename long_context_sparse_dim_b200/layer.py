@@ -471,6 +471,9 @@ class TreeDecodeLayer(CachedDecodeLayer):
         inv_freq, else normed and rotated; tree_mask int32 [B, T, words] (bit j of row
         t: token t attends draft j) and depth int32 [B, T] describe the trees.  With
         ``side_stream`` the local heads run there."""
+        for name, x, mine in (("q", q, self.tree_q), ("k", k, self.tree_k), ("v", v, self.tree_v)):
+            if x.shape != mine.shape:
+                raise ValueError(f"{name}: need {tuple(mine.shape)}, got {tuple(x.shape)}")
         main = torch.cuda.current_stream() if stream is None else stream
         R, RG, L = self.R, self.R * self.G, self.Hkv - self.R
         lens = self.lens

@@ -9,6 +9,7 @@ import pytest
 import torch
 
 from long_context_sparse_dim_b200 import rtp
+from long_context_sparse_dim_b200.layer import TreeDecodeLayer
 from test_speculative_gpu import (BF, D, _bits, _check_norm_rope, _check_tree, _freqs, _inputs, _norm_rope_ref,
                                   _run_tree, _tree_ref, _trees)
 
@@ -152,6 +153,34 @@ def test_tree_attn_nan_goes_where_it_is_attended(T, Hq, Hk, N):
         ref, tol = _tree_ref(q, k, v, lens, kn, vn, anc, depth, 0, False, None, SCALE)
         free = ~hit[..., None] | ~dims
         assert bool(((o.double() - ref).abs() <= tol)[free].all())
+
+
+@pytest.mark.parametrize("T,Hq,Hk,N", [(16, 16, 4, 500), (25, 20, 4, 500), (50, 32, 4, 300)])
+def test_tree_attn_rows_computed_anew_in_whole_groups(T, Hq, Hk, N):
+    """Groups that one CTA works on alone: a NaN among the drafts, and a reference far above all that is attended."""
+    B, G = 50, Hq // Hk
+    lens = [N - 3 * b for b in range(B)]
+    q, k, v, kn, vn = _inputs(B, Hq, Hk, N, T, 23, lens=lens)
+    one = torch.randn(D, generator=torch.Generator(device="cuda").manual_seed(4), device="cuda")
+    one /= one.norm()
+    q[1:] = (q[1:].float() * 0.3 + 6 * one).to(BF)
+    kn[1:, :, 0] = (2000 * one).to(BF)
+    anc, depth = _trees(B, T, "wide", 23)
+    anc[1:, 1:, 0] = False
+    anc[0, :, 2] = np.arange(T) % 3 == 2
+    bad_v = vn.clone()
+    bad_v[0, :, 2, 7] = float("nan")
+    for out in (F32, BF):
+        o = torch.empty(B, Hq, T, D, dtype=out, device="cuda")
+        ws = rtp.workspace(rtp.tree_attn_workspace_size(B, Hq, T, Hk, N), "cuda")
+        rtp.tree_attn(q, k, v, torch.tensor(lens, dtype=torch.int32, device="cuda"), kn, bad_v, _bits(anc), 0.25, o, ws)
+        torch.cuda.synchronize()
+        assert rtp.poll_device_error() == 0
+        assert bool(torch.isnan(o[0, :, 2::3, 7]).all())
+        o[0, :, 2::3, 7] = 0
+        ref, tol = _tree_ref(q, k, v, lens, kn, vn, anc, depth, 0, False, None, 0.25)
+        ref[0, :, 2::3, 7] = 0
+        _check_tree(o, ref, tol, "anew")
 
 
 @pytest.mark.parametrize("T,Hq,Hk,N", [(4, 8, 2, 700), (16, 16, 4, 9000), (25, 20, 4, 9000), (50, 16, 2, 9000)])
@@ -299,3 +328,14 @@ def test_tree_attn_of_nothing(B, T):
         rtp.tree_attn(q, cache, cache, None, kv, kv, mask, SCALE, torch.empty_like(q), rtp.workspace(0, "cuda"),
                       depth=mask[..., 0], W=W)
     torch.cuda.synchronize()
+
+
+def test_tree_step_refuses_other_shapes():
+    """Rows of another shape would be spread over the layer's drafts."""
+    layer = TreeDecodeLayer(2, 4, 2, 64, 1, 16, 0.9, torch.randn(1, 16, D, device="cuda"), 5)
+    q, kv = torch.zeros(2, 4, 5, D, dtype=BF, device="cuda"), torch.zeros(2, 2, 5, D, dtype=BF, device="cuda")
+    mask, depth = torch.zeros(2, 5, 1, dtype=torch.int32, device="cuda"), torch.zeros(2, 5, dtype=torch.int32, device="cuda")
+    for bad in ((q[:, :, :1], kv, kv), (q, kv[:, :1], kv), (q, kv, kv[:1])):
+        with pytest.raises(ValueError, match="need"):
+            layer.tree_step(*bad, mask, depth)
+    assert layer.tree_step(q, kv, kv, mask, depth).shape == q.shape
