@@ -418,11 +418,21 @@ RTP_DEVICE void tree_load(Smem& S, const CUtensorMap& kmap, const CUtensorMap& v
   auto copy_rows = [&](const View4& x, uint8_t* tile, const TrSeg& s, auto&& row_at) {
     const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(x.data) + s.b * x.sb + s.kvh * x.sh + chunk * 8;
     const uint32_t dst = smem_addr(tile) + slot_kv;
-#pragma unroll 2
-    for (int i = 0; i < 16; ++i) {
-      bool ok;
-      const int row = row_at(r_first + 8 * i, ok);
-      cp16(dst + 1024u * i, ok ? (const void*)(base + row * x.sn) : A.q.data, ok);
+    // (rows found some at a time: a copy keeps later looks at the shared memory behind it; with a selection there
+    // are no registers for it)
+    constexpr int kBatch = SEL ? 1 : 4;
+#pragma unroll SEL ? 2 : 1
+    for (int i0 = 0; i0 < 16; i0 += kBatch) {
+      int at[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        bool ok;
+        const int row = row_at(r_first + 8 * (i0 + i), ok);
+        at[i] = ok ? row : -1;
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        cp16(dst + 1024u * (i0 + i), at[i] >= 0 ? (const void*)(base + at[i] * x.sn) : A.q.data, at[i] >= 0);
     }
     cp_commit();
   };
@@ -602,29 +612,71 @@ RTP_DEVICE void tree_load(Smem& S, const CUtensorMap& kmap, const CUtensorMap& v
       // from all over the context (a prime larger than their number), since selected keys come in clusters
       uint32_t ahead[2][4];
       int next_key = 0;
-      auto fetch = [&](int u) {
-        const int i0 = u - s.span.draft_tiles;
-        const int round = (int)((uint64_t)i0 * 2654435761ull % (uint64_t)rounds);
+      // (a row's four words in one load where they lie so: every lane's row is another line, and four loads look
+      // each of them up four times: 8 x 32768 keys x 16 drafts 0.4 us)
+      const bool by_16 = ((reinterpret_cast<uintptr_t>(A.sel) & 15) | (A.sel_words & 3)) == 0;
+      const int i0 = max(s.u0 - s.span.draft_tiles, 0), step = rounds > 0 ? (int)(2654435761u % (uint32_t)rounds) : 0;
+      int round = rounds > 0 ? (int)((uint64_t)i0 * (uint32_t)step % (uint32_t)rounds) : 0;
+      auto fetch = [&] {
         next_key = s.span.lo + round * kTrRound + lw * 128;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const int wb = next_key + 32 * w, rem = s.span.n - wb;
+        for (int i = 0; i < 2; ++i) {
+          if (by_16) {
+            const uint4 x = words[i] && next_key < s.span.n
+                                ? __ldg(reinterpret_cast<const uint4*>(words[i] + (next_key >> 5)))
+                                : make_uint4(0u, 0u, 0u, 0u);
+            ahead[i][0] = x.x, ahead[i][1] = x.y, ahead[i][2] = x.z, ahead[i][3] = x.w;
+          } else {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) ahead[i][w] = words[i] && rem > 0 ? __ldg(words[i] + (wb >> 5)) : 0u;
+            for (int w = 0; w < 4; ++w) {
+              const int wb = next_key + 32 * w;
+              ahead[i][w] = words[i] && wb < s.span.n ? __ldg(words[i] + (wb >> 5)) : 0u;
+            }
+          }
         }
       };
-      fetch(max(s.u0, s.span.draft_tiles));
+      fetch();
+      // A gathered tile is handed on a round later: its rows are on their way meanwhile (with the shuffles
+      // below 8 x 32768 keys x 16 drafts 32.2 -> 30.5 us).
+      bool flying = false;
+      auto land = [&] {
+        if (!flying) return;
+        const int st = (it - 1) & 1;
+        cp_wait<1>();
+        landed(&S.k_full[st]);
+        cp_wait<0>();
+        landed(&S.v_full[st]);
+        k_loads = v_loads = it;
+        flying = false;
+      };
       auto emit = [&](int take, int flags) {
+        land();
         // one key per loader thread: its row bits for the softmax
         uint2 bits = make_uint2(0u, 0u);
         if (lt < take) bits = S.qbits[wrap(head + lt)];
         S.kmask[it & 3][0][lt] = bits.x;
         S.kmask[it & 3][1][lt] = bits.y;
-        const int at = head;
-        ok = gather(A.k, A.v, s, s.span.draft_tiles, flags, [&](int r, bool& live) {
-          live = r < take;
-          return live ? S.qkey[wrap(at + r)] : 0;
-        });
+        const int st = it & 1, r = r_first + 8 * (lane & 15);
+        const int mine = r < take ? S.qkey[wrap(head + r)] : -1;  // the row of this thread's copy lane % 16
+        auto copy_keys = [&](const View4& x, uint8_t* tile) {
+          const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(x.data) + s.b * x.sb + s.kvh * x.sh + chunk * 8;
+          const uint32_t dst = smem_addr(tile) + slot_kv;
+#pragma unroll 1
+          for (int i = 0; i < 16; ++i) {
+            const int row = __shfl_sync(0xffffffffu, mine, i, 16);
+            cp16(dst + 1024u * i, row >= 0 ? (const void*)(base + row * x.sn) : A.q.data, row >= 0);
+          }
+          cp_commit();
+        };
+        ok = stage_free(S.k_empty);
+        if (!ok) return;
+        if (lt == 0) S.meta[it % kTrRing] = make_int2(s.span.draft_tiles, flags);
+        copy_keys(A.k, S.k[st]);
+        ok = stage_free(S.v_empty);
+        if (!ok) return;
+        copy_keys(A.v, S.v[st]);
+        ++it;
+        flying = true;
         head = wrap(head + take);
         count -= take;
       };
@@ -636,7 +688,11 @@ RTP_DEVICE void tree_load(Smem& S, const CUtensorMap& kmap, const CUtensorMap& v
           x[0][w] = ahead[0][w];
           x[1][w] = ahead[1][w];
         }
-        if (u + 1 < s.u1) fetch(u + 1);
+        if (u + 1 < s.u1) {
+          round += step;
+          if (round >= rounds) round -= rounds;
+          fetch();
+        }
         int mine = 0;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
@@ -674,9 +730,11 @@ RTP_DEVICE void tree_load(Smem& S, const CUtensorMap& kmap, const CUtensorMap& v
         }
         count += all;
         named_sync(kBarLoad, kTrLoad);
+        land();
         while (count > kTrKeys && ok) emit(kTrKeys, seg_flags);
       }
       if (ok) emit(count, last_flags);
+      if (ok) land();
     }
   }
   cp_wait<0>();
