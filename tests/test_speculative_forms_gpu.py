@@ -112,7 +112,8 @@ def test_tree_attn_references(form, kind):
 
 @pytest.mark.parametrize("density", [0.0, 0.02, 1.0])
 @pytest.mark.parametrize("B,Hq,Hk,N,T,W", [(4, 16, 4, 9000, 16, 0), (3, 20, 4, 5001, 25, 0), (40, 4, 2, 1300, 8, 0),
-                                           (5, 8, 4, 4000, 16, 1100), (2, 8, 2, 12000, 40, 0), (2, 8, 2, 3500, 4, 50)])
+                                           (5, 8, 4, 4000, 16, 1100), (2, 8, 2, 12000, 40, 0), (2, 8, 2, 3500, 4, 50),
+                                           (4, 16, 4, 8192, 16, 0), (3, 8, 2, 12800, 20, 5000)])
 def test_tree_attn_selected_forms(B, Hq, Hk, N, T, W, density):
     rng = np.random.default_rng(B)
     lens = [int(x) for x in rng.integers(0, N + 1, B)]
