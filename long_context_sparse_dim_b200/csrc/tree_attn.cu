@@ -878,12 +878,13 @@ cudaError_t launch_tree_attn(const TreeAttnArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   // About this many pieces in a group.  A warp takes four at a time, and every further warp per row costs, too: 18
   // pieces of 256 rows in the small form take 11.4 us with two warps per row, 12.4 with four; 6 pieces 8.5 with one
-  // warp, 11.6 with four.
+  // warp, 11.6 with four; 11 pieces of 2025 rows in the wide form 24.1 with two, 25.3 with four; but 10 pieces of 1024
+  // rows of a selection 30.4 with four, 31.5 with two.
   const int64_t tiles = (a.T + kTrKeys - 1) / kTrKeys + a.N / kTrKeys + 1;
   const int64_t most = (int64_t)L.ranges / ((int64_t)a.B * a.Hk) + 1;
   const int64_t pieces = L.chunks ? L.chunks : most < tiles ? most : tiles;
   if (pieces <= 8) return launch_join<1>(a, w, stream);
-  if (L.chunks && pieces <= 24) return launch_join<2>(a, w, stream);
+  if (pieces <= 24 && (L.chunks || (int64_t)a.B * a.Hq * a.T > 1024)) return launch_join<2>(a, w, stream);
   if (pieces <= 40) return launch_join<4>(a, w, stream);
   return launch_join<8>(a, w, stream);
 }
