@@ -267,7 +267,7 @@ def test_tree_attn_on_two_streams():
         assert torch.equal(o, w)
 
 
-@pytest.mark.parametrize("T", [18950, 40001])
+@pytest.mark.parametrize("T", [7103, 7105, 18950, 40001])
 def test_norm_rope_many_rows(T):
     """Batches so large that a row has fewer lanes."""
     dev = "cuda"
