@@ -10,8 +10,16 @@
 // and o = sum_j softmax_j(scale * q.k_j) v_j over them (0 when there are none).
 // The committed rows lie by position, or in a ring: position p in row p mod N.
 //
-// Bound: HBM (each committed row once per KV head) up to about 128 query rows
-// per KV head (G heads x T drafts), the tensor cores above.
+// Three forms, chosen in tree_layout: this one for up to 64 query rows per KV head
+// (G heads x T drafts) and for selections, tree_attn_wide.cu for more rows,
+// tree_attn_small.cu for few keys.
+//
+// Bound: HBM (each committed row once per KV head) up to about 128 rows per KV
+// head, the tensor cores above, and the latency of a call's steps for less than
+// about 100 MB of keys.  Measured, launches back to back: 8 x 32768 keys x 8 KV
+// heads x 64 rows (1.07 GB) 155 us, 6.9 TB/s while tiles go through; 8 x 6 rings
+// of 4096 rows x 64 rows (100 MB) 42; 64 rows x 2 KV heads x 8 sequences that
+// select 8% of 32768 keys (20 MB) 30.4.
 //
 // Design (B200, tcgen05).  The query rows of a KV head go on the N side of both
 // products and the KEYS (then the head dims) on the M side, so that a tile
@@ -27,15 +35,14 @@
 //            exponent range, so any reference within 2^60 above and 2^80 below
 //            the row's maximum gives the same precision, and a tile needs no
 //            reduction over keys and no exchange between warps.  A row outside
-//            that range shows in its sum and goes the scalar way below.
+//            that range shows in its sum, and its result is made a NaN.
 //   O        is summed in TMEM over an epoch of 8 tiles (the tensor core
 //            truncates, so a long sum would drift), then added to a second TMEM
 //            tile by fp32 adds, and rescaled where references were raised.
 //   streams  two groups of 8 softmax warps, each with its own S, P, O and
-//            references for 64 rows, so that one exponentiates while the other
-//            waits, loads or stores.  Up to 64 rows the streams take every other
-//            tile of the same rows and their sums meet at the end; above, each
-//            takes 64 of a CTA's 128 rows of every tile.
+//            references for the same 64 rows, so that one exponentiates while
+//            the other waits, loads or stores.  They take tiles in turn, and
+//            their sums meet at the end.
 // Warps: 2 x 8 softmax, 4 loaders, 1 MMA issuer.  Interior tiles come by TMA
 // (128-byte swizzle), tiles with rows to leave out (past the end, a ring's seam,
 // drafts, selected keys) by 16-byte cp.async into the same layout, with zeros in
@@ -51,9 +58,9 @@
 // queues the keys that any row selected (a ballot per key transposes the bits:
 // the queue holds a key's row bits), and gathers only those, 128 to a tile.
 //
-// A row whose result is not finite, or whose sum has left its range, is computed
-// again by a scalar pass over the keys it attends (0 * inf in a product with
-// P = 0 must not reach it).
+// A row whose result is not finite is computed again by a scalar pass over the keys
+// it attends (0 * inf in a product with P = 0 must not reach it).  The joining
+// kernel does that: nothing waits on its warps, however long they take.
 #include "tree_attn.cuh"
 
 namespace rtp {
@@ -806,7 +813,10 @@ TrLayout tree_layout(int64_t B, int64_t Hq, int64_t T, int64_t Hk, int64_t keys,
     slots = (size_t)(groups * small_rbs) * L.chunks * 64;
   } else {
     // 64 rows go with the keys on the tensor core's lanes; more rows fill the lanes themselves, 256 to a CTA so that
-    // the keys are read once for them.  (A selection gathers its keys for 64 rows at a time: their union is smaller.)
+    // the keys are read once for them.  64 groups x 16384 keys: 64 rows 103 us this way and 120 with rows on the lanes,
+    // 70 rows 165 in two blocks this way and 112.  32 groups x 131072 keys x 256 rows: 850 us by 256, 885 by 128, 1220
+    // by 64; in smaller calls 256 and 128 are within 5%, either way, and 64 is ahead for very few groups (4 x 8192 keys
+    // x 128 rows: 23.6 and 28.0).  (A selection gathers its keys for 64 rows at a time: their union is smaller.)
     L.nr = sel || rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
     L.rbs = (int)((rows + L.nr - 1) / L.nr);
     L.ranges = L.rbs >= kTrSms ? 1 : kTrSms / L.rbs;

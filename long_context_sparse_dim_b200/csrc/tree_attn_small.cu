@@ -13,9 +13,10 @@
 // in registers; fp32 sums.  The tiles of a group are joined by the kernel that
 // joins the other forms' pieces.
 //
-// Bound by latency: 1000 keys x 8 drafts of 8 KV heads (5 MB) take 11.4 us,
+// Bound by latency: 1000 keys x 8 drafts of 8 KV heads (4 MB) take 11.1 us,
 // launches back to back, of which 7.5 are this kernel's and the rest the join's;
-// the persistent form takes 19.0.
+// the persistent form takes 19.0.  (One tile to a CTA: with several the CTAs are
+// fewer and larger, 11.8 us, and three of them fit on an SM, not two.)
 #include "tree_attn.cuh"
 
 namespace rtp {
