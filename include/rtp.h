@@ -406,7 +406,7 @@ RTP_API size_t rtp_window_attn_workspace_size(int64_t B, int64_t Hq, int64_t T, 
 #define RTP_DEVICE_ERR_TIMEOUT 1
 RTP_API rtp_status rtp_poll_device_error(int32_t* code);
 /* Budget, in GPU clock cycles, of each bounded device wait in the prefill
- * kernels launched after this call (process-wide).  0 restores the default
+ * and tree-attention kernels launched after this call (process-wide).  0 restores the default
  * (4e9 cycles, about two seconds); a negative value is RTP_ERR_INVALID_ARG.
  * A diagnostic knob: a tiny budget makes waits give up on purpose, which is
  * how the give-up path is tested; the results of such a launch are invalid,

@@ -757,7 +757,10 @@ __global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const __grid_
   const int grp = have ? x / rows : 0, r = have ? x % rows : 0;
   pdl_wait();
   pdl_release();
-  const int2 pieces = have ? W.table[grp] : make_int2(0, 1);
+  int2 pieces = have ? W.table[grp] : make_int2(0, 1);
+  // (a CTA that gave up a wait may have left the entry unwritten)
+  const int most = W.chunks ? W.chunks : W.ranges;
+  if (pieces.x < 0 || pieces.x >= most || pieces.y < 1 || pieces.y > most - pieces.x) pieces = make_int2(0, 1);
   const bool join = pieces.y > 1;  // (one piece: its CTA has written the output, not finite where it could not)
   TrSum sum;
   if (join) sum = join_pieces(W, grp, pieces, r / W.nr, r % W.nr, part, WPR);

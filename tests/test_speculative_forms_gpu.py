@@ -4,6 +4,10 @@ rows per KV head, with up to 128 and with more; selections; references that have
 move; workspaces and streams shared between them; long batches of rows and of
 accepted drafts.  Formulas and tolerances are those of test_speculative_gpu.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -340,3 +344,59 @@ def test_tree_step_refuses_other_shapes():
         with pytest.raises(ValueError, match="need"):
             layer.tree_step(*bad, mask, depth)
     assert layer.tree_step(q, kv, kv, mask, depth).shape == q.shape
+
+
+@pytest.mark.parametrize("shape", SHAPES[1:5])
+def test_tree_attn_wait_budget_runs_out(shape):
+    """Waits given up (a budget of a few cycles) are reported, read nothing that was not written for them, and leave
+    the next call as it should be."""
+    args, o, s, size = _call(*shape[:7], sel=shape[7] if len(shape) > 7 else None)
+    ws = rtp.workspace(size, "cuda")
+    rtp.tree_attn(*args, ws, sel=s)
+    torch.cuda.synchronize()
+    want = o.clone()
+    for fill in (255, 127, 0):
+        ws.fill_(fill)
+        try:
+            rtp.set_wait_budget_cycles(4)
+            rtp.tree_attn(*args, ws, sel=s)
+            torch.cuda.synchronize()
+        finally:
+            rtp.set_wait_budget_cycles(0)
+        assert rtp.poll_device_error() == 1
+        rtp.tree_attn(*args, ws, sel=s)
+        torch.cuda.synchronize()
+        assert rtp.poll_device_error() == 0
+        assert torch.equal(o, want)
+
+
+_FIRST = """
+import torch
+from long_context_sparse_dim_b200 import rtp
+D, dev = 128, "cuda"
+q, kv = torch.randn(1, 8, 16, D, device=dev).bfloat16(), torch.randn(1, 2, N, D, device=dev).bfloat16()
+new, mask = torch.randn(1, 2, 16, D, device=dev).bfloat16(), torch.full((1, 16, 1), 65535, dtype=torch.int32, device=dev)
+i, path = torch.zeros(1, dtype=torch.int32, device=dev), torch.arange(4, dtype=torch.int32, device=dev).view(1, 4)
+freq, o = torch.rand(64, dtype=torch.float64, device=dev), torch.zeros(1, 8, 16, D, device=dev)
+turned, ring = torch.zeros_like(q), torch.zeros(1, 2, 32, D, device=dev).bfloat16()
+ws = rtp.workspace(rtp.tree_attn_workspace_size(1, 8, 16, 2, N), dev)
+graph, st = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+torch.cuda.synchronize()
+with torch.cuda.graph(graph, stream=st):
+    rtp.qk_norm_rope(q, None, None, None, 1e-6, i, freq, turned, None, stream=st)
+    rtp.tree_attn(turned, kv, kv, None, new, new, mask, 0.1, o, ws, stream=st)
+    rtp.kv_accept(new, new, i, path, i + 4, 0, k_ring=ring, v_ring=ring.clone(), stream=st)
+graph.replay()
+torch.cuda.synchronize()
+got = o.clone()
+rtp.qk_norm_rope(q, None, None, None, 1e-6, i, freq, turned, None)
+rtp.tree_attn(turned, kv, kv, None, new, new, mask, 0.1, o, ws)
+torch.cuda.synchronize()
+assert torch.equal(got, o) and bool((got != 0).any()) and torch.equal(ring[0, :, :4], new[0, :, :4])
+"""
+
+
+@pytest.mark.parametrize("N", [500, 30000])
+def test_first_calls_of_a_process_are_captured(N):
+    subprocess.run([sys.executable, "-c", f"N = {N}\n" + _FIRST], check=True, timeout=300,
+                   cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
