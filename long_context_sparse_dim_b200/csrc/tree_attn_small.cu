@@ -10,7 +10,8 @@
 // each and, when R is below 64, share out the 64 keys, too (RG row groups x 4 /
 // RG key groups, met in shared memory at the end).  K and V rows come by 16-byte
 // cp.async with zeros in the rows that hold no token.  P as a bf16 hi + lo pair
-// in registers; fp32 sums.  The tiles of a group are joined by the kernel that
+// in registers (three terms, all 24 bits, for fp32 outputs: nothing here waits on
+// the tensor core); fp32 sums.  The tiles of a group are joined by the kernel that
 // joins the other forms' pieces.
 //
 // Bound by latency: 1000 keys x 8 drafts of 8 KV heads (4 MB) take 11.1 us,
@@ -212,21 +213,27 @@ tree_attn_small_kernel(const __grid_constant__ TreeAttnArgs A, const __grid_cons
   __syncthreads();
 #pragma unroll
   for (int ks = 0; ks < KW / 16; ++ks) {
-    uint32_t hi[4], lw[4];
+    uint32_t hi[4], lw[4], ll[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float p0v = s[2 * ks + (i >> 1)][2 * (i & 1)], p1v = s[2 * ks + (i >> 1)][2 * (i & 1) + 1];
       hi[i] = pack_bf16x2(p0v, p1v);
-      lw[i] = pack_bf16x2(p0v - bf16_lo(hi[i]), p1v - bf16_hi(hi[i]));
+      const float r0 = p0v - bf16_lo(hi[i]), r1 = p1v - bf16_hi(hi[i]);
+      lw[i] = pack_bf16x2(r0, r1);
+      ll[i] = pack_bf16x2(r0 - bf16_lo(lw[i]), r1 - bf16_hi(lw[i]));
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       uint32_t bb[4];
       ldsm_t(va + swz(KW * kg + 16 * ks + (lane & 15), 2 * i + (lane >> 4)), bb);
       mma16(o[2 * i], hi, bb[0], bb[1]);
-      mma16(o[2 * i], lw, bb[0], bb[1]);
       mma16(o[2 * i + 1], hi, bb[2], bb[3]);
+      mma16(o[2 * i], lw, bb[0], bb[1]);
       mma16(o[2 * i + 1], lw, bb[2], bb[3]);
+      if (!A.o_bf16) {
+        mma16(o[2 * i], ll, bb[0], bb[1]);
+        mma16(o[2 * i + 1], ll, bb[2], bb[3]);
+      }
     }
   }
   __syncthreads();  // (O goes over K and V)
