@@ -19,6 +19,10 @@
 // value at the very worst), then joins an fp32 total in the workspace, which the
 // L2 cache keeps (there is no room left in TMEM or registers: 1.5% of the time).
 //
+// P as a single bf16 term would be a fifth faster (32 groups x 131072 keys x 256
+// rows 885 -> 730 us) and take a bf16 output's error from 1.7e-3 to 2.4e-3; the pair
+// stays: a verified token is to see the numbers of a decode step, which has it.
+//
 // Bound: the tensor cores (P V counts twice) above about 100 rows; 128 drafted
 // rows and a tile of 128 keys are 512 + 1024 cycles of the tensor pipe.  Measured,
 // launches back to back: 4 x 131072 keys x 8 KV heads x 256 rows 850 to 930 us (1.2
