@@ -400,3 +400,22 @@ assert torch.equal(got, o) and bool((got != 0).any()) and torch.equal(ring[0, :,
 def test_first_calls_of_a_process_are_captured(N):
     subprocess.run([sys.executable, "-c", f"N = {N}\n" + _FIRST], check=True, timeout=300,
                    cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+
+
+@pytest.mark.parametrize("form", range(len(FORMS)))
+def test_tree_attn_logits_at_the_end_of_fp32(form):
+    """All logits the same and near fp32's lowest value: the mean of the attended rows.  (The key-by-key pass adds
+    n terms of weight 1 in fp32: n u of the largest value, and a division.)"""
+    T, Hq, Hk, _ = FORMS[form]
+    N = 900 if form == 0 else 9000
+    q, k, v, kn, vn = _inputs(2, Hq, Hk, N, T, 77, lens=[N, N - 5], dead=0.0)
+    q.zero_(), k.zero_(), kn.zero_()
+    q[..., 0], k[..., 0], kn[..., 0] = 2.0 ** 60, -2.0 ** 60, -2.0 ** 60
+    anc, depth = _trees(2, T, "wide", 77)
+    o = _run_tree(q, k, v, [N, N - 5], kn, vn, anc, depth, 0, False, None, 128.0, F32)
+    for b, n in enumerate((N, N - 5)):
+        a = torch.from_numpy(anc[b]).cuda().double()
+        total = v[b, :, None, :n].double().sum(2) + torch.einsum("tj,hjd->htd", a, vn[b].double())
+        want = (total / (n + a.sum(1))[None, :, None]).repeat_interleave(Hq // Hk, 0)
+        tol = float(v[b].abs().max()) * (n + T + 8) * 2.0 ** -24
+        assert bool(((o[b].double() - want).abs() <= tol).all())
