@@ -19,7 +19,7 @@
 // about 100 MB of keys.  Measured, launches back to back: 8 x 12768 to 32768 keys
 // x 8 KV heads x 64 rows (0.79 GB) 155 to 165 us (4.8 to 5.1 TB/s); 8 x 6 rings of
 // 4096 rows x 64 rows (103 MB) 42; 8 x 2 KV heads x 64 rows that select 8% of as
-// many keys (20 MB) 30.4 to 31.8.
+// many keys (20 MB) 29.2 to 31.
 //
 // Design (B200, tcgen05).  The query rows of a KV head go on the N side of both
 // products and the KEYS (then the head dims) on the M side, so that a tile

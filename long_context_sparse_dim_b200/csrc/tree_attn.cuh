@@ -231,14 +231,11 @@ template <bool SEL>
 struct TrWalk {
   int hi, base_b, align;
   TrSeg s;
-  RTP_DEVICE void start(const TreeAttnArgs& A, int lo, int end, int b, int base, int al) {
+  RTP_DEVICE void start(const TrSeg& first, int lo, int end, int al) {
     hi = end;
     align = al;
-    base_b = base;
-    s.b = b;
-    s.span = span_of<SEL>(A, b, align);
-    s.kvh = (lo - base) / s.span.units;
-    s.base = base_b + s.kvh * s.span.units;
+    s = first;
+    base_b = s.base - s.kvh * s.span.units;
     s.u0 = lo - s.base;
     s.u1 = min(s.span.tiles, hi - s.base);
   }
@@ -277,8 +274,8 @@ struct TrFeed {
   int row_at[NR];                // each row's draft times 8 plus its head in the group
   int2 meta[kTrRing];            // per tile: its number in the group; 4 * segment + 2 * (CTA's last) + (segment's last)
   TrSegInfo seg[kTrRing];
-  int start_b, start_base, start;  // where this CTA's range begins: sequence, the sequence's place on the line, tile
-  int end;                       // and where it ends (start >= end: nothing to do)
+  TrSeg first;                   // the group in which this CTA's range begins (its tiles: later)
+  int start, end;                // where on the line the range begins and ends (start >= end: nothing to do)
   int per, align;                // length of a range; see units_of
   int cnt[2][kTrLoadWarps];
   int qkey[kQueue];              // selected keys waiting for a tile (ring)
@@ -385,8 +382,18 @@ RTP_DEVICE void tree_find_range(Smem& S, const TreeAttnArgs& A, const TrParts& W
         // in the room behind a group: from the next one on
         const bool skip = u >= span.tiles, last = kvh + 1 == A.Hk;
         S.start = skip ? base_b + (kvh + 1) * span.units : lo;
-        S.start_b = skip && last ? b + 1 : b;
-        S.start_base = skip && last ? base_b + mine : base_b;
+        TrSeg& f = S.first;
+        if (skip & last) {
+          if (b + 1 < A.B) f.span = span_of<SEL>(A, b + 1, align);
+          f.b = b + 1;
+          f.kvh = 0;
+          f.base = base_b + mine;
+        } else {
+          f.span = span;
+          f.b = b;
+          f.kvh = skip ? kvh + 1 : kvh;
+          f.base = base_b + f.kvh * span.units;
+        }
       }
       break;
     }
@@ -471,7 +478,7 @@ RTP_DEVICE void tree_load(Smem& S, const CUtensorMap& kmap, const CUtensorMap& v
   };
   TrWalk<SEL> walk;
   bool more = lo < hi, ok = true;
-  if (more) walk.start(A, lo, hi, S.start_b, S.start_base, S.align);
+  if (more) walk.start(S.first, lo, hi, S.align);
 #pragma unroll 1
   while (more && ok) {
     const TrSeg s = walk.s;
