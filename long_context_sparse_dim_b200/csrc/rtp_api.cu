@@ -643,7 +643,7 @@ rtp_status rtp_tree_attn(const rtp_tensor* q, const rtp_tensor* k, const rtp_ten
   if (ring != 0 && ring != 1) return RTP_ERR_INVALID_ARG;
   // a ring holds the last N tokens: the window must lie inside it, and selections name positions, not its rows
   if (ring && (W < 1 || W > N || sel)) return RTP_ERR_INVALID_ARG;
-  if (sel && !sel->mask) return RTP_ERR_INVALID_ARG;
+  if (sel && !sel->mask && B * T > 0 && N > 0) return RTP_ERR_INVALID_ARG;
   if (sel && sel->mask_words < (N + 31) / 32) return RTP_ERR_SHAPE;
   if (B * Hk > INT32_MAX / 8 || Hq * T > INT32_MAX / 8) return RTP_ERR_UNSUPPORTED;
   if (B * Hq * T > INT32_MAX) return RTP_ERR_UNSUPPORTED;  // (rows are numbered with 32 bits)

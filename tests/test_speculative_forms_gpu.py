@@ -419,3 +419,16 @@ def test_tree_attn_logits_at_the_end_of_fp32(form):
         want = (total / (n + a.sum(1))[None, :, None]).repeat_interleave(Hq // Hk, 0)
         tol = float(v[b].abs().max()) * (n + T + 8) * 2.0 ** -24
         assert bool(((o[b].double() - want).abs() <= tol).all())
+
+
+def test_tree_attn_selects_from_an_empty_cache():
+    q, k, v, kn, vn = _inputs(2, 4, 2, 0, 5, 3, lens=[0, 0])
+    anc, depth = _trees(2, 5, "wide", 3)
+    o = _run_tree(q, k, v, [0, 0], kn, vn, anc, depth, 0, False, None, SCALE, F32)
+    none = torch.zeros(2 * 4 * 5, 0, dtype=torch.int32, device="cuda")
+    got, one = torch.empty_like(o), torch.zeros(40, dtype=torch.int32, device="cuda")
+    rtp.tree_attn(q, k, v, torch.zeros(2, dtype=torch.int32, device="cuda"), kn, vn, _bits(anc), SCALE, got,
+                  rtp.workspace(rtp.tree_attn_workspace_size(2, 4, 5, 2, 0), "cuda"),
+                  sel=rtp.Selection(tau_bits=one, tiepos=one, count=one, mask=none))
+    torch.cuda.synchronize()
+    assert torch.equal(got, o)
